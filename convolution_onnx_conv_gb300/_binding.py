@@ -27,6 +27,7 @@ CONVF_VARIANT_AUTO, CONVF_VARIANT_IMPLICIT_GEMM, CONVF_VARIANT_GEMM_1X1, CONVF_V
 VARIANT_NAMES = {0: "auto", 1: "implicit_gemm_im2col", 2: "gemm_1x1", 3: "depthwise",
                  4: "int8_mma", 5: "implicit_gemm_gather", 6: "implicit_gemm_window", 7: "implicit_gemm_halo",
                  8: "int8_tcgen05_exact", 9: "grouped_direct", 10: "mbv2_block"}
+CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3 = 0, 1
 AUTO_PAD = {"NOTSET": 0, "SAME_UPPER": 1, "SAME_LOWER": 2, "VALID": 3}
 
 EXPORTED = ["conv_fused_output_shape", "conv_fused_resolve_pads", "conv_bn_scale_shift",
@@ -37,7 +38,10 @@ EXPORTED = ["conv_fused_output_shape", "conv_fused_resolve_pads", "conv_bn_scale
             "conv_fused_run_residual", "conv_fused_create_qlinear", "conv_fused_create_preact",
             "conv_fused_create_mbv2_block", "conv_fused_debug_fail_alloc", "conv_fused_debug_live_handles",
             "conv_fused_chain_create", "conv_fused_chain_create_ex", "conv_fused_chain_run", "conv_fused_chain_status",
-            "conv_fused_chain_clear_status", "conv_fused_chain_describe", "conv_fused_chain_destroy"]
+            "conv_fused_chain_clear_status", "conv_fused_chain_describe", "conv_fused_chain_destroy",
+            "conv_fused_quantize_blocks", "conv_fused_linear_create", "conv_fused_linear_run",
+            "conv_fused_linear_status", "conv_fused_linear_clear_status", "conv_fused_linear_describe",
+            "conv_fused_linear_destroy"]
 
 
 class ConvDesc(ctypes.Structure):
@@ -62,6 +66,28 @@ class BlockDesc(ctypes.Structure):
 class ChainStep(ctypes.Structure):
     """convf_chain_step: one conv run of a chain (handle, x, residual or NULL, y)."""
     _fields_ = [("conv", ctypes.c_void_p), ("x", ctypes.c_void_p), ("r", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class QuantArgs(ctypes.Structure):
+    """convf_quant_args: what conv_fused_quantize_blocks reads and writes."""
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int),
+                ("x_rows", ctypes.c_int), ("ldx", ctypes.c_longlong), ("index", ctypes.c_void_p),
+                ("gated", ctypes.c_int), ("block_rows", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("ldq", ctypes.c_longlong), ("scale", ctypes.c_void_p), ("lds", ctypes.c_longlong)]
+
+
+class LinearDesc(ctypes.Structure):
+    """convf_linear_desc: a linear layer, or one per expert."""
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("experts", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("ldw", ctypes.c_longlong), ("expert_stride", ctypes.c_longlong), ("act", ctypes.c_int),
+                ("clip_lo", ctypes.c_float), ("clip_hi", ctypes.c_float), ("out_dtype", ctypes.c_int)]
+
+
+class LinearArgs(ctypes.Structure):
+    """convf_linear_args: one run's rows."""
+    _fields_ = [("rows", ctypes.c_int), ("x", ctypes.c_void_p), ("ldx", ctypes.c_longlong),
+                ("x_scale", ctypes.c_void_p), ("xs_row", ctypes.c_longlong), ("xs_blk", ctypes.c_longlong),
+                ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_longlong)]
 
 
 class QParams(ctypes.Structure):
@@ -164,8 +190,17 @@ def load_library(build_if_missing: bool = False):
     lib.conv_fused_chain_describe.argtypes = [vp, ctypes.c_char_p, ctypes.c_size_t]
     lib.conv_fused_chain_destroy.argtypes = [vp]
     lib.conv_fused_chain_destroy.restype = None
+    lib.conv_fused_quantize_blocks.argtypes = [P(QuantArgs), vp]
+    lib.conv_fused_linear_create.argtypes = [P(LinearDesc), vp, vp, vp, P(vp)]
+    lib.conv_fused_linear_run.argtypes = [vp, P(LinearArgs), vp]
+    lib.conv_fused_linear_status.argtypes = [vp]
+    lib.conv_fused_linear_clear_status.argtypes = [vp]
+    lib.conv_fused_linear_describe.argtypes = [vp, ctypes.c_int, ctypes.c_char_p, ctypes.c_size_t]
+    lib.conv_fused_linear_destroy.argtypes = [vp]
+    lib.conv_fused_linear_destroy.restype = None
     for name in EXPORTED:
-        if name not in ("conv_fused_destroy", "conv_fused_last_error", "conv_fused_chain_destroy"):
+        if name not in ("conv_fused_destroy", "conv_fused_last_error", "conv_fused_chain_destroy",
+                        "conv_fused_linear_destroy"):
             getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
     return lib
@@ -376,6 +411,42 @@ def conv_fused_chain_describe(chain: int) -> str:
 
 def conv_fused_chain_destroy(chain: int):
     load_library().conv_fused_chain_destroy(chain)
+
+
+def conv_fused_quantize_blocks(args: QuantArgs, stream=None):
+    s = stream.cuda_stream if stream is not None and hasattr(stream, "cuda_stream") else stream
+    _check(load_library().conv_fused_quantize_blocks(ctypes.byref(args), s))
+
+
+def conv_fused_linear_create(desc: LinearDesc, W, w_scale=None, bias=None) -> int:
+    """Device pointers (ints) or CUDA tensors, which must outlive the layer; returns its handle."""
+    out = ctypes.c_void_p()
+    _check(load_library().conv_fused_linear_create(ctypes.byref(desc), _addr(W), _addr(w_scale), _addr(bias),
+                                                   ctypes.byref(out)))
+    return out.value
+
+
+def conv_fused_linear_run(layer: int, args: LinearArgs, stream=None):
+    s = stream.cuda_stream if stream is not None and hasattr(stream, "cuda_stream") else stream
+    _check(load_library().conv_fused_linear_run(layer, ctypes.byref(args), s))
+
+
+def conv_fused_linear_status(layer: int) -> int:
+    return load_library().conv_fused_linear_status(layer)
+
+
+def conv_fused_linear_clear_status(layer: int):
+    _check(load_library().conv_fused_linear_clear_status(layer))
+
+
+def conv_fused_linear_describe(layer: int, rows: int) -> str:
+    buf = ctypes.create_string_buffer(512)
+    _check(load_library().conv_fused_linear_describe(layer, int(rows), buf, 512))
+    return buf.value.decode()
+
+
+def conv_fused_linear_destroy(layer: int):
+    load_library().conv_fused_linear_destroy(layer)
 
 
 # --------------------------------------------------------------------------- torch convenience
@@ -589,3 +660,171 @@ class ConvChain:
             self.close()
         except Exception:
             pass
+
+
+def _stream_of(t, stream):
+    """cudaStream_t of `stream` (a torch stream or an int), else the current stream of t's device."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _rows_2d(t, name):
+    """(rows, cols, row stride) of a CUDA tensor [rows][cols] whose columns are adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be adjacent (stride 1)")
+    return r, c, (t.stride(0) if r > 1 else max(c, t.stride(0)))
+
+
+def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None, stream=None):
+    """(q, scale): the rows of ``x`` (CUDA, bf16 or fp32, [rows][cols], any row stride) as e4m3 values
+    and a float scale per row and 128 columns (``block_rows=1``), or per 128 x 128 block
+    (``block_rows=128``, as a layer's weights have them); x is about q * scale.
+
+    ``index`` (int32, CUDA) takes the rows x[index] instead (an entry outside x gives a row of zeros);
+    ``gated=True`` takes x as [rows][2*cols] and quantises g / (1 + exp(-g)) * u of its halves g and
+    u.  Rows of q lie a multiple of 16 bytes apart, as the layers read them; ``q`` and ``scale`` may
+    be given.  Runs on the current torch stream."""
+    import torch
+    xr, wide, ldx = _rows_2d(x, "x")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bf16 or fp32")
+    if gated and wide % 2:
+        raise ValueError("gated rows have an even number of columns")
+    if index is not None and (not index.is_cuda or index.dtype != torch.int32 or index.dim() != 1
+                              or not index.is_contiguous()):
+        raise ValueError("index must be a contiguous int32 CUDA vector")
+    cols = wide // 2 if gated else wide
+    rows = xr if index is None else index.shape[0]
+    nblk, srows = -(-cols // 128), -(-rows // block_rows) if block_rows > 0 else rows
+    if q is None:
+        q = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=x.device)
+        if q.shape[1] != cols:
+            q = q[:, :cols]
+    if scale is None:
+        scale = torch.empty((srows, nblk), dtype=torch.float32, device=x.device)
+    qr, qc, ldq = _rows_2d(q, "q")
+    sr, sc, lds = _rows_2d(scale, "scale")
+    if q.dtype != torch.float8_e4m3fn or (qr, qc) != (rows, cols):
+        raise ValueError(f"q must be float8_e4m3fn of shape ({rows}, {cols})")
+    if scale.dtype != torch.float32 or (sr, sc) != (srows, nblk):
+        raise ValueError(f"scale must be float32 of shape ({srows}, {nblk})")
+    a = QuantArgs(rows, cols, x.data_ptr(), CONVF_OUT_BF16 if x.dtype == torch.bfloat16 else CONVF_OUT_F32, xr, ldx,
+                  None if index is None else index.data_ptr(), int(bool(gated)), int(block_rows), q.data_ptr(), ldq,
+                  scale.data_ptr(), lds)
+    conv_fused_quantize_blocks(a, _stream_of(x, stream))
+    return q, scale
+
+
+class ExpertLinear:
+    """Linear layers, one per expert, over rows sorted by expert: rows offsets[e] up to offsets[e+1]
+    of x times ``w[e]``.
+
+    ``w``: CUDA [experts][N][K], bf16 or float8_e4m3fn, read in place (rows and experts a multiple
+    of 16 bytes apart); ``w_scale`` (e4m3) fp32 [experts][ceil(N/128)][ceil(K/128)]; ``bias`` fp32
+    [experts][N] or None; ``act`` and ``clip`` as for a conv; y is fp32, or bf16 with ``out_bf16``.
+    Calling it runs on the current torch stream."""
+
+    def __init__(self, w, w_scale=None, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
+        import torch
+        if not w.is_cuda or w.dim() != 3:
+            raise ValueError("w must be a CUDA tensor [experts][N][K]")
+        if w.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("w must be bf16 or float8_e4m3fn")
+        E, N, K = w.shape
+        if K > 1 and w.stride(2) != 1:
+            raise ValueError("w's columns must be adjacent (stride 1)")
+        self.e4m3 = w.dtype == torch.float8_e4m3fn
+        if self.e4m3 != (w_scale is not None):
+            raise ValueError("w_scale goes with float8_e4m3fn weights, and with those only")
+        blocks = (E, -(-N // 128), -(-K // 128))
+        for name, t, shape in (("w_scale", w_scale, blocks), ("bias", bias, (E, N))):
+            if t is not None and (not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape):
+                raise ValueError(f"{name} must be a CUDA fp32 tensor of shape {shape}")
+        w_scale = None if w_scale is None else w_scale.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        self._keep = (w, w_scale, bias)   # the layer reads them in place
+        self.experts, self.N, self.K = E, N, K
+        self.out_dtype = torch.bfloat16 if out_bf16 else torch.float32
+        d = LinearDesc(N, K, E, CONVF_LINEAR_E4M3 if self.e4m3 else CONVF_LINEAR_BF16,
+                       w.stride(1) if N > 1 else max(w.stride(1), -(-K // 16) * 16), w.stride(0), act, float(clip[0]), float(clip[1]),
+                       CONVF_OUT_BF16 if out_bf16 else CONVF_OUT_F32)
+        self.handle = conv_fused_linear_create(d, w, w_scale, bias)
+
+    def _run(self, x, offsets, x_scale, y, stream):
+        import torch
+        rows, K, ldx = _rows_2d(x, "x")
+        if K != self.K:
+            raise ValueError(f"x must have {self.K} columns")
+        if x.dtype != self._keep[0].dtype:
+            raise ValueError(f"x must be {self._keep[0].dtype}")
+        if rows <= 1:   # one row has no stride of its own
+            ldx = -(-ldx // 16) * 16
+        if self.e4m3:
+            if x_scale is None or not x_scale.is_cuda or x_scale.dtype != torch.float32 \
+                    or tuple(x_scale.shape) != (rows, -(-K // 128)):
+                raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows, -(-K // 128))}")
+        elif x_scale is not None:
+            raise ValueError("x_scale goes with float8_e4m3fn layers only")
+        if y is None:
+            y = torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device)
+        yr, yc, ldy = _rows_2d(y, "y")
+        if y.dtype != self.out_dtype or (yr, yc) != (rows, self.N):
+            raise ValueError(f"y must be {self.out_dtype} of shape ({rows}, {self.N})")
+        a = LinearArgs(rows, x.data_ptr(), ldx, None, 0, 0, None if offsets is None else offsets.data_ptr(),
+                       y.data_ptr(), ldy)
+        if x_scale is not None:
+            a.x_scale, a.xs_row, a.xs_blk = x_scale.data_ptr(), x_scale.stride(0), x_scale.stride(1)
+        conv_fused_linear_run(self.handle, a, _stream_of(x, stream))
+        return y
+
+    def __call__(self, x, offsets, x_scale=None, y=None, stream=None):
+        """y [rows][N] for ``x`` [rows][K] (w's type; rows a multiple of 16 bytes apart), ``offsets``
+        int32 CUDA [experts+1] and, for e4m3, ``x_scale`` fp32 [rows][ceil(K/128)] (any strides).
+        Rows that no expert takes are not written."""
+        import torch
+        if not offsets.is_cuda or offsets.dtype != torch.int32 or tuple(offsets.shape) != (self.experts + 1,) \
+                or not offsets.is_contiguous():
+            raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {self.experts + 1}")
+        return self._run(x, offsets, x_scale, y, stream)
+
+    def describe(self, rows: int) -> str:
+        return conv_fused_linear_describe(self.handle, rows)
+
+    def status(self) -> int:
+        return conv_fused_linear_status(self.handle)
+
+    def clear_status(self):
+        conv_fused_linear_clear_status(self.handle)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            conv_fused_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class BlockLinear(ExpertLinear):
+    """One linear layer on block-scaled e4m3 operands: ``w`` float8_e4m3fn [N][K] with ``w_scale``
+    [ceil(N/128)][ceil(K/128)] (or bf16 without scales), ``bias`` fp32 [N] or None; the rest as
+    ExpertLinear.  Calling it with x and x_scale, as quantize_blocks gives them, returns y."""
+
+    def __init__(self, w, w_scale=None, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
+        if w.dim() != 2:
+            raise ValueError("w must be a CUDA tensor [N][K]")
+        super().__init__(w[None], None if w_scale is None else w_scale[None], None if bias is None else bias[None], act,
+                         clip, out_bf16)
+
+    def __call__(self, x, x_scale=None, y=None, stream=None):
+        return self._run(x, None, x_scale, y, stream)

@@ -1,0 +1,274 @@
+// Host side of the block-scaled operators (conv_fused_quantize_blocks, conv_fused_linear_*):
+// validates every argument (refuse, never guess) and launches on the caller's stream.  Weights
+// and scales are read where they are; nothing of a run is kept for the next.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <new>
+
+#include "../../include/conv_fused.h"
+#include "api_internal.h"
+#include "convf_internal.h"
+#include "linear_internal.h"
+
+using namespace convf;
+
+namespace {
+
+constexpr uint32_t kLinearMagic = 0x11EA4001u;
+constexpr uint32_t kLinearDead = 0xDEAD11EAu;
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// bytes that rows of `row` bytes, `stride` bytes apart, span from their first
+unsigned long long span(long long rows, long long stride, long long row) {
+  return rows > 0 ? static_cast<unsigned long long>(rows - 1) * stride + row : 0;
+}
+bool overlap(const void* a, unsigned long long an, const void* b, unsigned long long bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an && bn && x < y + bn && y < x + an;
+}
+
+// SMs of the current device (looked up once per device), or an error
+convf_status current_device(int* dev, int* num_sms) {
+  static int sms[kMaxDevices];   // 0 = not looked up; every writer stores the same value
+  if (cudaGetDevice(dev) != cudaSuccess) return record_error(CONVF_ERR_CUDA, "no current CUDA device");
+  const bool known = *dev >= 0 && *dev < kMaxDevices;
+  *num_sms = known ? sms[*dev] : 0;
+  if (*num_sms == 0) {
+    if (cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess || *num_sms < 1)
+      return record_error(CONVF_ERR_CUDA, "the SM count of device %d could not be read", *dev);
+    if (known) sms[*dev] = *num_sms;
+  }
+  return CONVF_OK;
+}
+
+}  // namespace
+
+struct convf_linear {
+  uint32_t magic;
+  int device, num_sms;
+  convf_linear_desc d;
+  const void* w;
+  const float* w_scale;
+  const float* bias;
+  float lo, hi;
+  int* status;   // device
+};
+
+namespace {
+
+convf_status check_linear(const convf_linear* l) {
+  if (!l) return record_error(CONVF_ERR_INVALID_ARG, "layer is NULL");
+  if (l->magic == kLinearDead) return record_error(CONVF_ERR_INVALID_ARG, "layer was destroyed");
+  if (l->magic != kLinearMagic) return record_error(CONVF_ERR_INVALID_ARG, "not a convf linear layer");
+  return CONVF_OK;
+}
+
+convf_status check_linear_desc(const convf_linear_desc* d) {
+  if (!d) return record_error(CONVF_ERR_INVALID_ARG, "desc is NULL");
+  if (d->N < 1 || d->K < 1) return record_error(CONVF_ERR_INVALID_ARG, "N=%d and K=%d must be >= 1", d->N, d->K);
+  if (d->experts < 1) return record_error(CONVF_ERR_INVALID_ARG, "experts=%d must be >= 1", d->experts);
+  if (d->experts > kMaxExperts)
+    return record_error(CONVF_ERR_UNSUPPORTED, "experts=%d: at most %d are served", d->experts, kMaxExperts);
+  if (d->dtype != CONVF_LINEAR_BF16 && d->dtype != CONVF_LINEAR_E4M3)
+    return record_error(CONVF_ERR_INVALID_ARG, "dtype=%d is not CONVF_LINEAR_BF16 or CONVF_LINEAR_E4M3", d->dtype);
+  const long long esz = d->dtype == CONVF_LINEAR_E4M3 ? 1 : 2;
+  if (d->ldw < d->K) return record_error(CONVF_ERR_INVALID_ARG, "ldw=%lld is less than K=%d", d->ldw, d->K);
+  if (d->ldw * esz % 16)
+    return record_error(CONVF_ERR_UNSUPPORTED, "ldw=%lld: weight rows must be a multiple of 16 bytes apart", d->ldw);
+  if (d->experts > 1) {
+    if (d->expert_stride < (d->N - 1LL) * d->ldw + d->K)
+      return record_error(CONVF_ERR_INVALID_ARG, "expert_stride=%lld: the experts' weights overlap", d->expert_stride);
+    if (d->expert_stride * esz % 16)
+      return record_error(CONVF_ERR_UNSUPPORTED, "expert_stride=%lld: experts must be a multiple of 16 bytes apart",
+                          d->expert_stride);
+  }
+  if (d->act < CONVF_ACT_NONE || d->act > CONVF_ACT_CLIP)
+    return record_error(CONVF_ERR_INVALID_ARG, "act=%d is not a convf_act", d->act);
+  if (d->act == CONVF_ACT_CLIP && !(d->clip_lo <= d->clip_hi))
+    return record_error(CONVF_ERR_INVALID_ARG, "clip bounds (%g, %g) need lo <= hi", d->clip_lo, d->clip_hi);
+  if (d->out_dtype != CONVF_OUT_F32 && d->out_dtype != CONVF_OUT_BF16)
+    return record_error(CONVF_ERR_INVALID_ARG, "out_dtype=%d is not CONVF_OUT_F32 or CONVF_OUT_BF16", d->out_dtype);
+  return CONVF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream) {
+  if (!a) return record_error(CONVF_ERR_INVALID_ARG, "args is NULL");
+  if (a->rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", a->rows);
+  if (a->cols < 1) return record_error(CONVF_ERR_INVALID_ARG, "cols=%d must be >= 1", a->cols);
+  if (a->x_rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "x_rows=%d must be >= 0", a->x_rows);
+  if (a->x_dtype != CONVF_OUT_F32 && a->x_dtype != CONVF_OUT_BF16)
+    return record_error(CONVF_ERR_INVALID_ARG, "x_dtype=%d is not CONVF_OUT_F32 or CONVF_OUT_BF16", a->x_dtype);
+  if (a->gated != 0 && a->gated != 1) return record_error(CONVF_ERR_INVALID_ARG, "gated=%d is not 0 or 1", a->gated);
+  if (a->block_rows != 1 && a->block_rows != kScaleBlock)
+    return record_error(CONVF_ERR_INVALID_ARG, "block_rows=%d is not 1 or %d", a->block_rows, kScaleBlock);
+  if (a->block_rows != 1 && (a->index || a->gated))
+    return record_error(CONVF_ERR_UNSUPPORTED, "an index or gated values are quantised with block_rows = 1 only");
+  if (!a->index && a->x_rows != a->rows)
+    return record_error(CONVF_ERR_INVALID_ARG, "x_rows=%d must be rows=%d without an index", a->x_rows, a->rows);
+  const long long wide = static_cast<long long>(a->cols) * (a->gated ? 2 : 1);
+  const int nblk = (a->cols - 1) / kScaleBlock + 1;
+  if (a->ldx < wide) return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld is less than the row's %lld", a->ldx, wide);
+  if (a->ldq < a->cols) return record_error(CONVF_ERR_INVALID_ARG, "ldq=%lld is less than cols=%d", a->ldq, a->cols);
+  if (a->lds < nblk) return record_error(CONVF_ERR_INVALID_ARG, "lds=%lld is less than the row's %d scales", a->lds, nblk);
+  if (a->rows == 0) return record_ok();
+  if (!a->q || !a->scale || (!a->x && a->x_rows > 0)) return record_error(CONVF_ERR_INVALID_ARG, "x, q or scale is NULL");
+  const int esz = a->x_dtype == CONVF_OUT_BF16 ? 2 : 4;
+  if (!aligned(a->x, esz) || !aligned(a->scale, 4) || !aligned(a->index, 4))
+    return record_error(CONVF_ERR_INVALID_ARG, "x, index and scale must be aligned to their elements");
+  const unsigned long long xb = span(a->x_rows, a->ldx * esz, wide * esz), qb = span(a->rows, a->ldq, a->cols);
+  const unsigned long long sb =
+      span((a->rows - 1LL) / a->block_rows + 1, a->lds * 4, static_cast<long long>(nblk) * 4);
+  if (overlap(a->x, xb, a->q, qb) || overlap(a->x, xb, a->scale, sb) || overlap(a->q, qb, a->scale, sb))
+    return record_error(CONVF_ERR_INVALID_ARG, "x, q and scale overlap");
+  int dev = -1, sms = 0;
+  convf_status st = current_device(&dev, &sms);
+  if (st != CONVF_OK) return st;
+  QuantParams p{};
+  p.x = a->x; p.ldx = a->ldx; p.x_rows = a->x_rows; p.index = a->index;
+  p.rows = a->rows; p.cols = a->cols; p.nblk = nblk;
+  p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
+  const bool row16 = a->ldx * esz % 16 == 0;
+  p.vec_x = row16 && aligned(a->x, 16);
+  p.vec_u = p.vec_x && static_cast<long long>(a->cols) * esz % 16 == 0;
+  p.vec_q = a->ldq % 8 == 0 && aligned(a->q, 8);
+  const cudaError_t e = launch_quantize_blocks(p, esz == 2, a->gated != 0, a->block_rows, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "quantising launch failed: %s", cudaGetErrorString(e));
+  return record_ok();
+}
+
+convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void* W, const float* w_scale,
+                                      const float* bias, convf_linear** out) {
+  if (!out) return record_error(CONVF_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  convf_status st = check_linear_desc(desc);
+  if (st != CONVF_OK) return st;
+  if (!W) return record_error(CONVF_ERR_INVALID_ARG, "W is NULL");
+  if (!aligned(W, 16)) return record_error(CONVF_ERR_INVALID_ARG, "W must be 16-byte aligned");
+  if ((desc->dtype == CONVF_LINEAR_E4M3) != (w_scale != nullptr))
+    return record_error(CONVF_ERR_INVALID_ARG, "w_scale goes with e4m3 weights, and with those only");
+  if (!aligned(w_scale, 4) || !aligned(bias, 4))
+    return record_error(CONVF_ERR_INVALID_ARG, "w_scale and bias must be aligned to their elements");
+  const bool host_injected = take_injected_alloc_failure();
+  convf_linear* l = host_injected ? nullptr : new (std::nothrow) convf_linear();
+  if (!l) return record_error(CONVF_ERR_OOM, "allocation of the layer failed%s", host_injected ? " (injected)" : "");
+  l->magic = kLinearMagic;
+  l->d = *desc;
+  l->w = W;
+  l->w_scale = w_scale;
+  l->bias = bias;
+  switch (desc->act) {
+    case CONVF_ACT_RELU: l->lo = 0.f; l->hi = INFINITY; break;
+    case CONVF_ACT_RELU6: l->lo = 0.f; l->hi = 6.f; break;
+    case CONVF_ACT_CLIP: l->lo = desc->clip_lo; l->hi = desc->clip_hi; break;
+    default: l->lo = -INFINITY; l->hi = INFINITY; break;
+  }
+  st = current_device(&l->device, &l->num_sms);
+  if (st != CONVF_OK) {
+    delete l;
+    return st;
+  }
+  const bool dev_injected = take_injected_alloc_failure();
+  cudaError_t e = dev_injected ? cudaErrorMemoryAllocation : cudaMalloc(&l->status, 256);
+  if (e != cudaSuccess) {
+    delete l;
+    return record_error(CONVF_ERR_OOM, "device allocation of 256 bytes failed%s", dev_injected ? " (injected)" : "");
+  }
+  e = cudaMemset(l->status, 0, 256);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    cudaFree(l->status);
+    delete l;
+    return record_error(CONVF_ERR_CUDA, "clearing the layer's status failed: %s", cudaGetErrorString(e));
+  }
+  *out = l;
+  return record_ok();
+}
+
+convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, void* stream) {
+  convf_status st = check_linear(l);
+  if (st != CONVF_OK) return st;
+  if (!a) return record_error(CONVF_ERR_INVALID_ARG, "args is NULL");
+  const convf_linear_desc& d = l->d;
+  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
+  const long long esz = e4m3 ? 1 : 2, osz = d.out_dtype == CONVF_OUT_BF16 ? 2 : 4;
+  if (a->rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", a->rows);
+  if (a->ldx < d.K) return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld is less than K=%d", a->ldx, d.K);
+  if (a->ldx * esz % 16)
+    return record_error(CONVF_ERR_UNSUPPORTED, "ldx=%lld: rows of x must be a multiple of 16 bytes apart", a->ldx);
+  if (a->ldy < d.N) return record_error(CONVF_ERR_INVALID_ARG, "ldy=%lld is less than N=%d", a->ldy, d.N);
+  if (e4m3 && (a->xs_row < 0 || a->xs_blk < 0))
+    return record_error(CONVF_ERR_INVALID_ARG, "x_scale strides (%lld, %lld) must be >= 0", a->xs_row, a->xs_blk);
+  if (!a->offsets && d.experts > 1) return record_error(CONVF_ERR_INVALID_ARG, "%d experts need row offsets", d.experts);
+  if (a->rows == 0) return record_ok();
+  if (!a->x || !a->y) return record_error(CONVF_ERR_INVALID_ARG, "x or y is NULL");
+  if (e4m3 != (a->x_scale != nullptr))
+    return record_error(CONVF_ERR_INVALID_ARG, "x_scale goes with e4m3 layers, and with those only");
+  if (!aligned(a->x, 16)) return record_error(CONVF_ERR_INVALID_ARG, "x must be 16-byte aligned");
+  if (!aligned(a->y, osz) || !aligned(a->x_scale, 4) || !aligned(a->offsets, 4))
+    return record_error(CONVF_ERR_INVALID_ARG, "y, x_scale and offsets must be aligned to their elements");
+  if (overlap(a->x, span(a->rows, a->ldx * esz, d.K * esz), a->y, span(a->rows, a->ldy * osz, d.N * osz)))
+    return record_error(CONVF_ERR_INVALID_ARG, "x and y overlap");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
+    return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
+  LinearParams p{};
+  p.rows = a->rows; p.N = d.N; p.K = d.K; p.experts = d.experts;
+  p.x = a->x; p.ldx = a->ldx; p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk;
+  p.w = l->w; p.ldw = d.ldw; p.expert_stride = d.expert_stride; p.w_scale = l->w_scale; p.bias = l->bias;
+  p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
+  p.lo = l->lo; p.hi = l->hi; p.status = l->status;
+  const cudaError_t e = launch_linear_simple(p, e4m3, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "linear launch failed: %s", cudaGetErrorString(e));
+  return record_ok();
+}
+
+convf_status conv_fused_linear_status(convf_linear* l) {
+  convf_status st = check_linear(l);
+  if (st != CONVF_OK) return st;
+  int v = 0;
+  if (cudaMemcpy(&v, l->status, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess)
+    return record_error(CONVF_ERR_CUDA, "reading the layer's status failed");
+  if (v & kStatusTimeout)
+    return record_error(CONVF_ERR_TIMEOUT, "a bounded device wait ran out in an earlier run of the layer");
+  if (v & kStatusBounds)
+    return record_error(CONVF_ERR_BOUNDS, "a linear kernel computed an out-of-range index (bounds-checking build)");
+  if (v & kStatusOffsets)
+    return record_error(CONVF_ERR_INVALID_ARG, "an earlier run's offsets decreased or passed its rows");
+  return record_ok();
+}
+
+convf_status conv_fused_linear_clear_status(convf_linear* l) {
+  convf_status st = check_linear(l);
+  if (st != CONVF_OK) return st;
+  if (cudaMemset(l->status, 0, sizeof(int)) != cudaSuccess)
+    return record_error(CONVF_ERR_CUDA, "clearing the layer's status failed");
+  return record_ok();
+}
+
+convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* buf, size_t len) {
+  convf_status st = check_linear(l);
+  if (st != CONVF_OK) return st;
+  if (!buf || len == 0) return record_error(CONVF_ERR_INVALID_ARG, "buf is NULL or len is 0");
+  if (rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
+  snprintf(buf, len, "N=%d K=%d experts=%d %s rows=%d out=%s", l->d.N, l->d.K, l->d.experts,
+           l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : "bf16", rows, l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
+  return record_ok();
+}
+
+void conv_fused_linear_destroy(convf_linear* l) {
+  if (!l || l->magic != kLinearMagic) return;
+  cudaFree(l->status);
+  l->magic = kLinearDead;
+  delete l;
+}
+
+}  // extern "C"

@@ -438,6 +438,106 @@ convf_status conv_fused_chain_describe(const convf_chain* c, char* buf, size_t l
 /* Frees the chain's device memory (the caller must have synchronised); NULL is ignored. */
 void conv_fused_chain_destroy(convf_chain* c);
 
+/* ---------------------------------------------------------------------------------------------
+ * Block-scaled 8-bit floating point: quantising, products, and products of row groups with an
+ * expert's weights each.
+ *
+ * Numbers.  A matrix of e4m3 values (sign, 4 exponent bits of bias 7, 3 fraction bits; largest
+ * finite value 448; ONNX's FLOAT8E4M3FN) stands for q * scale, with one float scale per block:
+ * activations [rows][K] have one per row and 128 consecutive columns (scale[r][b], b = k / 128),
+ * weights [N][K] one per 128 x 128 block (scale[n / 128][k / 128]).  Blocks at a ragged edge are
+ * short; no multiple of 128 is asked for.
+ *
+ * These calls take device pointers throughout: a layer's weights stay where they are and are
+ * read in place (no prepack), and the row count is an argument of the run. */
+
+/* Operand type of a linear layer. */
+typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1 } convf_linear_dtype;
+
+/* What conv_fused_quantize_blocks reads and writes.  With v the values to quantise, [rows][cols]
+ * in float32:
+ *   v[r][c] = x[s(r)][c]                              (gated = 0)
+ *   v[r][c] = g / (1 + exp(-g)) * u, g = x[s(r)][c], u = x[s(r)][cols + c]   (gated = 1)
+ * with s(r) = index[r], or r without an index,
+ *   scale[i][b] = max |v| over the block / 448        (float32, round to nearest)
+ *   q[r][c] = e4m3(clamp(v[r][c] / scale, -448, 448)) (float32 quotient, then nearest, ties to even)
+ * and q = 0 where the scale is 0 (a block of zeros, or of values so small that it underflows).
+ * A NaN in a block makes its scale and its values NaN; an infinity makes the scale infinite, so
+ * that every value of the block reads back as NaN. */
+typedef struct {
+  int rows, cols;          /* of q; rows may be 0                                              */
+  const void* x;           /* device [x_rows][cols], or [x_rows][2*cols] when gated            */
+  int x_dtype;             /* convf_out_dtype of x: CONVF_OUT_F32 or CONVF_OUT_BF16            */
+  int x_rows;              /* rows of x (== rows without an index)                             */
+  long long ldx;           /* elements between rows of x                                       */
+  const int32_t* index;    /* device [rows] or NULL; an entry outside [0, x_rows) makes its row
+                              zeros with scales 0 (a padding row)                              */
+  int gated;               /* 1: the gated form above                                          */
+  int block_rows;          /* 1: scales per row, scale [rows][ceil(cols/128)];
+                              128: per 128 x 128 block, scale [ceil(rows/128)][ceil(cols/128)]
+                              (neither index nor gated then)                                   */
+  void* q;                 /* device [rows][cols] e4m3 bytes; columns past cols are not written */
+  long long ldq;           /* bytes between rows of q                                          */
+  float* scale;            /* device                                                           */
+  long long lds;           /* elements between rows of scale                                   */
+} convf_quant_args;
+
+/* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row
+ * stride of at least a row is served; rows that begin on 16 bytes are read and written as vectors.
+ * q and scale must not overlap x. */
+convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
+
+/* A linear layer, or one per expert: y[m][n] = act(sum_k x[m][k] W[e(m)][n][k] + bias[e(m)][n]),
+ * with the act of a conv.  Sums are held in float32 (e4m3: each block's sum of products, then
+ * times its two scales into a float32 sum over the blocks); y is rounded once. */
+typedef struct {
+  int N, K;                /* W[e]: [N][K]                                                     */
+  int experts;             /* >= 1, at most 1024                                               */
+  int dtype;               /* convf_linear_dtype of x and W                                    */
+  long long ldw;           /* elements between rows of W; ldw * element size % 16 == 0         */
+  long long expert_stride; /* elements between experts' W (same rule; ignored for one expert)  */
+  int act;                 /* convf_act                                                        */
+  float clip_lo, clip_hi;  /* bounds for CONVF_ACT_CLIP                                        */
+  int out_dtype;           /* convf_out_dtype of y                                             */
+} convf_linear_desc;
+typedef struct convf_linear convf_linear;
+
+/* Validates, and keeps the pointers: W (device, 16-byte aligned), w_scale (device
+ * [experts][ceil(N/128)][ceil(K/128)], NULL for bf16) and bias (device float [experts][N] or NULL)
+ * are read by every run and must outlive the layer.  One small device allocation (status). */
+convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void* W, const float* w_scale,
+                                      const float* bias, convf_linear** out);
+
+typedef struct {
+  int rows;                /* rows of x and y; 0 is an empty run                               */
+  const void* x;           /* device [rows][K], 16-byte aligned                                */
+  long long ldx;           /* elements between rows; ldx * element size % 16 == 0              */
+  const float* x_scale;    /* device, scale of row m and block b at x_scale[m*xs_row + b*xs_blk];
+                              NULL for bf16                                                    */
+  long long xs_row, xs_blk;
+  const int32_t* offsets;  /* device [experts+1], nondecreasing: expert e takes rows offsets[e]
+                              up to offsets[e+1] (possibly none).  NULL: one expert takes all
+                              rows (experts == 1 only).  Rows outside [offsets[0],
+                              offsets[experts]) are not written.  Offsets that decrease or pass
+                              `rows` reach no memory outside x and y, leave what rows they name
+                              unspecified, and are reported by conv_fused_linear_status.       */
+  void* y;                 /* device [rows][N], element aligned; must not overlap x            */
+  long long ldy;           /* elements between rows of y                                       */
+} convf_linear_args;
+
+/* One launch on `stream`; asynchronous, allocates nothing, may be captured in a CUDA graph.  The
+ * order of every sum depends on the sizes and the row groups only: results repeat bit for bit. */
+convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, void* stream);
+/* Device status of earlier runs (read after the caller synchronised): CONVF_OK, CONVF_ERR_TIMEOUT,
+ * or CONVF_ERR_INVALID_ARG for offsets that decreased or passed the rows; sticky until
+ * conv_fused_linear_clear_status. */
+convf_status conv_fused_linear_status(convf_linear* l);
+convf_status conv_fused_linear_clear_status(convf_linear* l);
+/* One line: what a run of this many rows launches. */
+convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* buf, size_t len);
+/* Frees the layer's device memory (the caller must have synchronised); NULL is ignored. */
+void conv_fused_linear_destroy(convf_linear* l);
+
 #ifdef __cplusplus
 }
 #endif

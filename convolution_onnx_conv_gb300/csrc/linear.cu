@@ -50,6 +50,7 @@ convf_status current_device(int* dev, int* num_sms) {
 
 struct convf_linear {
   uint32_t magic;
+  CUtensorMap tmW;
   int device, num_sms;
   convf_linear_desc d;
   const void* w;
@@ -93,6 +94,70 @@ convf_status check_linear_desc(const convf_linear_desc* d) {
     return record_error(CONVF_ERR_INVALID_ARG, "clip bounds (%g, %g) need lo <= hi", d->clip_lo, d->clip_hi);
   if (d->out_dtype != CONVF_OUT_F32 && d->out_dtype != CONVF_OUT_BF16)
     return record_error(CONVF_ERR_INVALID_ARG, "out_dtype=%d is not CONVF_OUT_F32 or CONVF_OUT_BF16", d->out_dtype);
+  return CONVF_OK;
+}
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// clusters of `split` CTAs of the few-rows kernel that run at once (looked up once per process and
+// device; every writer stores the same value)
+int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
+  if (split == 1) return num_sms;
+  static int known[kMaxDevices][2][4][4];
+  int ti = 0, si = 0;
+  while ((16 << ti) < tile) ++ti;
+  while ((1 << si) < split) ++si;
+  int* at = dev >= 0 && dev < kMaxDevices ? &known[dev][e4m3][ti][si] : nullptr;
+  if (at && *at) return *at;
+  const int n = linear_few_max_clusters(e4m3, tile, split);
+  if (at) *at = n;
+  return n;
+}
+
+// What a run of `rows` rows launches.  How the rows fall on the experts is known on the device only:
+// the plan goes by their mean (any offsets are right with any plan).
+LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows) {
+  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
+  const long long taken = rows < d.experts ? rows : d.experts;   // experts that can have rows
+  const long long mean = ceil_div(rows, taken);
+  LinearPlan plan{};
+  plan.form = kLinearFew;
+  plan.tile = 16;
+  while (plan.tile < 128 && plan.tile < mean) plan.tile *= 2;
+  const int num_kb = static_cast<int>(ceil_div(static_cast<long long>(d.K) * (e4m3 ? 1 : 2), kKBlockBytes));
+  const long long nt = ceil_div(d.N, 128);
+  const long long likely = taken * ceil_div(mean, plan.tile) * nt;
+  const long long most = (d.experts > 1 ? rows / plan.tile + taken : ceil_div(rows, plan.tile)) * nt;
+  // cost in k-blocks: the waves of tiles, each its share of the reduction and a start and end worth
+  // about 4 k-blocks (8 with the exchange of partial sums)
+  long long best = -1;
+  for (int split = 1; split <= 8; split *= 2) {
+    if (split > num_kb) break;
+    const int at_once = few_clusters(dev, num_sms, e4m3, plan.tile, split);
+    if (at_once < 1) continue;
+    const long long cost = ceil_div(likely, at_once) * (ceil_div(num_kb, split) + (split > 1 ? 8 : 4));
+    if (best < 0 || cost < best) {
+      best = cost;
+      plan.split = split;
+      plan.grid = split * static_cast<int>(most < at_once ? most : at_once);
+    }
+  }
+  return plan;
+}
+
+convf_status encode_map(CUtensorMap* m, bool e4m3, int dims, const void* p, const cuuint64_t* size,
+                        const cuuint64_t* strides, int box_rows, const char* what) {
+  EncodeTiledFn tiled;
+  EncodeIm2colFn im2col;
+  if (!tensor_map_encoders(&tiled, &im2col)) return record_error(CONVF_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(e4m3 ? kKBlockBytes : kKBlockBytes / 2),
+                             static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = tiled(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims,
+                           const_cast<void*>(p), size, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return record_error(CONVF_ERR_CUDA, "encoding the tensor map of %s failed (%d)", what, (int)r);
   return CONVF_OK;
 }
 
@@ -176,6 +241,19 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
     delete l;
     return st;
   }
+  {
+    const bool e4m3 = desc->dtype == CONVF_LINEAR_E4M3;
+    const cuuint64_t esz = e4m3 ? 1 : 2;
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(desc->K), static_cast<cuuint64_t>(desc->N),
+                                static_cast<cuuint64_t>(desc->experts)};
+    const cuuint64_t strides[2] = {desc->ldw * esz,
+                                   (desc->experts > 1 ? desc->expert_stride : desc->N * desc->ldw) * esz};
+    st = encode_map(&l->tmW, e4m3, 3, W, size, strides, 128, "W");
+    if (st != CONVF_OK) {
+      delete l;
+      return st;
+    }
+  }
   const bool dev_injected = take_injected_alloc_failure();
   cudaError_t e = dev_injected ? cudaErrorMemoryAllocation : cudaMalloc(&l->status, 256);
   if (e != cudaSuccess) {
@@ -220,13 +298,20 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
     return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
+  const LinearPlan plan = make_plan(d, l->device, l->num_sms, a->rows);
+  CUtensorMap tmX;
+  const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
+  const cuuint64_t stride = a->ldx * esz;
+  st = encode_map(&tmX, e4m3, 2, a->x, size, &stride, plan.tile, "x");
+  if (st != CONVF_OK) return st;
   LinearParams p{};
-  p.rows = a->rows; p.N = d.N; p.K = d.K; p.experts = d.experts;
-  p.x = a->x; p.ldx = a->ldx; p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk;
-  p.w = l->w; p.ldw = d.ldw; p.expert_stride = d.expert_stride; p.w_scale = l->w_scale; p.bias = l->bias;
+  p.rows = a->rows; p.N = d.N; p.experts = d.experts;
+  p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
+  p.n_tiles = static_cast<int>(ceil_div(d.N, 128));
+  p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;
-  const cudaError_t e = launch_linear_simple(p, e4m3, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_linear_few(p, plan, e4m3, l->tmW, tmX, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "linear launch failed: %s", cudaGetErrorString(e));
   return record_ok();
 }
@@ -259,8 +344,13 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
   if (st != CONVF_OK) return st;
   if (!buf || len == 0) return record_error(CONVF_ERR_INVALID_ARG, "buf is NULL or len is 0");
   if (rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
-  snprintf(buf, len, "N=%d K=%d experts=%d %s rows=%d out=%s", l->d.N, l->d.K, l->d.experts,
-           l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : "bf16", rows, l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
+  const int n = snprintf(buf, len, "N=%d K=%d experts=%d %s rows=%d out=%s", l->d.N, l->d.K, l->d.experts,
+                         l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : "bf16", rows,
+                         l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
+  if (rows > 0 && n > 0 && static_cast<size_t>(n) < len) {
+    const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
+    snprintf(buf + n, len - n, " form=few_rows tile=128x%d split=%d grid=%d", plan.tile, plan.split, plan.grid);
+  }
   return record_ok();
 }
 

@@ -11,6 +11,7 @@ constexpr int kStatusOffsets = 4;
 constexpr int kScaleBlock = 128;    // columns (and weight rows) that share a scale
 constexpr float kE4m3Max = 448.0f;
 constexpr int kMaxExperts = 1024;   // the tile schedule keeps a prefix of them in shared memory
+constexpr int kKBlockBytes = 128;   // bytes of a k-block's operand row: 128 e4m3 or 64 bf16 values
 
 struct QuantParams {
   const void* x;
@@ -29,14 +30,12 @@ cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, 
                                    cudaStream_t stream);
 
 struct LinearParams {
-  int rows, N, K, experts;
-  const void* x;
-  long long ldx;
+  int rows, N, experts;
+  int num_kb;                // k-blocks of 128 bytes
+  int n_tiles;               // weight-row tiles of the chosen form
   const float* x_scale;
   long long xs_row, xs_blk;
-  const void* w;
-  long long ldw, expert_stride;
-  const float* w_scale;      // [experts][nblk][kblk]
+  const float* w_scale;      // [experts][nblk][num_kb]
   const float* bias;         // [experts][N] or null
   const int32_t* offsets;    // [experts + 1] or null
   void* y;
@@ -45,6 +44,21 @@ struct LinearParams {
   float lo, hi;
   int* status;
 };
-cudaError_t launch_linear_simple(const LinearParams& p, bool e4m3, cudaStream_t stream);
+
+// What a run launches (linear_plan): the form, its row tile, and how many CTAs share a tile's k.
+enum LinearForm : int { kLinearFew = 0 };
+struct LinearPlan {
+  int form;
+  int tile;     // kLinearFew: rows of x per tile (16, 32, 64 or 128)
+  int split;    // kLinearFew: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
+  int grid;     // CTAs
+};
+
+// tmW: {K, N, experts}, boxes of 128 bytes x 128 rows; tmX: {K, rows}, boxes of 128 bytes x plan.tile
+// rows; both in the 128-byte swizzle.
+cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
+                              const CUtensorMap& tmX, cudaStream_t stream);
+// clusters of `split` CTAs that run at once on the current device (0 on an error)
+int linear_few_max_clusters(bool e4m3, int tile, int split);
 
 }  // namespace convf

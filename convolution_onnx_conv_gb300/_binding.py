@@ -666,7 +666,9 @@ def _stream_of(t, stream):
     """cudaStream_t of `stream` (a torch stream or an int), else the current stream of t's device."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        # the public call builds a Stream object (2 us of a 10 us call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -677,9 +679,10 @@ def _rows_2d(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    ld, adjacent = t.stride()
+    if adjacent != 1 and c > 1:
         raise ValueError(f"{name}'s columns must be adjacent (stride 1)")
-    return r, c, (t.stride(0) if r > 1 else max(c, t.stride(0)))
+    return r, c, (ld if r > 1 or ld > c else c)   # one row has no stride of its own
 
 
 def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None, stream=None):
@@ -692,33 +695,43 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     u.  Rows of q lie a multiple of 16 bytes apart, as the layers read them; ``q`` and ``scale`` may
     be given.  Runs on the current torch stream."""
     import torch
-    xr, wide, ldx = _rows_2d(x, "x")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    rows, cols, ldx = _rows_2d(x, "x")
+    xr = rows
+    if x.dtype is torch.bfloat16:
+        kind = CONVF_OUT_BF16
+    elif x.dtype is torch.float32:
+        kind = CONVF_OUT_F32
+    else:
         raise ValueError("x must be bf16 or fp32")
-    if gated and wide % 2:
-        raise ValueError("gated rows have an even number of columns")
-    if index is not None and (not index.is_cuda or index.dtype != torch.int32 or index.dim() != 1
-                              or not index.is_contiguous()):
-        raise ValueError("index must be a contiguous int32 CUDA vector")
-    cols = wide // 2 if gated else wide
-    rows = xr if index is None else index.shape[0]
-    nblk, srows = -(-cols // 128), -(-rows // block_rows) if block_rows > 0 else rows
+    if gated:
+        if cols % 2:
+            raise ValueError("gated rows have an even number of columns")
+        cols //= 2
+    where = None
+    if index is not None:
+        if not index.is_cuda or index.dtype is not torch.int32 or index.dim() != 1 or not index.is_contiguous():
+            raise ValueError("index must be a contiguous int32 CUDA vector")
+        rows, where = index.shape[0], index.data_ptr()
+    nblk, srows = -(-cols // 128), rows if block_rows == 1 else -(-rows // 128)
     if q is None:
-        q = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=x.device)
-        if q.shape[1] != cols:
-            q = q[:, :cols]
+        ldq = -(-cols // 16) * 16
+        q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        qr, qc, ldq = _rows_2d(q, "q")
+        if q.dtype is not torch.float8_e4m3fn or qr != rows or qc != cols:
+            raise ValueError(f"q must be float8_e4m3fn of shape ({rows}, {cols})")
     if scale is None:
+        lds = nblk
         scale = torch.empty((srows, nblk), dtype=torch.float32, device=x.device)
-    qr, qc, ldq = _rows_2d(q, "q")
-    sr, sc, lds = _rows_2d(scale, "scale")
-    if q.dtype != torch.float8_e4m3fn or (qr, qc) != (rows, cols):
-        raise ValueError(f"q must be float8_e4m3fn of shape ({rows}, {cols})")
-    if scale.dtype != torch.float32 or (sr, sc) != (srows, nblk):
-        raise ValueError(f"scale must be float32 of shape ({srows}, {nblk})")
-    a = QuantArgs(rows, cols, x.data_ptr(), CONVF_OUT_BF16 if x.dtype == torch.bfloat16 else CONVF_OUT_F32, xr, ldx,
-                  None if index is None else index.data_ptr(), int(bool(gated)), int(block_rows), q.data_ptr(), ldq,
+    else:
+        sr, sc, lds = _rows_2d(scale, "scale")
+        if scale.dtype is not torch.float32 or sr != srows or sc != nblk:
+            raise ValueError(f"scale must be float32 of shape ({srows}, {nblk})")
+    a = QuantArgs(rows, cols, x.data_ptr(), kind, xr, ldx, where, 1 if gated else 0, block_rows, q.data_ptr(), ldq,
                   scale.data_ptr(), lds)
-    conv_fused_quantize_blocks(a, _stream_of(x, stream))
+    st = (_LIB or load_library()).conv_fused_quantize_blocks(ctypes.byref(a), _stream_of(x, stream))
+    if st != CONVF_OK:
+        _check(st)
     return q, scale
 
 
@@ -750,7 +763,7 @@ class ExpertLinear:
         w_scale = None if w_scale is None else w_scale.contiguous()
         bias = None if bias is None else bias.contiguous()
         self._keep = (w, w_scale, bias)   # the layer reads them in place
-        self.experts, self.N, self.K = E, N, K
+        self.experts, self.N, self.K, self.kblk, self.dtype = E, N, K, blocks[2], w.dtype
         self.out_dtype = torch.bfloat16 if out_bf16 else torch.float32
         d = LinearDesc(N, K, E, CONVF_LINEAR_E4M3 if self.e4m3 else CONVF_LINEAR_BF16,
                        w.stride(1) if N > 1 else max(w.stride(1), -(-K // 16) * 16), w.stride(0), act, float(clip[0]), float(clip[1]),
@@ -762,26 +775,30 @@ class ExpertLinear:
         rows, K, ldx = _rows_2d(x, "x")
         if K != self.K:
             raise ValueError(f"x must have {self.K} columns")
-        if x.dtype != self._keep[0].dtype:
-            raise ValueError(f"x must be {self._keep[0].dtype}")
-        if rows <= 1:   # one row has no stride of its own
+        if x.dtype is not self.dtype:
+            raise ValueError(f"x must be {self.dtype}")
+        if rows <= 1:
             ldx = -(-ldx // 16) * 16
+        xs = xs_row = xs_blk = 0
         if self.e4m3:
-            if x_scale is None or not x_scale.is_cuda or x_scale.dtype != torch.float32 \
-                    or tuple(x_scale.shape) != (rows, -(-K // 128)):
-                raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows, -(-K // 128))}")
+            if x_scale is None or not x_scale.is_cuda or x_scale.dtype is not torch.float32 \
+                    or x_scale.shape != (rows, self.kblk):
+                raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows, self.kblk)}")
+            xs = x_scale.data_ptr()
+            xs_row, xs_blk = x_scale.stride()
         elif x_scale is not None:
             raise ValueError("x_scale goes with float8_e4m3fn layers only")
         if y is None:
-            y = torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device)
-        yr, yc, ldy = _rows_2d(y, "y")
-        if y.dtype != self.out_dtype or (yr, yc) != (rows, self.N):
-            raise ValueError(f"y must be {self.out_dtype} of shape ({rows}, {self.N})")
-        a = LinearArgs(rows, x.data_ptr(), ldx, None, 0, 0, None if offsets is None else offsets.data_ptr(),
+            y, ldy = torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device), self.N
+        else:
+            yr, yc, ldy = _rows_2d(y, "y")
+            if y.dtype is not self.out_dtype or yr != rows or yc != self.N:
+                raise ValueError(f"y must be {self.out_dtype} of shape ({rows}, {self.N})")
+        a = LinearArgs(rows, x.data_ptr(), ldx, xs, xs_row, xs_blk, None if offsets is None else offsets.data_ptr(),
                        y.data_ptr(), ldy)
-        if x_scale is not None:
-            a.x_scale, a.xs_row, a.xs_blk = x_scale.data_ptr(), x_scale.stride(0), x_scale.stride(1)
-        conv_fused_linear_run(self.handle, a, _stream_of(x, stream))
+        st = _LIB.conv_fused_linear_run(self.handle, ctypes.byref(a), _stream_of(x, stream))
+        if st != CONVF_OK:
+            _check(st)
         return y
 
     def __call__(self, x, offsets, x_scale=None, y=None, stream=None):
@@ -789,7 +806,7 @@ class ExpertLinear:
         int32 CUDA [experts+1] and, for e4m3, ``x_scale`` fp32 [rows][ceil(K/128)] (any strides).
         Rows that no expert takes are not written."""
         import torch
-        if not offsets.is_cuda or offsets.dtype != torch.int32 or tuple(offsets.shape) != (self.experts + 1,) \
+        if not offsets.is_cuda or offsets.dtype is not torch.int32 or offsets.shape != (self.experts + 1,) \
                 or not offsets.is_contiguous():
             raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {self.experts + 1}")
         return self._run(x, offsets, x_scale, y, stream)

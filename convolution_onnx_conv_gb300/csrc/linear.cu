@@ -102,14 +102,13 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // clusters of `split` CTAs of the few-rows kernel that run at once (looked up once per process and
 // device; every writer stores the same value)
 int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
-  if (split == 1) return num_sms;
   static int known[kMaxDevices][2][4][4];
   int ti = 0, si = 0;
   while ((16 << ti) < tile) ++ti;
   while ((1 << si) < split) ++si;
   int* at = dev >= 0 && dev < kMaxDevices ? &known[dev][e4m3][ti][si] : nullptr;
   if (at && *at) return *at;
-  const int n = linear_few_max_clusters(e4m3, tile, split);
+  const int n = linear_few_max_clusters(e4m3, tile, split, num_sms);
   if (at) *at = n;
   return n;
 }

@@ -59,6 +59,6 @@ struct LinearPlan {
 cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
                               const CUtensorMap& tmX, cudaStream_t stream);
 // clusters of `split` CTAs that run at once on the current device (0 on an error)
-int linear_few_max_clusters(bool e4m3, int tile, int split);
+int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
 
 }  // namespace convf

@@ -37,14 +37,18 @@ struct FewCfg {
   static constexpr int kSchedBytes = (kMaxExperts + 1) * 4 + 12;
   static constexpr int kBarBytes = 512;
   static constexpr int kFixed = 1024 + kTableBytes + kRedBytes + kSchedBytes + kBarBytes;
-  static constexpr int kStages = (232448 - kFixed) / (kWBytes + kXBytes) > 12 ? 12 : (232448 - kFixed) / (kWBytes + kXBytes);
+  // 16 and 32 columns: two CTAs on an SM, so that one's start, exchange and end are behind the
+  // other's loads (and a dependent launch's start behind this one's end)
+  static constexpr int kPerSm = TN <= 32 ? 2 : 1;
+  static constexpr int kBudget = kPerSm == 2 ? 115712 : 232448;
+  static constexpr int kStages = (kBudget - kFixed) / (kWBytes + kXBytes);
   static constexpr int kSmem = kFixed + kStages * (kWBytes + kXBytes);
-  static_assert(kStages >= 4 && (2 * kStages + 3 * kBufs + 2) * 8 + 16 <= kBarBytes && kSmem <= 232448, "shared memory");
+  static_assert(kStages >= 4 && (2 * kStages + 3 * kBufs + 2) * 8 + 16 <= kBarBytes && kSmem <= kBudget, "shared memory");
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
 };
 
 template <bool F8, int TN>
-__global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, 1)
+__global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPerSm)
     linear_few_kernel(const LinearParams p, const int split, const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX) {
   using Cfg = FewCfg<F8, TN>;
@@ -95,17 +99,25 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, 1)
   if (split > 1) cluster_sync();   // the peers' barriers exist before anything is sent to them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  const long long t0 = blockIdx.x / split, tstep = gridDim.x / split;
+  const int ka = static_cast<int>(static_cast<long long>(p.num_kb) * rank / split);
+  const int kb_end = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / split);
+  const long long first_tiles = static_cast<long long>((p.rows + TN - 1) / TN) * p.n_tiles;
+  constexpr int kPrefetch = 16;
   // after the TMEM allocation: a dependent kernel's CTA that took this SM's TMEM first would wait for
   // this kernel, and this kernel for it
   pdl_launch_dependents();
+  // one layer: this CTA's first weight tile is known before the previous kernel has ended, and its
+  // way to L2 can begin (a prefetch reads nothing stale: what that kernel still writes lands in L2)
+  if (!p.offsets && warp == 0 && lane == 0 && t0 < first_tiles) {
+    const int n0 = static_cast<int>(t0 / ((p.rows + TN - 1) / TN)) * 128;
+    for (int kb = ka; kb < min(kb_end, ka + kPrefetch); ++kb) tma_prefetch_l2_3d(&tmW, kb * kElems, n0, 0);
+  }
   pdl_wait_prior();
   if (warp == 2) build_schedule(p, TN, prefix, blockIdx.x == 0);
   __syncthreads();
 
   const long long tiles = static_cast<long long>(prefix[p.experts]) * p.n_tiles;
-  const long long t0 = blockIdx.x / split, tstep = gridDim.x / split;
-  const int ka = static_cast<int>(static_cast<long long>(p.num_kb) * rank / split);
-  const int kb_end = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / split);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -326,7 +338,8 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
 }
 
 template <bool F8, int TN>
-int max_clusters_t(int split) {
+int max_clusters_t(int split, int num_sms) {
+  if (split == 1) return num_sms * FewCfg<F8, TN>::kPerSm;
   if (configure<F8, TN>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split);
@@ -355,12 +368,12 @@ cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, boo
   return cudaErrorInvalidValue;
 }
 
-int linear_few_max_clusters(bool e4m3, int tile, int split) {
+int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms) {
   switch (tile) {
-    case 16: return e4m3 ? max_clusters_t<true, 16>(split) : max_clusters_t<false, 16>(split);
-    case 32: return e4m3 ? max_clusters_t<true, 32>(split) : max_clusters_t<false, 32>(split);
-    case 64: return e4m3 ? max_clusters_t<true, 64>(split) : max_clusters_t<false, 64>(split);
-    case 128: return e4m3 ? max_clusters_t<true, 128>(split) : max_clusters_t<false, 128>(split);
+    case 16: return e4m3 ? max_clusters_t<true, 16>(split, num_sms) : max_clusters_t<false, 16>(split, num_sms);
+    case 32: return e4m3 ? max_clusters_t<true, 32>(split, num_sms) : max_clusters_t<false, 32>(split, num_sms);
+    case 64: return e4m3 ? max_clusters_t<true, 64>(split, num_sms) : max_clusters_t<false, 64>(split, num_sms);
+    case 128: return e4m3 ? max_clusters_t<true, 128>(split, num_sms) : max_clusters_t<false, 128>(split, num_sms);
   }
   return 0;
 }

@@ -50,7 +50,7 @@ convf_status current_device(int* dev, int* num_sms) {
 
 struct convf_linear {
   uint32_t magic;
-  CUtensorMap tmW;
+  CUtensorMap tmW, tmW256;   // boxes of 128 and of 256 weight rows
   int device, num_sms;
   convf_linear_desc d;
   const void* w;
@@ -113,34 +113,41 @@ int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
   return n;
 }
 
-// What a run of `rows` rows launches.  How the rows fall on the experts is known on the device only:
-// the plan goes by their mean (any offsets are right with any plan).
+// What a run of `rows` rows launches: the form with the least estimated time.  How the rows fall on
+// the experts is known on the device only, so the estimate goes by their mean, with half a tile per
+// expert lost at the groups' ends (any offsets are right with any plan).
 LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows) {
   const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
   const long long taken = rows < d.experts ? rows : d.experts;   // experts that can have rows
-  const long long mean = ceil_div(rows, taken);
-  LinearPlan plan{};
-  plan.form = kLinearFew;
-  plan.tile = 16;
-  while (plan.tile < 128 && plan.tile < mean) plan.tile *= 2;
   const int num_kb = static_cast<int>(ceil_div(static_cast<long long>(d.K) * (e4m3 ? 1 : 2), kKBlockBytes));
-  const long long nt = ceil_div(d.N, 128);
-  const long long likely = taken * ceil_div(mean, plan.tile) * nt;
-  const long long most = (d.experts > 1 ? rows / plan.tile + taken : ceil_div(rows, plan.tile)) * nt;
-  // cost in k-blocks: the waves of tiles, each its share of the reduction and a start and end worth
-  // about 4 k-blocks (8 with the exchange of partial sums)
+  auto row_tiles = [&](int tile) {
+    if (d.experts == 1) return ceil_div(rows, tile);
+    const long long n = (2LL * rows / tile + taken) / 2;
+    return n > taken ? n : taken;
+  };
+  LinearPlan plan{};
   long long best = -1;
-  for (int split = 1; split <= 8; split *= 2) {
-    if (split > num_kb) break;
-    const int at_once = few_clusters(dev, num_sms, e4m3, plan.tile, split);
-    if (at_once < 1) continue;
-    const long long cost = ceil_div(likely, at_once) * (ceil_div(num_kb, split) + (split > 1 ? 8 : 4));
-    if (best < 0 || cost < best) {
-      best = cost;
-      plan.split = split;
-      plan.grid = split * static_cast<int>(most < at_once ? most : at_once);
+  auto offer = [&](int form, int tile, int split, long long at_once, long long n_tiles, long long cycles) {
+    if (best >= 0 && cycles >= best) return;
+    best = cycles;
+    const long long most = (d.experts > 1 ? rows / tile + taken : ceil_div(rows, tile)) * n_tiles;
+    plan = LinearPlan{form, tile, split, split * static_cast<int>(most < at_once ? most : at_once)};
+  };
+  // cycles of an SM per k-block of a tile, and of a tile's start and end
+  for (int tile = 16; tile <= 128; tile *= 2) {
+    const long long nt = ceil_div(d.N, 128);
+    const long long per_kb = tile <= 32 ? 320 : tile == 64 ? 200 : e4m3 ? 340 : 280;   // (<= 32: of two tiles at once)
+    for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
+      const int at_once = few_clusters(dev, num_sms, e4m3, tile, split);
+      if (at_once < 1) continue;
+      offer(kLinearFew, tile, split, at_once, nt,
+            ceil_div(row_tiles(tile) * nt, at_once) * (ceil_div(num_kb, split) * per_kb + (split > 1 ? 3000 : 1500)));
     }
   }
+  const long long nt = ceil_div(d.N, kManyCols);
+  offer(kLinearMany, 128, 1, num_sms, nt, ceil_div(row_tiles(128) * nt, num_sms) * (num_kb * 600LL + 2500));
+  if (num_sms >= 2)
+    offer(kLinearMany, 256, 2, num_sms / 2, nt, ceil_div(row_tiles(256) * nt, num_sms / 2) * (num_kb * 540LL + 2500));
   return plan;
 }
 
@@ -248,6 +255,7 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
     const cuuint64_t strides[2] = {desc->ldw * esz,
                                    (desc->experts > 1 ? desc->expert_stride : desc->N * desc->ldw) * esz};
     st = encode_map(&l->tmW, e4m3, 3, W, size, strides, 128, "W");
+    if (st == CONVF_OK) st = encode_map(&l->tmW256, e4m3, 3, W, size, strides, 256, "W");
     if (st != CONVF_OK) {
       delete l;
       return st;
@@ -301,16 +309,23 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   CUtensorMap tmX;
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
   const cuuint64_t stride = a->ldx * esz;
-  st = encode_map(&tmX, e4m3, 2, a->x, size, &stride, plan.tile, "x");
+  st = encode_map(&tmX, e4m3, 2, a->x, size, &stride, plan.tile < 128 ? plan.tile : 128, "x");
   if (st != CONVF_OK) return st;
   LinearParams p{};
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
   p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
-  p.n_tiles = static_cast<int>(ceil_div(d.N, 128));
+  p.n_tiles = static_cast<int>(ceil_div(d.N, plan.form == kLinearMany ? kManyCols : 128));
+  // fp32 results of bf16 operands: the MMA's own accumulator truncates (1.2e-6 of the result at K =
+  // 1000, against 3e-7 when every 256 values are added in registers); bf16 results cannot tell
+  p.chunk_kb = e4m3 ? 1 : osz == 2 ? p.num_kb : 4;
+  p.vec_y = aligned(a->y, 16) && a->ldy * osz % 16 == 0;
   p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;
-  const cudaError_t e = launch_linear_few(p, plan, e4m3, l->tmW, tmX, static_cast<cudaStream_t>(stream));
+  const cudaStream_t strm = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = plan.form == kLinearFew
+                            ? launch_linear_few(p, plan, e4m3, l->tmW, tmX, strm)
+                            : launch_linear_many(p, plan, e4m3, plan.tile == 256 ? l->tmW : l->tmW256, tmX, strm);
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "linear launch failed: %s", cudaGetErrorString(e));
   return record_ok();
 }
@@ -348,7 +363,8 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
                          l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
   if (rows > 0 && n > 0 && static_cast<size_t>(n) < len) {
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
-    snprintf(buf + n, len - n, " form=few_rows tile=128x%d split=%d grid=%d", plan.tile, plan.split, plan.grid);
+    snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.form == kLinearFew ? "few_rows" : "many_rows",
+             plan.tile, plan.form == kLinearFew ? 128 : kManyCols, plan.form == kLinearFew ? plan.split : 1, plan.grid);
   }
   return record_ok();
 }

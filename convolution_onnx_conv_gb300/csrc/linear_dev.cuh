@@ -20,6 +20,16 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor, kind::f8f6f4 with e4m3 A/B (formats 0), fp32 D, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -47,6 +57,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
       return false;
     }
   }
+}
+
+// Arrive on another CTA's mbarrier without publishing this thread's memory accesses: for handing
+// back a TMEM buffer, whose reads tcgen05.wait::ld has completed.  (A release at cluster scope first
+// waits for every load and store in flight, the scales' prefetch among them: 2400 cycles per k-block
+// instead of 600.)
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
@@ -98,8 +116,10 @@ __device__ __forceinline__ void build_schedule(const LinearParams& p, int tile, 
 struct LinearTile {
   int e, row0, rows, n0;
 };
-// Tile t of prefix[experts] * n_tiles: within an expert the row tiles run fastest, so that the CTAs
-// of a wave share weight tiles (each is then read from memory once, and again from L2).
+// Tile t of prefix[experts] * n_tiles.  Within an expert the row tiles run fastest, in groups of
+// kRasterRows: the CTAs of a wave share weight tiles (each is then read from memory once, and again
+// from L2), and a long prompt's rows are not all passed over once per weight tile.
+constexpr int kRasterRows = 8;
 template <int TILE, int NTILE>
 __device__ __forceinline__ LinearTile tile_at(const LinearParams& p, const int* prefix, long long t) {
   int lo = 0, hi = p.experts;   // the last expert whose tiles start at or before t
@@ -112,7 +132,10 @@ __device__ __forceinline__ LinearTile tile_at(const LinearParams& p, const int* 
   }
   const int mt = prefix[lo + 1] - prefix[lo];
   const long long local = t - static_cast<long long>(prefix[lo]) * p.n_tiles;
-  const int nt = static_cast<int>(local / mt), m = static_cast<int>(local - static_cast<long long>(nt) * mt);
+  const int group = static_cast<int>(local / (static_cast<long long>(kRasterRows) * p.n_tiles));
+  const int in_group = static_cast<int>(local - static_cast<long long>(group) * kRasterRows * p.n_tiles);
+  const int height = min(kRasterRows, mt - group * kRasterRows);
+  const int nt = in_group / height, m = group * kRasterRows + in_group - nt * height;
   const RowGroup g = row_group(p, lo);
   LinearTile r;
   r.e = lo;
@@ -120,6 +143,15 @@ __device__ __forceinline__ LinearTile tile_at(const LinearParams& p, const int* 
   r.rows = min(TILE, g.last - r.row0);
   r.n0 = nt * NTILE;
   return r;
+}
+
+// tcgen05.wait::ld that the uses of r cannot be moved above
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
 // the clamp of an activation that keeps a NaN

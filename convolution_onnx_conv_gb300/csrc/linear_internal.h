@@ -32,6 +32,8 @@ cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, 
 struct LinearParams {
   int rows, N, experts;
   int num_kb;                // k-blocks of 128 bytes
+  int chunk_kb;              // k-blocks that an MMA accumulator sums before its sum goes to the registers'
+  int vec_y;                 // y's 16-byte stores are aligned
   int n_tiles;               // weight-row tiles of the chosen form
   const float* x_scale;
   long long xs_row, xs_blk;
@@ -46,10 +48,10 @@ struct LinearParams {
 };
 
 // What a run launches (linear_plan): the form, its row tile, and how many CTAs share a tile's k.
-enum LinearForm : int { kLinearFew = 0 };
+enum LinearForm : int { kLinearFew = 0, kLinearMany = 1 };
 struct LinearPlan {
   int form;
-  int tile;     // kLinearFew: rows of x per tile (16, 32, 64 or 128)
+  int tile;     // rows of x per tile: kLinearFew 16, 32, 64 or 128; kLinearMany 128, or 256 on CTA pairs
   int split;    // kLinearFew: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
   int grid;     // CTAs
 };
@@ -60,5 +62,11 @@ cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, boo
                               const CUtensorMap& tmX, cudaStream_t stream);
 // clusters of `split` CTAs that run at once on the current device (0 on an error)
 int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
+
+
+// tmW: boxes of 128 bytes x 256 rows (x 128 on CTA pairs); tmX: boxes of 128 bytes x 128 rows.
+cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
+                               const CUtensorMap& tmX, cudaStream_t stream);
+constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile
 
 }  // namespace convf

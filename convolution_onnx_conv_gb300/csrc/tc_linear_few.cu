@@ -12,7 +12,7 @@
 // e4m3: the MMAs of one 128-value k-block go to a TMEM buffer of their own, and the epilogue
 // adds buffer * (x_scale * w_scale) to fp32 sums in registers (a lane holds one weight row: the
 // weight scale is the same for the whole tile, the row scales differ by column and come from a
-// table that a warp fills ahead).  bf16: one buffer sums all of k.
+// table that a warp fills ahead).  bf16: a buffer sums LinearParams::chunk_kb k-blocks.
 //
 //   warp 0      TMA: weight and x tiles of each k-block
 //   warp 1      TMEM, MMA issue
@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       for (long long t = t0; t < tiles; t += tstep) {
-        for (int kb = ka; kb < kb_end; ++kb) {
-          const bool first = F8 || kb == ka;
+        for (int kb = ka, in_chunk = 0; kb < kb_end; ++kb) {
+          const bool first = F8 || in_chunk == 0;
           if (first && !mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) goto teardown;
           if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
           tc_fence_after();
@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
             stage = 0;
             phase ^= 1;
           }
-          if (F8 || kb == kb_end - 1) {
+          if (F8 || ++in_chunk == p.chunk_kb || kb == kb_end - 1) {
+            in_chunk = 0;
             tc_commit(&tfull[buf]);
             if (++buf == kBufs) {
               buf = 0;
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-      for (int kb = F8 ? ka : kb_end - 1; kb < kb_end; ++kb) {
+      for (int kb = ka; kb < kb_end; kb += F8 ? 1 : p.chunk_kb) {
         if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
         if (F8 && !mbar_wait(&sfull[buf], bphase, abort_flag, p.status)) goto teardown;
         tc_fence_after();
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(r[i]);
           }
         }
         tc_fence_before();

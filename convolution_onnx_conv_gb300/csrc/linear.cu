@@ -50,7 +50,7 @@ convf_status current_device(int* dev, int* num_sms) {
 
 struct convf_linear {
   uint32_t magic;
-  CUtensorMap tmW, tmW256;   // boxes of 128 and of 256 weight rows
+  CUtensorMap tmW64, tmW128, tmW256;   // boxes of 64, 128 and 256 weight rows
   int device, num_sms;
   convf_linear_desc d;
   const void* w;
@@ -145,22 +145,23 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
     }
   }
   const long long nt = ceil_div(d.N, kManyCols);
-  offer(kLinearMany, 128, 1, num_sms, nt, ceil_div(row_tiles(128) * nt, num_sms) * (num_kb * 600LL + 2500));
+  if (d.experts <= kManyExperts)
+    offer(kLinearMany, 128, 1, num_sms, nt, ceil_div(row_tiles(128) * nt, num_sms) * (num_kb * 600LL + 2500));
   if (num_sms >= 2)
     offer(kLinearMany, 256, 2, num_sms / 2, nt, ceil_div(row_tiles(256) * nt, num_sms / 2) * (num_kb * 540LL + 2500));
   return plan;
 }
 
-convf_status encode_map(CUtensorMap* m, bool e4m3, int dims, const void* p, const cuuint64_t* size,
+// boxes of 128 bytes x box_rows rows in the 128-byte swizzle
+convf_status encode_map(CUtensorMap* m, CUtensorMapDataType type, int esz, int dims, const void* p, const cuuint64_t* size,
                         const cuuint64_t* strides, int box_rows, const char* what) {
   EncodeTiledFn tiled;
   EncodeIm2colFn im2col;
   if (!tensor_map_encoders(&tiled, &im2col)) return record_error(CONVF_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(e4m3 ? kKBlockBytes : kKBlockBytes / 2),
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kKBlockBytes / esz),
                              static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = tiled(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims,
-                           const_cast<void*>(p), size, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = tiled(m, type, dims, const_cast<void*>(p), size, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return record_error(CONVF_ERR_CUDA, "encoding the tensor map of %s failed (%d)", what, (int)r);
@@ -254,8 +255,10 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
                                 static_cast<cuuint64_t>(desc->experts)};
     const cuuint64_t strides[2] = {desc->ldw * esz,
                                    (desc->experts > 1 ? desc->expert_stride : desc->N * desc->ldw) * esz};
-    st = encode_map(&l->tmW, e4m3, 3, W, size, strides, 128, "W");
-    if (st == CONVF_OK) st = encode_map(&l->tmW256, e4m3, 3, W, size, strides, 256, "W");
+    const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    st = encode_map(&l->tmW64, type, esz, 3, W, size, strides, 64, "W");
+    if (st == CONVF_OK) st = encode_map(&l->tmW128, type, esz, 3, W, size, strides, 128, "W");
+    if (st == CONVF_OK) st = encode_map(&l->tmW256, type, esz, 3, W, size, strides, 256, "W");
     if (st != CONVF_OK) {
       delete l;
       return st;
@@ -309,7 +312,8 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   CUtensorMap tmX;
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
   const cuuint64_t stride = a->ldx * esz;
-  st = encode_map(&tmX, e4m3, 2, a->x, size, &stride, plan.tile < 128 ? plan.tile : 128, "x");
+  st = encode_map(&tmX, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
+                  a->x, size, &stride, plan.tile < 128 ? plan.tile : 128, "x");
   if (st != CONVF_OK) return st;
   LinearParams p{};
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
@@ -322,10 +326,20 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;
+  p.clamp = l->lo != -INFINITY || l->hi != INFINITY;
+  CUtensorMap tmY = tmX;   // (not used without vec_y)
+  if (plan.form == kLinearMany && p.vec_y) {
+    const cuuint64_t ysize[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(a->rows)};
+    const cuuint64_t ystride = a->ldy * osz;
+    st = encode_map(&tmY, osz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                    static_cast<int>(osz), 2, a->y, ysize, &ystride, 32, "y");
+    if (st != CONVF_OK) return st;
+  }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
   const cudaError_t e = plan.form == kLinearFew
-                            ? launch_linear_few(p, plan, e4m3, l->tmW, tmX, strm)
-                            : launch_linear_many(p, plan, e4m3, plan.tile == 256 ? l->tmW : l->tmW256, tmX, strm);
+                            ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
+                            : launch_linear_many(p, plan, e4m3, plan.tile != 256 ? l->tmW256 : e4m3 ? l->tmW64 : l->tmW128,
+                                                 tmX, tmY, strm);
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "linear launch failed: %s", cudaGetErrorString(e));
   return record_ok();
 }

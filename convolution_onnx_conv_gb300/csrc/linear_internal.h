@@ -44,6 +44,7 @@ struct LinearParams {
   long long ldy;
   int out_bf16;
   float lo, hi;
+  int clamp;                 // [lo, hi] is not all numbers
   int* status;
 };
 
@@ -64,9 +65,11 @@ cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, boo
 int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
 
 
-// tmW: boxes of 128 bytes x 256 rows (x 128 on CTA pairs); tmX: boxes of 128 bytes x 128 rows.
+// tmW: boxes of 128 bytes x 256 rows (on CTA pairs x 64 for e4m3, x 128 for bf16); tmX: boxes of 128 bytes x 128 rows; tmY (used
+// where vec_y): {N, rows} of y, boxes of 128 bytes x 32 rows; all in the 128-byte swizzle.
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
-                               const CUtensorMap& tmX, cudaStream_t stream);
-constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile
+                               const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream);
+constexpr int kManyCols = 256;     // weight rows of a kLinearMany tile
+constexpr int kManyExperts = 640;  // at most, on single CTAs (the schedule's room beside the stages)
 
 }  // namespace convf

@@ -7,10 +7,13 @@
 // pair's 256 x 256 tile 64 (each CTA holds half of the weights), and L2 has to deliver 2/3 as many
 // bytes.
 //
-// e4m3: TMEM holds two accumulators of 256 columns.  The MMAs of a 128-value k-block fill one while the
-// epilogue adds the other, times x_scale * w_scale, to fp32 sums in registers: 128 columns per thread,
-// two warpgroups, as packed multiply-adds (64 per thread and k-block, half of the issue slots of the
-// 512 cycles that the MMAs take).  bf16: an accumulator sums LinearParams::chunk_kb k-blocks.
+// e4m3: a k-block's sums have to leave TMEM to be scaled, so the epilogue works all the time.  TMEM
+// holds a ring of four accumulators of 128 columns; the MMAs of a 128-value k-block fill one for each
+// half of the tile's columns, and a warpgroup adds its half's, times x_scale * w_scale, to fp32 sums in
+// registers: 128 columns per thread, as packed multiply-adds.  While it does the MMAs fill the other
+// three: 768 cycles for the way from the last MMA over the reads back to the next one (two accumulators
+// of 256 columns leave 512, and ran at half the rate).  bf16: an accumulator of 256 columns sums
+// LinearParams::chunk_kb k-blocks.
 //
 //   warp 0      TMA: x and weight tiles of each k-block
 //   warp 1      TMEM, MMA issue (of a pair: the leader's)
@@ -27,12 +30,12 @@ struct ManyCfg {
   static constexpr int kTileM = PAIR ? 256 : 128;
   static constexpr int kXBytes = 128 * kKBlockBytes;
   static constexpr int kWBytes = (PAIR ? 128 : 256) * kKBlockBytes;   // a pair's CTA holds half
-  static constexpr int kStages = PAIR ? 6 : 4;
-  static constexpr int kOutBytes = 2048;   // per epilogue warp: 32 rows of 64 bytes on the way out
-  static constexpr int kSchedBytes = (kMaxExperts + 1) * 4 + 12;
+  static constexpr int kStages = PAIR ? 5 : 4;
+  static constexpr int kOutBytes = 4096;   // per epilogue warp: 32 rows of 128 bytes on the way out
   static constexpr int kBarBytes = 256;
-  static constexpr int kSmem = 1024 + kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes + kSchedBytes;
-  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr int kFixed = kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes;   // and the schedule
+  static_assert((2 * kStages + 8) * 8 + 8 <= kBarBytes, "barriers");
+  static_assert(kFixed + ((PAIR ? kMaxExperts : kManyExperts) + 4) * 4 <= 232448, "shared memory");
   // registers: 168 per thread at launch; the epilogue's two warpgroups take what the others give up
   static constexpr int kRegs = 168, kRegsEpi = 224, kRegsOther = 56;
   static_assert(256 * kRegsEpi + 128 * kRegsOther <= kThreads * kRegs, "register split");
@@ -59,20 +62,19 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 template <bool F8, bool PAIR>
 __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     linear_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW,
-                       const __grid_constant__ CUtensorMap tmX) {
+                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
   using Cfg = ManyCfg<PAIR>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kElems = F8 ? 128 : 64;
   constexpr uint32_t kTmemCols = 512;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sX = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t sX[];   // (the swizzle goes by address bits 7 to 9)
   uint8_t* sW = sX + kStages * Cfg::kXBytes;
   uint8_t* sOut = sW + kStages * Cfg::kWBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * Cfg::kOutBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* tempty = tfull + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
 
@@ -85,9 +87,9 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {   // accumulator b: 128 columns, of half b & 1 of a tile
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], PAIR ? 16 : 8);   // every epilogue warp, of both CTAs
+      mbar_init(&tempty[b], PAIR ? 8 : 4);   // the warps of a half's warpgroup, of both CTAs
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -116,6 +118,13 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
   const long long tiles = static_cast<long long>(prefix[p.experts]) * p.n_tiles;
   const long long t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, tstep = PAIR ? gridDim.x >> 1 : gridDim.x;
 
+  // every earlier MMA of this thread has completed -> an arrival on `bar`, of a pair in both CTAs
+  auto commit_to = [&](uint64_t* bar) {
+    if (PAIR)
+      tc_commit_pair(bar, 3);
+    else
+      tc_commit(bar);
+  };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
     if (warp == 0 && lane == 0) {
@@ -130,7 +139,13 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
           if (PAIR) {
             const uint32_t bar = map_to_rank(smem_u32(&full[stage]), 0);
             tma_load_2d_pair(sX + stage * Cfg::kXBytes, &tmX, bar, kb * kElems, q.row0 + crank * 128);
-            tma_load_3d_pair(sW + stage * Cfg::kWBytes, &tmW, bar, kb * kElems, q.n0 + crank * 128, q.e);
+            if (F8) {   // this CTA's half of each half of the columns
+              tma_load_3d_pair(sW + stage * Cfg::kWBytes, &tmW, bar, kb * kElems, q.n0 + crank * 64, q.e);
+              tma_load_3d_pair(sW + stage * Cfg::kWBytes + 64 * kKBlockBytes, &tmW, bar, kb * kElems,
+                               q.n0 + 128 + crank * 64, q.e);
+            } else {
+              tma_load_3d_pair(sW + stage * Cfg::kWBytes, &tmW, bar, kb * kElems, q.n0 + crank * 128, q.e);
+            }
           } else {
             tma_load_2d(sX + stage * Cfg::kXBytes, &tmX, &full[stage], kb * kElems, q.row0);
             tma_load_3d(sW + stage * Cfg::kWBytes, &tmW, &full[stage], kb * kElems, q.n0, q.e);
@@ -141,49 +156,65 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 1 && lane == 0 && leader) {
-      constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(Cfg::kTileM, kManyCols) : idesc_bf16_f32(Cfg::kTileM, kManyCols);
-      int stage = 0, buf = 0;
+    } else if (warp == 1 && leader) {
+      // The whole warp walks the loop and one lane issues: the loop's state then stays in uniform
+      // registers, which is where the MMA takes its descriptors from.
+      const bool issue = elect_one();
+      constexpr int kCols = F8 ? 128 : 256;   // of an MMA
+      constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(Cfg::kTileM, kCols) : idesc_bf16_f32(Cfg::kTileM, kCols);
+      // weight rows of the second half of the columns (a pair's CTA holds half of each half)
+      constexpr uint32_t kHalf = (PAIR ? 64 : 128) * kKBlockBytes >> 4;
+      const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(sX)), b0 = sdesc_kmajor_sw128(smem_u32(sW));
+      int stage = 0, buf = 0;   // buf: 0 or 2, the first accumulator of the k-block
       uint32_t phase = 0, bphase = 0;
-      for (long long t = t0; t < tiles; t += tstep) {
+      const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;
+      for (long long j = 0; j < mine; ++j) {
         for (int kb = 0, in_chunk = 0; kb < p.num_kb; ++kb) {
           const bool first = F8 || in_chunk == 0;
-          if (first && !mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) goto teardown;
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-          tc_fence_after();
-          const uint64_t a = sdesc_kmajor_sw128(smem_u32(sX + stage * Cfg::kXBytes));
-          const uint64_t b = sdesc_kmajor_sw128(smem_u32(sW + stage * Cfg::kWBytes));
-          const uint32_t d = tmem_base + buf * kManyCols;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {   // 32 bytes of k each
-            const uint32_t acc = !first || i > 0;
-            if (F8 && PAIR)
-              tc_mma_f8_pair(d, a + 2 * i, b + 2 * i, idesc, acc);
-            else if (F8)
-              tc_mma_f8(d, a + 2 * i, b + 2 * i, idesc, acc);
-            else if (PAIR)
-              tc_mma_bf16_pair(d, a + 2 * i, b + 2 * i, idesc, acc);
-            else
-              tc_mma_bf16(d, a + 2 * i, b + 2 * i, idesc, acc);
+          const bool last = F8 || ++in_chunk == p.chunk_kb || kb == p.num_kb - 1;
+          // the three barriers are asked at once: their answers, one after the other, took longer
+          // than the MMAs
+          bool ready = mbar_test_wait(&full[stage], phase);
+          if (first) {
+            const bool r0 = mbar_test_wait(&tempty[buf], bphase ^ 1), r1 = mbar_test_wait(&tempty[buf + 1], bphase ^ 1);
+            ready = ready & r0 & r1;
           }
-          if (PAIR)
-            tc_commit_pair(&empty[stage], 3);
-          else
-            tc_commit(&empty[stage]);
+          if (!ready) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+            if (first && !mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) goto teardown;
+            if (first && !mbar_wait(&tempty[buf + 1], bphase ^ 1, abort_flag, p.status)) goto teardown;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + stage * (Cfg::kXBytes >> 4), b = b0 + stage * (Cfg::kWBytes >> 4);
+          const uint32_t d = tmem_base + buf * 128;
+          if (issue) {
+#pragma unroll
+            for (int h = 0; h < (F8 ? 2 : 1); ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {   // 32 bytes of k each
+                if (F8 && PAIR)
+                  tc_mma_f8_pair(d + h * 128, a + 2 * i, b + h * kHalf + 2 * i, idesc, i > 0);
+                else if (F8)
+                  tc_mma_f8(d + h * 128, a + 2 * i, b + h * kHalf + 2 * i, idesc, i > 0);
+                else if (PAIR)
+                  tc_mma_bf16_pair(d, a + 2 * i, b + 2 * i, idesc, !first || i > 0);
+                else
+                  tc_mma_bf16(d, a + 2 * i, b + 2 * i, idesc, !first || i > 0);
+              }
+              if (F8 && h == 0) commit_to(&tfull[buf]);
+            }
+            commit_to(&empty[stage]);
+            if (!F8 && last) commit_to(&tfull[buf]);
+            if (last) commit_to(&tfull[buf + 1]);
+          }
+          __syncwarp();
+          if (last) {
+            in_chunk = 0;
+            if ((buf ^= 2) == 0) bphase ^= 1;
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
-          }
-          if (F8 || ++in_chunk == p.chunk_kb || kb == p.num_kb - 1) {
-            in_chunk = 0;
-            if (PAIR)
-              tc_commit_pair(&tfull[buf], 3);
-            else
-              tc_commit(&tfull[buf]);
-            if (++buf == 2) {
-              buf = 0;
-              bphase ^= 1;
-            }
           }
         }
       }
@@ -192,57 +223,56 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
     const int quad = warp & 3, half = (warp - 4) >> 2;
     uint8_t* out = sOut + (warp - 4) * Cfg::kOutBytes;
-    const uint32_t lane_base = (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    const uint32_t from0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
     const int nblk = (p.N + kScaleBlock - 1) / kScaleBlock;
-    int buf = 0;
+    int buf = half;
     uint32_t bphase = 0;
     for (long long t = t0; t < tiles; t += tstep) {
       const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
       const int mrow = crank * 128 + quad * 32;   // this warp's first row of the tile
       const int n0 = q.n0 + half * 128;           // and its first column
+      // the scales are loaded two k-blocks ahead (and multiplied when they are used: a product at the
+      // load would wait for it); rows and columns past the edge read the last scale there is, and
+      // their sums are not stored
       const float *xs = nullptr, *ws = nullptr;
+      float x0 = 1.f, w0 = 1.f, x1 = 1.f, w1 = 1.f;
       if (F8) {
-        // rows and columns past the edge read the last scale there is; their sums are not stored
         xs = p.x_scale + (q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row;
         ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(n0 / kScaleBlock, nblk - 1)) * p.num_kb;
+        x0 = __ldg(xs);
+        w0 = __ldg(ws);
+        if (p.num_kb > 1) {
+          xs += p.xs_blk;
+          ++ws;
+        }
+        x1 = __ldg(xs);
+        w1 = __ldg(ws);
       }
-      // the scales of the next kAhead k-blocks are on their way (multiplied when they are used: a
-      // product here would wait for them)
-      constexpr int kAhead = 4;
-      float sx[kAhead], sw[kAhead];
-      auto fetch = [&](int kb, float& a, float& b) {
-        const bool in = F8 && kb < p.num_kb;
-        a = in ? __ldg(xs + kb * p.xs_blk) : 1.f;
-        b = in ? __ldg(ws + kb) : 1.f;
-      };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(i, sx[i], sw[i]);
       f32x2 acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0;
+#pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += F8 ? 1 : p.chunk_kb) {
-        const float both = sx[0] * sw[0];
+        const float both = x0 * w0;
         const f32x2 s = pair_of(__float_as_uint(both), __float_as_uint(both));
         if (F8) {
-#pragma unroll
-          for (int i = 0; i + 1 < kAhead; ++i) {
-            sx[i] = sx[i + 1];
-            sw[i] = sw[i + 1];
+          x0 = x1;
+          w0 = w1;
+          if (kb + 2 < p.num_kb) {
+            xs += p.xs_blk;
+            ++ws;
           }
-          fetch(kb + kAhead, sx[kAhead - 1], sw[kAhead - 1]);
+          x1 = __ldg(xs);
+          w1 = __ldg(ws);
         }
         if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
         tc_fence_after();
-        const uint32_t from = tmem_base + lane_base + buf * kManyCols;
-        // the next 16 columns are on their way while these are added
-        uint32_t r[2][16];
-        tmem_ld_32x32b_x16(from, r[0]);
+        const uint32_t from = from0 + (buf & 2) * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_ld_wait_for(r[c & 1]);
-          if (c < 7) {
-            tmem_ld_32x32b_x16(from + 16 * (c + 1), r[(c + 1) & 1]);
-          } else {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[64];
+          tmem_ld_32x32b_x64(from + 64 * c, r);   // waits for the values
+          if (c == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -253,75 +283,97 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[8 * c + i] = fma2(pair_of(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s, acc[8 * c + i]);
+          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fma2(pair_of(r[2 * i], r[2 * i + 1]), s, acc[32 * c + i]);
         }
-        if (++buf == 2) {
-          buf = 0;
-          bphase ^= 1;
-        }
+        buf ^= 2;
+        if (buf == half) bphase ^= 1;
       }
-      // the sums leave through shared memory, 32 rows of 64 bytes at a time (16-byte units swizzled
-      // by row), as 16-byte stores of 64 consecutive bytes per row
+      // out through shared memory, 32 rows of 128 bytes at a time (in the 128-byte swizzle): one TMA
+      // store where all 32 rows are the tile's (it clips the columns past N), else row by row
+      const bool whole = p.vec_y && mrow + 32 <= q.rows;
       const float* bias = p.bias ? p.bias + static_cast<long long>(q.e) * p.N : nullptr;
-      auto value = [&](float v, int n) { return act_clamp(bias && n < p.N ? v + __ldg(bias + n) : v, p.lo, p.hi); };
-      const int per_unit = p.out_bf16 ? 8 : 4;   // columns of a 16-byte unit
-      auto leave = [&](int n) {                  // the staged columns begin at n
+      auto finish = [&](float2 v, int n) {
+        if (bias) {
+          v.x += n < p.N ? __ldg(bias + n) : 0.f;
+          v.y += n + 1 < p.N ? __ldg(bias + n + 1) : 0.f;
+        }
+        if (p.clamp) {
+          v.x = act_clamp(v.x, p.lo, p.hi);
+          v.y = act_clamp(v.y, p.lo, p.hi);
+        }
+        return v;
+      };
+      auto room = [&] {   // the staged rows of the last store have been read
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 8 + (lane >> 2), u = lane & 3;
-          const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-          const int c = n + u * per_unit;
-          if (mrow + r < q.rows && c < p.N) {
-            const long long at = static_cast<long long>(q.row0 + mrow + r) * p.ldy + c;
-            if (p.vec_y && c + per_unit <= p.N) {
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + at * (p.out_bf16 ? 2 : 4)) = v;
-            } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              for (int j = 0; j < per_unit; ++j)
-                if (c + j < p.N) {
-                  if (p.out_bf16)
-                    static_cast<uint16_t*>(p.y)[at + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-                  else
-                    static_cast<uint32_t*>(p.y)[at + j] = w[j];
-                }
+      };
+      auto unit = [&](int u) { return reinterpret_cast<uint4*>(out + lane * 128 + ((u ^ (lane & 7)) << 4)); };
+      auto leave = [&](int n) {
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n < p.N) {
+            tma_store_2d(&tmY, out, n, q.row0 + mrow);
+            bulk_commit();
+          }
+          return;
+        }
+        __syncwarp();
+        const int osz = p.out_bf16 ? 2 : 4, per_unit = 16 / osz;
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3), u = lane & 7, c = n + u * per_unit;
+          if (mrow + r >= q.rows || c >= p.N) continue;
+          const uint8_t* v = out + r * 128 + ((u ^ (r & 7)) << 4);
+          uint8_t* to = static_cast<uint8_t*>(p.y) + (static_cast<long long>(q.row0 + mrow + r) * p.ldy + c) * osz;
+          if (p.vec_y && c + per_unit <= p.N) {
+            *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(v);
+          } else {
+            for (int j = 0; j < per_unit && c + j < p.N; ++j) {
+              if (osz == 2)
+                reinterpret_cast<uint16_t*>(to)[j] = reinterpret_cast<const uint16_t*>(v)[j];
+              else
+                reinterpret_cast<uint32_t*>(to)[j] = reinterpret_cast<const uint32_t*>(v)[j];
             }
           }
         }
         __syncwarp();
       };
-      auto unit = [&](int u) { return reinterpret_cast<uint4*>(out + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)); };
-      if (p.out_bf16) {
+      if (mrow < q.rows) {
+        if (p.out_bf16) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {   // 32 columns
+          for (int c = 0; c < 2; ++c) {
+            room();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
+            for (int u = 0; u < 8; ++u) {
+              uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = n0 + 32 * c + 8 * u + 2 * i;
-              const float2 v = split_of(acc[16 * c + 4 * u + i]);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(value(v.x, n), value(v.y, n + 1));
-              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = finish(split_of(acc[32 * c + 4 * u + i]), n0 + 64 * c + 8 * u + 2 * i);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *unit(u) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *unit(u) = make_uint4(w[0], w[1], w[2], w[3]);
+            leave(n0 + 64 * c);
           }
-          leave(n0 + 32 * c);
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {   // 16 columns
+          for (int c = 0; c < 4; ++c) {
+            room();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int n = n0 + 16 * c + 4 * u;
-            const float2 v0 = split_of(acc[8 * c + 2 * u]), v1 = split_of(acc[8 * c + 2 * u + 1]);
-            *unit(u) = make_uint4(__float_as_uint(value(v0.x, n)), __float_as_uint(value(v0.y, n + 1)),
-                                  __float_as_uint(value(v1.x, n + 2)), __float_as_uint(value(v1.y, n + 3)));
+            for (int u = 0; u < 8; ++u) {
+              const int n = n0 + 32 * c + 4 * u;
+              const float2 v0 = finish(split_of(acc[16 * c + 2 * u]), n);
+              const float2 v1 = finish(split_of(acc[16 * c + 2 * u + 1]), n + 2);
+              *unit(u) = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
+                                    __float_as_uint(v1.y));
+            }
+            leave(n0 + 32 * c);
           }
-          leave(n0 + 16 * c);
         }
       }
     }
+    if (lane == 0) bulk_wait_all();   // the stores have been written before the CTA ends
   }
 
 teardown:
@@ -344,7 +396,7 @@ teardown:
 
 template <bool F8, bool PAIR>
 cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                     cudaStream_t stream) {
+                     const CUtensorMap& tmY, cudaStream_t stream) {
   using Cfg = ManyCfg<PAIR>;
   static bool configured = false;
   if (!configured) {
@@ -353,21 +405,23 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
     cudaError_t e = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR>);
     if (e == cudaSuccess && at.numRegs < Cfg::kRegs) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
     configured = true;
   }
-  return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
-                    tmW, tmX);
+  const int smem = Cfg::kFixed + (p.experts + 4) / 4 * 16;   // experts + 1 ints
+  if (smem > 232448) return cudaErrorInvalidValue;
+  return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), smem, stream, PAIR ? 2 : 1, p,
+                    tmW, tmX, tmY);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
-                               const CUtensorMap& tmX, cudaStream_t stream) {
+                               const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream) {
   if (plan.tile == 256)
-    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, stream) : launch_t<false, true>(p, plan, tmW, tmX, stream);
-  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, stream) : launch_t<false, false>(p, plan, tmW, tmX, stream);
+    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, true>(p, plan, tmW, tmX, tmY, stream);
+  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, false>(p, plan, tmW, tmX, tmY, stream);
 }
 
 }  // namespace convf

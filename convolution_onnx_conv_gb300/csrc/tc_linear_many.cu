@@ -9,15 +9,17 @@
 //
 // e4m3: a k-block's sums have to leave TMEM to be scaled, so the epilogue works all the time.  TMEM
 // holds a ring of four accumulators of 128 columns; the MMAs of a 128-value k-block fill one for each
-// half of the tile's columns, and a warpgroup adds its half's, times x_scale * w_scale, to fp32 sums in
-// registers: 128 columns per thread, as packed multiply-adds.  While it does the MMAs fill the other
-// three: 768 cycles for the way from the last MMA over the reads back to the next one (two accumulators
-// of 256 columns leave 512, and ran at half the rate).  bf16: an accumulator of 256 columns sums
-// LinearParams::chunk_kb k-blocks.
+// half of the tile's columns, and the epilogue adds it, times x_scale * w_scale, to fp32 sums in
+// registers, as packed multiply-adds.  An accumulator has 768 cycles for the way from its last MMA over
+// the reads back to its next MMA before the tensor cores wait; sixteen warps of 64 columns each have
+// read theirs after two loads (eight warps of 128 columns took 720 cycles per k-block, and two
+// accumulators of 256 columns 1080).  bf16: an accumulator of 256 columns sums LinearParams::chunk_kb
+// k-blocks.
 //
-//   warp 0      TMA: x and weight tiles of each k-block
-//   warp 1      TMEM, MMA issue (of a pair: the leader's)
-//   warps 4-11  epilogue
+//   warps 0-7   epilogue: warp w the rows 32 (w % 4) .. and the columns 128 (w / 4) .. of the CTA's tile
+//   warp 8      TMA: x and weight tiles of each k-block
+//   warp 9      TMEM, MMA issue (of a pair: the leader's)
+//   (warps 10, 11: none; registers are handed over by warpgroups)
 #include "linear_dev.cuh"
 
 namespace convf {
@@ -27,18 +29,19 @@ namespace {
 template <bool PAIR>
 struct ManyCfg {
   static constexpr int kThreads = 384;
+  // registers: 168 per thread at launch; the epilogue's two warpgroups take what the third gives up
+  static constexpr int kRegs = 168, kRegsEpi = 224, kRegsOther = 56;
+  static_assert(256 * kRegsEpi + 128 * kRegsOther <= kThreads * kRegs, "register split");
   static constexpr int kTileM = PAIR ? 256 : 128;
   static constexpr int kXBytes = 128 * kKBlockBytes;
   static constexpr int kWBytes = (PAIR ? 128 : 256) * kKBlockBytes;   // a pair's CTA holds half
-  static constexpr int kStages = PAIR ? 5 : 4;
-  static constexpr int kOutBytes = 4096;   // per epilogue warp: 32 rows of 128 bytes on the way out
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kOutBytes = 1024;   // per epilogue warp: 8 rows of 128 bytes on the way out
   static constexpr int kBarBytes = 256;
-  static constexpr int kFixed = kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes;   // and the schedule
+  static constexpr int kFixed = kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes;
+  static constexpr int kSmem = kFixed + (kMaxExperts + 4) * 4;
   static_assert((2 * kStages + 8) * 8 + 8 <= kBarBytes, "barriers");
-  static_assert(kFixed + ((PAIR ? kMaxExperts : kManyExperts) + 4) * 4 <= 232448, "shared memory");
-  // registers: 168 per thread at launch; the epilogue's two warpgroups take what the others give up
-  static constexpr int kRegs = 168, kRegsEpi = 224, kRegsOther = 56;
-  static_assert(256 * kRegsEpi + 128 * kRegsOther <= kThreads * kRegs, "register split");
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 // two fp32 columns in a register pair
@@ -53,16 +56,61 @@ __device__ __forceinline__ float2 split_of(f32x2 v) {
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
   return make_float2(__uint_as_float(lo), __uint_as_float(hi));
 }
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+__device__ __forceinline__ void fma2(f32x2& c, f32x2 a, f32x2 b) {
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bf16_pair(f32x2 v) {
+  const float2 f = split_of(v);
+  return bf16_pair(f.x, f.y);
+}
+__device__ __forceinline__ uint4 unit_of(f32x2 a, f32x2 b) {
+  const float2 u = split_of(a), v = split_of(b);
+  return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
+}
+// four columns from n of a row of y (element `at`): the bias, the clamp, the one rounding
+__device__ __forceinline__ void finish4(const LinearParams& p, long long at, int n, float4 v, const float (&b)[4]) {
+  float f[4] = {v.x + b[0], v.y + b[1], v.z + b[2], v.w + b[3]};
+  if (p.clamp) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = act_clamp(f[j], p.lo, p.hi);
+  }
+  if (p.vec_y && n + 4 <= p.N) {
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(f[0], f[1], f[2], f[3]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < p.N) {
+      if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.y)[at + j] = __float2bfloat16_rn(f[j]);
+      else
+        static_cast<float*>(p.y)[at + j] = f[j];
+    }
+}
+// 32 bytes: a whole sector at once where they are one
+__device__ __forceinline__ void st_global_32(uint8_t* p, uint4 a, uint4 b, bool sector) {
+  if (!sector) {
+    *reinterpret_cast<uint4*>(p) = a;
+    *reinterpret_cast<uint4*>(p + 16) = b;
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 
 template <bool F8, bool PAIR>
 __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     linear_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW,
-                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
+                       const __grid_constant__ CUtensorMap tmX) {
   using Cfg = ManyCfg<PAIR>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kElems = F8 ? 128 : 64;
@@ -89,14 +137,14 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     }
     for (int b = 0; b < 4; ++b) {   // accumulator b: 128 columns, of half b & 1 of a tile
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], PAIR ? 8 : 4);   // the warps of a half's warpgroup, of both CTAs
+      mbar_init(&tempty[b], PAIR ? 8 : 4);   // the epilogue warps of a half, of both CTAs
     }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
   }
-  if (warp == 1) {
+  if (warp == 9) {
     if (PAIR) {
       tmem_alloc_pair(tmem_slot, kTmemCols);
       tmem_relinquish_pair();
@@ -112,7 +160,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();   // after the TMEM allocation, which a dependent's CTA would otherwise take
   pdl_wait_prior();
-  if (warp == 2) build_schedule(p, Cfg::kTileM, prefix, blockIdx.x == 0);
+  if (warp == 8) build_schedule(p, Cfg::kTileM, prefix, blockIdx.x == 0);
   __syncthreads();
 
   const long long tiles = static_cast<long long>(prefix[p.experts]) * p.n_tiles;
@@ -125,9 +173,9 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     else
       tc_commit(bar);
   };
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
-    if (warp == 0 && lane == 0) {
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
+  if (warp == 8) {
+    if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       for (long long t = t0; t < tiles; t += tstep) {
@@ -156,7 +204,9 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 1 && leader) {
+    }
+  } else if (warp == 9) {
+    if (leader) {
       // The whole warp walks the loop and one lane issues: the loop's state then stays in uniform
       // registers, which is where the MMA takes its descriptors from.
       const bool issue = elect_one();
@@ -219,32 +269,25 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
       }
     }
-  } else {
+  } else if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* out = sOut + (warp - 4) * Cfg::kOutBytes;
+    const int quad = warp & 3, half = warp >> 2;
+    const int mrow = crank * 128 + quad * 32;   // this warp's first row of the tile
     const uint32_t from0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-    const int nblk = (p.N + kScaleBlock - 1) / kScaleBlock;
     int buf = half;
     uint32_t bphase = 0;
+    bool ready = false;
     for (long long t = t0; t < tiles; t += tstep) {
-      const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
-      const int mrow = crank * 128 + quad * 32;   // this warp's first row of the tile
-      const int n0 = q.n0 + half * 128;           // and its first column
-      // the scales are loaded two k-blocks ahead (and multiplied when they are used: a product at the
-      // load would wait for it); rows and columns past the edge read the last scale there is, and
-      // their sums are not stored
+      // the scales are loaded a k-block ahead (and multiplied when they are used: a product at the load
+      // would wait for it); rows and columns past the edge read the last scale there is, and their
+      // sums are not stored
       const float *xs = nullptr, *ws = nullptr;
-      float x0 = 1.f, w0 = 1.f, x1 = 1.f, w1 = 1.f;
+      float x1 = 1.f, w1 = 1.f;
       if (F8) {
+        const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
+        const int nblk = (p.N + kScaleBlock - 1) / kScaleBlock;
         xs = p.x_scale + (q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row;
-        ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(n0 / kScaleBlock, nblk - 1)) * p.num_kb;
-        x0 = __ldg(xs);
-        w0 = __ldg(ws);
-        if (p.num_kb > 1) {
-          xs += p.xs_blk;
-          ++ws;
-        }
+        ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(q.n0 / kScaleBlock + half, nblk - 1)) * p.num_kb;
         x1 = __ldg(xs);
         w1 = __ldg(ws);
       }
@@ -253,127 +296,97 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       for (int c = 0; c < 64; ++c) acc[c] = 0;
 #pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += F8 ? 1 : p.chunk_kb) {
-        const float both = x0 * w0;
+        if (!ready && !mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
+        tc_fence_after();
+        const uint32_t from = from0 + (buf & 2) * 128;
+        f32x2 r[32];
+        tmem_ld_64_wait(from, r);
+        const float both = x1 * w1;
         const f32x2 s = pair_of(__float_as_uint(both), __float_as_uint(both));
-        if (F8) {
-          x0 = x1;
-          w0 = w1;
-          if (kb + 2 < p.num_kb) {
-            xs += p.xs_blk;
-            ++ws;
-          }
+        if (F8 && kb + 1 < p.num_kb) {
+          xs += p.xs_blk;
+          ++ws;
           x1 = __ldg(xs);
           w1 = __ldg(ws);
         }
-        if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
-        tc_fence_after();
-        const uint32_t from = from0 + (buf & 2) * 128;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[64];
-          tmem_ld_32x32b_x64(from + 64 * c, r);   // waits for the values
-          if (c == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (PAIR)
-                mbar_arrive_remote_relaxed(map_to_rank(smem_u32(&tempty[buf]), 0));
-              else
-                mbar_arrive(&tempty[buf]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fma2(pair_of(r[2 * i], r[2 * i + 1]), s, acc[32 * c + i]);
+        for (int i = 0; i < 32; ++i) fma2(acc[i], r[i], s);
+        tmem_ld_64_wait(from + 64, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_remote_relaxed(map_to_rank(smem_u32(&tempty[buf]), 0));
+          else
+            mbar_arrive(&tempty[buf]);
         }
         buf ^= 2;
         if (buf == half) bphase ^= 1;
+        // asked before the last sums, so that the answer is not waited for
+        ready = mbar_test_wait(&tfull[buf], bphase);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) fma2(acc[32 + i], r[i], s);
       }
-      // out through shared memory, 32 rows of 128 bytes at a time (in the 128-byte swizzle): one TMA
-      // store where all 32 rows are the tile's (it clips the columns past N), else row by row
-      const bool whole = p.vec_y && mrow + 32 <= q.rows;
+      const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
+      const int n0 = q.n0 + half * 128;   // this warp's first column
+      if (mrow >= q.rows || n0 >= p.N) continue;
       const float* bias = p.bias ? p.bias + static_cast<long long>(q.e) * p.N : nullptr;
-      auto finish = [&](float2 v, int n) {
-        if (bias) {
-          v.x += n < p.N ? __ldg(bias + n) : 0.f;
-          v.y += n + 1 < p.N ? __ldg(bias + n + 1) : 0.f;
-        }
-        if (p.clamp) {
-          v.x = act_clamp(v.x, p.lo, p.hi);
-          v.y = act_clamp(v.y, p.lo, p.hi);
-        }
-        return v;
-      };
-      auto room = [&] {   // the staged rows of the last store have been read
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-      };
-      auto unit = [&](int u) { return reinterpret_cast<uint4*>(out + lane * 128 + ((u ^ (lane & 7)) << 4)); };
-      auto leave = [&](int n) {
-        if (whole) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && n < p.N) {
-            tma_store_2d(&tmY, out, n, q.row0 + mrow);
-            bulk_commit();
-          }
-          return;
-        }
-        __syncwarp();
-        const int osz = p.out_bf16 ? 2 : 4, per_unit = 16 / osz;
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3), u = lane & 7, c = n + u * per_unit;
-          if (mrow + r >= q.rows || c >= p.N) continue;
-          const uint8_t* v = out + r * 128 + ((u ^ (r & 7)) << 4);
-          uint8_t* to = static_cast<uint8_t*>(p.y) + (static_cast<long long>(q.row0 + mrow + r) * p.ldy + c) * osz;
-          if (p.vec_y && c + per_unit <= p.N) {
-            *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(v);
+      if (!bias && !p.clamp && p.vec_y && n0 + 128 <= p.N) {
+        // a thread's row, in whole 32-byte sectors where rows begin on them
+        if (mrow + lane < q.rows) {
+          const long long at = static_cast<long long>(q.row0 + mrow + lane) * p.ldy + n0;
+          const bool sector = p.vec_y == 2;
+          if (p.out_bf16) {
+            uint8_t* row = static_cast<uint8_t*>(p.y) + at * 2;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              st_global_32(row + 32 * u,
+                           make_uint4(bf16_pair(acc[8 * u]), bf16_pair(acc[8 * u + 1]), bf16_pair(acc[8 * u + 2]),
+                                      bf16_pair(acc[8 * u + 3])),
+                           make_uint4(bf16_pair(acc[8 * u + 4]), bf16_pair(acc[8 * u + 5]), bf16_pair(acc[8 * u + 6]),
+                                      bf16_pair(acc[8 * u + 7])),
+                           sector);
           } else {
-            for (int j = 0; j < per_unit && c + j < p.N; ++j) {
-              if (osz == 2)
-                reinterpret_cast<uint16_t*>(to)[j] = reinterpret_cast<const uint16_t*>(v)[j];
-              else
-                reinterpret_cast<uint32_t*>(to)[j] = reinterpret_cast<const uint32_t*>(v)[j];
-            }
+            uint8_t* row = static_cast<uint8_t*>(p.y) + at * 4;
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              st_global_32(row + 32 * u, unit_of(acc[4 * u], acc[4 * u + 1]), unit_of(acc[4 * u + 2], acc[4 * u + 3]), sector);
           }
         }
-        __syncwarp();
-      };
-      if (mrow < q.rows) {
-        if (p.out_bf16) {
+      } else {
+        // A bias, a clamp, unaligned rows or the ragged edge of N: 8 rows of 32 columns at a time through
+        // shared memory, where a lane then has 4 columns of 2 rows.  (Arithmetic on the registers' own
+        // halves has the compiler keep the halves of every pair apart: the multiply-adds of the loop
+        // above then cost two each, 800 instead of 650 cycles per k-block.)
+        uint8_t* out = sOut + warp * Cfg::kOutBytes;
+        const int rows = min(32, q.rows - mrow);
+        const int c4 = (lane & 7) * 4;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            room();
+        for (int pass = 0; pass < 4; ++pass) {
+          const int n = n0 + 32 * pass + c4;
+          float b[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              uint32_t w[4];
+          for (int j = 0; j < 4; ++j) b[j] = bias ? __ldg(bias + min(n + j, p.N - 1)) : 0.f;
+          for (int r0 = 0; r0 < rows; r0 += 8) {
+            if ((lane & ~7) == r0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = finish(split_of(acc[32 * c + 4 * u + i]), n0 + 64 * c + 8 * u + 2 * i);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              *unit(u) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(out + (lane & 7) * 128 + ((u ^ (lane & 7)) << 4)) =
+                    unit_of(acc[16 * pass + 2 * u], acc[16 * pass + 2 * u + 1]);
             }
-            leave(n0 + 64 * c);
-          }
-        } else {
+            __syncwarp();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            room();
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int n = n0 + 32 * c + 4 * u;
-              const float2 v0 = finish(split_of(acc[16 * c + 2 * u]), n);
-              const float2 v1 = finish(split_of(acc[16 * c + 2 * u + 1]), n + 2);
-              *unit(u) = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
-                                    __float_as_uint(v1.y));
+            for (int i = 0; i < 2; ++i) {
+              const int r = (lane >> 3) + 4 * i;
+              const float4 v = *reinterpret_cast<const float4*>(out + r * 128 + (((lane & 7) ^ r) << 4));
+              if (r0 + r < rows && n < p.N)
+                finish4(p, static_cast<long long>(q.row0 + mrow + r0 + r) * p.ldy + n, n, v, b);
             }
-            leave(n0 + 32 * c);
+            __syncwarp();
           }
         }
       }
     }
-    if (lane == 0) bulk_wait_all();   // the stores have been written before the CTA ends
   }
 
 teardown:
@@ -384,7 +397,7 @@ teardown:
   }
   __syncthreads();
   if (PAIR) cluster_sync();   // no CTA of the pair leaves while the other may still signal it
-  if (warp == 1) {
+  if (warp == 9) {
     __syncwarp();
     tc_fence_after();
     if (PAIR)
@@ -396,7 +409,7 @@ teardown:
 
 template <bool F8, bool PAIR>
 cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                     const CUtensorMap& tmY, cudaStream_t stream) {
+                     cudaStream_t stream) {
   using Cfg = ManyCfg<PAIR>;
   static bool configured = false;
   if (!configured) {
@@ -405,23 +418,21 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
     cudaError_t e = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR>);
     if (e == cudaSuccess && at.numRegs < Cfg::kRegs) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     configured = true;
   }
-  const int smem = Cfg::kFixed + (p.experts + 4) / 4 * 16;   // experts + 1 ints
-  if (smem > 232448) return cudaErrorInvalidValue;
-  return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), smem, stream, PAIR ? 2 : 1, p,
-                    tmW, tmX, tmY);
+  return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
+                    tmW, tmX);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
-                               const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream) {
+                               const CUtensorMap& tmX, cudaStream_t stream) {
   if (plan.tile == 256)
-    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, true>(p, plan, tmW, tmX, tmY, stream);
-  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, false>(p, plan, tmW, tmX, tmY, stream);
+    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, stream) : launch_t<false, true>(p, plan, tmW, tmX, stream);
+  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, stream) : launch_t<false, false>(p, plan, tmW, tmX, stream);
 }
 
 }  // namespace convf

@@ -102,7 +102,7 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // clusters of `split` CTAs of the few-rows kernel that run at once (looked up once per process and
 // device; every writer stores the same value)
 int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
-  static int known[kMaxDevices][2][4][4];
+  static int known[kMaxDevices][2][3][4];
   int ti = 0, si = 0;
   while ((16 << ti) < tile) ++ti;
   while ((1 << si) < split) ++si;
@@ -125,29 +125,41 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
     const long long n = (2LL * rows / tile + taken) / 2;
     return n > taken ? n : taken;
   };
+  // Estimated nanoseconds, fitted to runs of every form at 1 to 24576 rows, 1 to 64 experts and N, K from
+  // 1024 to 4096: waves of tiles, each its k-blocks' time and a start and end, behind a launch; or the
+  // bytes, at 6.3 TB/s, if that is more.  (2048 x 2048 layers, 16 experts, e4m3: 64 rows few/16 15.4 us,
+  // many/128 16.2; 512 rows 21.3, 16.6; 4096 x 4096 layer: 48 rows few/16 12.5 us, few/64 14.0, many/256
+  // 15.7; 2048 rows of 2048 x 2048 few/64 29 us, many/128 12.5.)
   LinearPlan plan{};
   long long best = -1;
-  auto offer = [&](int form, int tile, int split, long long at_once, long long n_tiles, long long cycles) {
-    if (best >= 0 && cycles >= best) return;
-    best = cycles;
+  const long long esz = e4m3 ? 1 : 2;
+  const long long bytes = taken * d.N * d.K * esz + static_cast<long long>(rows) * (d.K * esz + d.N * 2LL);
+  auto offer = [&](int form, int tile, int split, long long units, long long n_tiles, long long per_kb, long long ends) {
+    const long long waves = ceil_div(row_tiles(tile) * n_tiles, units);
+    const long long model = 3500 + waves * (ceil_div(num_kb, split) * per_kb + ends), memory = 3500 + bytes / 6300;
+    const long long ns = (model > memory ? model : memory) + model / 8;
+    if (best >= 0 && ns >= best) return;
+    best = ns;
     const long long most = (d.experts > 1 ? rows / tile + taken : ceil_div(rows, tile)) * n_tiles;
-    plan = LinearPlan{form, tile, split, split * static_cast<int>(most < at_once ? most : at_once)};
+    const int ctas = form == kLinearMany && tile == 256 ? 2 : split;
+    plan = LinearPlan{form, tile, split, ctas * static_cast<int>(most < units ? most : units)};
   };
-  // cycles of an SM per k-block of a tile, and of a tile's start and end
-  for (int tile = 16; tile <= 128; tile *= 2) {
-    const long long nt = ceil_div(d.N, 128);
-    const long long per_kb = tile <= 32 ? 320 : tile == 64 ? 200 : e4m3 ? 340 : 280;   // (<= 32: of two tiles at once)
+  const long long nt = ceil_div(d.N, 128), nt_many = ceil_div(d.N, kManyCols);
+  for (int tile = 16; tile <= 64; tile *= 2) {
+    // with two CTAs on an SM (16 and 32 columns), and alone
+    const long long shared = tile == 16 ? (e4m3 ? 330 : 240) : (e4m3 ? 480 : 280);
+    const long long alone = tile == 16 ? (e4m3 ? 220 : 160) : tile == 32 ? (e4m3 ? 240 : 180) : (e4m3 ? 430 : 245);
     for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
-      const int at_once = few_clusters(dev, num_sms, e4m3, tile, split);
-      if (at_once < 1) continue;
-      offer(kLinearFew, tile, split, at_once, nt,
-            ceil_div(row_tiles(tile) * nt, at_once) * (ceil_div(num_kb, split) * per_kb + (split > 1 ? 3000 : 1500)));
+      const long long tiles = row_tiles(tile) * nt;
+      const int units = few_clusters(dev, num_sms, e4m3, tile, split);
+      if (units < 1 || (split > 1 && tiles > units)) continue;   // sharing a tile pays in a single wave
+      const bool one_each = tiles * split <= num_sms;
+      offer(kLinearFew, tile, split, units, nt, one_each || tile == 64 ? (tile == 64 && one_each && e4m3 ? 330 : alone) : shared,
+            split == 1 ? 700 : 1000 + 500 * split + 75 * tile);
     }
   }
-  const long long nt = ceil_div(d.N, kManyCols);
-  offer(kLinearMany, 128, 1, num_sms, nt, ceil_div(row_tiles(128) * nt, num_sms) * (num_kb * 600LL + 2500));
-  if (num_sms >= 2)
-    offer(kLinearMany, 256, 2, num_sms / 2, nt, ceil_div(row_tiles(256) * nt, num_sms / 2) * (num_kb * 540LL + 2500));
+  offer(kLinearMany, 128, 1, num_sms, nt_many, e4m3 ? 440 : 375, 2000);
+  if (num_sms >= 2) offer(kLinearMany, 256, 1, num_sms / 2, nt_many, e4m3 ? 420 : 280, 2000);
   return plan;
 }
 
@@ -207,10 +219,11 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   p.x = a->x; p.ldx = a->ldx; p.x_rows = a->x_rows; p.index = a->index;
   p.rows = a->rows; p.cols = a->cols; p.nblk = nblk;
   p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
-  const bool row16 = a->ldx * esz % 16 == 0;
-  p.vec_x = row16 && aligned(a->x, 16);
-  p.vec_u = p.vec_x && static_cast<long long>(a->cols) * esz % 16 == 0;
-  p.vec_q = a->ldq % 8 == 0 && aligned(a->q, 8);
+  auto rows_on = [&](int bytes) {
+    return aligned(a->x, bytes) && a->ldx * esz % bytes == 0 && (!a->gated || static_cast<long long>(a->cols) * esz % bytes == 0);
+  };
+  p.vec = rows_on(8) && a->ldq % 8 == 0 && aligned(a->q, 8);
+  p.wide = rows_on(16);
   const cudaError_t e = launch_quantize_blocks(p, esz == 2, a->gated != 0, a->block_rows, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "quantising launch failed: %s", cudaGetErrorString(e));
   return record_ok();
@@ -369,7 +382,7 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
   if (rows > 0 && n > 0 && static_cast<size_t>(n) < len) {
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
     snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.form == kLinearFew ? "few_rows" : "many_rows",
-             plan.tile, plan.form == kLinearFew ? 128 : kManyCols, plan.form == kLinearFew ? plan.split : 1, plan.grid);
+             plan.tile, plan.form == kLinearFew ? 128 : kManyCols, plan.split, plan.grid);
   }
   return record_ok();
 }

@@ -23,8 +23,7 @@ struct QuantParams {
   long long ldq;
   float* scale;
   long long lds;
-  // vector accesses: x's (and, gated, the second half's) 16-byte and q's 8-byte ones are aligned
-  int vec_x, vec_u, vec_q;
+  int vec, wide;   // rows of x (and its second half, gated) and of q begin on 8 bytes; those of x on 16
 };
 cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, int block_rows, int num_sms,
                                    cudaStream_t stream);
@@ -52,7 +51,7 @@ struct LinearParams {
 enum LinearForm : int { kLinearFew = 0, kLinearMany = 1 };
 struct LinearPlan {
   int form;
-  int tile;     // rows of x per tile: kLinearFew 16, 32, 64 or 128; kLinearMany 128, or 256 on CTA pairs
+  int tile;     // rows of x per tile: kLinearFew 16, 32 or 64; kLinearMany 128, or 256 on CTA pairs
   int split;    // kLinearFew: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
   int grid;     // CTAs
 };

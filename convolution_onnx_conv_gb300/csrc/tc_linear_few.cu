@@ -1,7 +1,7 @@
 // Linear layers for few rows per weight matrix (one token up to some hundred rows, or the ragged
 // row groups of experts): y^T = W x^T on tcgen05.
 //
-// The weights are the MMA's 128-row operand and the rows of x its N columns (16 to 128), so a call
+// The weights are the MMA's 128-row operand and the rows of x its N columns (16, 32 or 64), so a call
 // with one row wastes 15 columns of a narrow MMA instead of 127 rows of a wide one, and a ragged
 // group's last tile wastes little.  Such a call is bound by the weights' bytes: each is read once,
 // by TMA, many stages ahead.  When there are fewer tiles than SMs, the CTAs of a cluster share one
@@ -17,7 +17,7 @@
 //   warp 0      TMA: weight and x tiles of each k-block
 //   warp 1      TMEM, MMA issue
 //   warp 2      e4m3: the scale table
-//   warps 4-7   epilogue (4-11 for 64 and 128 columns, each half of them)
+//   warps 4-7   epilogue (4-11 for 64 columns, each half of them)
 #include "linear_dev.cuh"
 
 namespace convf {
@@ -30,7 +30,7 @@ struct FewCfg {
   static constexpr int kCols = TN >= 64 ? TN / 2 : TN;    // columns per epilogue thread
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kWBytes = 128 * kKBlockBytes, kXBytes = TN * kKBlockBytes;
-  static constexpr int kBufs = F8 ? (TN == 128 ? 4 : 8) : 2;   // TMEM accumulators (and table slots)
+  static constexpr int kBufs = F8 ? 8 : 2;   // TMEM accumulators (and table slots)
   static constexpr int kTmemCols = kBufs * TN;
   static constexpr int kTableBytes = F8 ? kBufs * TN * 4 : 0;
   static constexpr int kRedBytes = TN * 128 * 4;               // partial sums of this CTA's columns, by rank
@@ -138,39 +138,49 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, TN) : idesc_bf16_f32(128, TN);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
-      for (long long t = t0; t < tiles; t += tstep) {
-        for (int kb = ka, in_chunk = 0; kb < kb_end; ++kb) {
-          const bool first = F8 || in_chunk == 0;
+    // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
+    // registers, which is where the MMA takes its descriptors from
+    const bool issue = elect_one();
+    constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, TN) : idesc_bf16_f32(128, TN);
+    const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(sW)), b0 = sdesc_kmajor_sw128(smem_u32(sX));
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, bphase = 0;
+    const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;
+    for (long long j = 0; j < mine; ++j) {
+      for (int kb = ka, in_chunk = 0; kb < kb_end; ++kb) {
+        const bool first = F8 || in_chunk == 0;
+        const bool last = F8 || ++in_chunk == p.chunk_kb || kb == kb_end - 1;
+        // both barriers are asked at once, before either is waited for
+        bool ready = mbar_test_wait(&full[stage], phase);
+        if (first) ready = mbar_test_wait(&tempty[buf], bphase ^ 1) & ready;
+        if (!ready) {
           if (first && !mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) goto teardown;
           if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-          tc_fence_after();
-          const uint64_t a = sdesc_kmajor_sw128(smem_u32(sW + stage * Cfg::kWBytes));
-          const uint64_t b = sdesc_kmajor_sw128(smem_u32(sX + stage * Cfg::kXBytes));
-          const uint32_t d = tmem_base + buf * TN;
+        }
+        tc_fence_after();
+        const uint64_t a = a0 + stage * (Cfg::kWBytes >> 4), b = b0 + stage * (Cfg::kXBytes >> 4);
+        const uint32_t d = tmem_base + buf * TN;
+        if (issue) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 32 bytes of k each
-            const uint32_t acc = !first || i > 0;
             if (F8)
-              tc_mma_f8(d, a + 2 * i, b + 2 * i, idesc, acc);
+              tc_mma_f8(d, a + 2 * i, b + 2 * i, idesc, i > 0);
             else
-              tc_mma_bf16(d, a + 2 * i, b + 2 * i, idesc, acc);
+              tc_mma_bf16(d, a + 2 * i, b + 2 * i, idesc, !first || i > 0);
           }
           tc_commit(&empty[stage]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (F8 || ++in_chunk == p.chunk_kb || kb == kb_end - 1) {
-            in_chunk = 0;
-            tc_commit(&tfull[buf]);
-            if (++buf == kBufs) {
-              buf = 0;
-              bphase ^= 1;
-            }
+          if (last) tc_commit(&tfull[buf]);
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (last) {
+          in_chunk = 0;
+          if (++buf == kBufs) {
+            buf = 0;
+            bphase ^= 1;
           }
         }
       }
@@ -364,7 +374,6 @@ cudaError_t launch_linear_few(const LinearParams& p, const LinearPlan& plan, boo
     case 16: return e4m3 ? launch_t<true, 16>(p, plan, tmW, tmX, stream) : launch_t<false, 16>(p, plan, tmW, tmX, stream);
     case 32: return e4m3 ? launch_t<true, 32>(p, plan, tmW, tmX, stream) : launch_t<false, 32>(p, plan, tmW, tmX, stream);
     case 64: return e4m3 ? launch_t<true, 64>(p, plan, tmW, tmX, stream) : launch_t<false, 64>(p, plan, tmW, tmX, stream);
-    case 128: return e4m3 ? launch_t<true, 128>(p, plan, tmW, tmX, stream) : launch_t<false, 128>(p, plan, tmW, tmX, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -374,7 +383,6 @@ int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms) {
     case 16: return e4m3 ? max_clusters_t<true, 16>(split, num_sms) : max_clusters_t<false, 16>(split, num_sms);
     case 32: return e4m3 ? max_clusters_t<true, 32>(split, num_sms) : max_clusters_t<false, 32>(split, num_sms);
     case 64: return e4m3 ? max_clusters_t<true, 64>(split, num_sms) : max_clusters_t<false, 64>(split, num_sms);
-    case 128: return e4m3 ? max_clusters_t<true, 128>(split, num_sms) : max_clusters_t<false, 128>(split, num_sms);
   }
   return 0;
 }

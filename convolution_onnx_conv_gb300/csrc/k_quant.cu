@@ -62,8 +62,6 @@ __device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c
   typedef typename RawOf<T>::type Raw;
   constexpr int kWords = sizeof(Raw) / 4;
   Raw r;
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) r.w[i] = 0;
   if (VEC && c0 + sub * 8 + 8 <= cols) {
     const T* p = row + c0 + sub * 8;
     if (wide) {
@@ -85,6 +83,8 @@ __device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c
     }
   } else {
 #pragma unroll
+    for (int i = 0; i < kWords; ++i) r.w[i] = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = VEC ? c0 + sub * 8 + i : c0 + sub + LANES * i;
       if (c < cols) set(r, i, row + c);
@@ -105,13 +105,23 @@ __device__ __forceinline__ float scale_of(float m) {
 // place, the first correction leaves it within one, and the second then rounds correctly (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  The remainders
 // are exact while nothing is subnormal; a quotient that is, is zero in e4m3 either way.
-__device__ __forceinline__ float quotient(float v, float s, float r) {
-  float t = v * r;
-  t = fmaf(fmaf(-t, s, v), r, t);
-  return fmaf(fmaf(-t, s, v), r, t);
+// Two values at a time (packed multiply-adds).
+__device__ __forceinline__ float2 quotients(float v0, float v1, float s, float r) {
+  float2 t;
+  asm("{\n\t.reg .b64 v, r, s, t, e;\n\t"
+      "mov.b64 v, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\tmov.b64 s, {%5, %5};\n\t"
+      "mul.rn.f32x2 t, v, r;\n\t"
+      "fma.rn.f32x2 e, t, s, v;\n\t"
+      "fma.rn.f32x2 t, e, r, t;\n\t"
+      "fma.rn.f32x2 e, t, s, v;\n\t"
+      "fma.rn.f32x2 t, e, r, t;\n\t"
+      "mov.b64 {%0, %1}, t;\n\t}"
+      : "=f"(t.x), "=f"(t.y)
+      : "f"(v0), "f"(v1), "f"(r), "f"(-s));
+  return t;
 }
 
-// 1 / s for quotient(), or 0 where a remainder could be subnormal or s is no number
+// 1 / s for quotients(), or 0 where a remainder could be subnormal or s is no number
 __device__ __forceinline__ float reciprocal_of(float s) { return s > 0x1p-60f && s < 0x1p60f ? __frcp_rn(s) : 0.f; }
 
 // the same columns of a row of q
@@ -121,7 +131,11 @@ __device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int co
   float t[8];
   if (r != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = quotient(v[i], s, r);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 q = quotients(v[i], v[i + 1], s, r);
+      t[i] = q.x;
+      t[i + 1] = q.y;
+    }
   } else {
     // s == 0: a block of zeros (or one whose scale underflowed): zeros, not 0 / 0
 #pragma unroll
@@ -148,7 +162,7 @@ __device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int co
 __device__ __forceinline__ float max8(const float (&v)[8]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+  for (int i = 0; i < 8; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
   return m;
 }
 
@@ -166,24 +180,34 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
   int b = static_cast<int>(first - r * p.nblk);
   const long long dr = step / p.nblk;
   const int db = static_cast<int>(step - dr * p.nblk);
+  auto advance = [&] {
+    r += dr;
+    b += db;
+    if (b >= p.nblk) {
+      b -= p.nblk;
+      ++r;
+    }
+  };
+  auto source = [&] { return r >= p.rows ? -1 : p.index ? __ldg(p.index + r) : static_cast<int>(r); };
   Raw raw[2], up[2];
-  auto fetch = [&] {
-    int src = -1;
-    if (r < p.rows) src = p.index ? __ldg(p.index + r) : static_cast<int>(r);
+  auto fetch = [&](int src, int fb) {
     const bool there = src >= 0 && src < p.x_rows;
     const T* row = static_cast<const T*>(p.x) + static_cast<long long>(there ? src : 0) * p.ldx;
     const int cols = there ? p.cols : 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      raw[h] = load_lane<VEC, 8>(row, b * kScaleBlock + 64 * h, sub, cols, p.wide);
-      if (GATED) up[h] = load_lane<VEC, 8>(row + p.cols, b * kScaleBlock + 64 * h, sub, cols, p.wide);
+      raw[h] = load_lane<VEC, 8>(row, fb * kScaleBlock + 64 * h, sub, cols, p.wide);
+      if (GATED) up[h] = load_lane<VEC, 8>(row + p.cols, fb * kScaleBlock + 64 * h, sub, cols, p.wide);
     }
   };
-  fetch();
+  // in turn: this block's values are here, the next one's row is known, the one's after it is looked up
+  long long cr = r;
+  int cb = b;
+  fetch(source(), b);
+  advance();
+  int next_src = source();
   // whole warps loop together (the shuffles below name all 32 lanes): the first lane group's row decides
-  while (__shfl_sync(0xFFFFFFFFu, r < p.rows, 0)) {
-    const long long cr = r;
-    const int cb = b;
+  while (__shfl_sync(0xFFFFFFFFu, cr < p.rows, 0)) {
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -195,13 +219,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         for (int i = 0; i < 8; ++i) v[h][i] = __fdividef(v[h][i], 1.f + expf(-v[h][i])) * u[i];   // within 2 ulp
       }
     }
-    r += dr;
-    b += db;
-    if (b >= p.nblk) {
-      b -= p.nblk;
-      ++r;
-    }
-    fetch();
+    const long long nr = r;
+    const int nb = b;
+    fetch(next_src, nb);
+    advance();
+    next_src = source();
     float m = max_nan(max8(v[0]), max8(v[1]));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -212,6 +234,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
       for (int h = 0; h < 2; ++h)
         store_lane<VEC, 8>(p.q + cr * p.ldq, cb * kScaleBlock + 64 * h, sub, p.cols, v[h], s, rs);
     }
+    cr = nr;
+    cb = nb;
   }
 }
 

@@ -334,16 +334,24 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   // fp32 results of bf16 operands: the MMA's own accumulator truncates (1.2e-6 of the result at K =
   // 1000, against 3e-7 when every 256 values are added in registers); bf16 results cannot tell
   p.chunk_kb = e4m3 ? 1 : osz == 2 ? p.num_kb : 4;
-  p.vec_y = aligned(a->y, 32) && a->ldy * osz % 32 == 0 ? 2 : aligned(a->y, 16) && a->ldy * osz % 16 == 0 ? 1 : 0;
+  p.vec_y = aligned(a->y, 16) && a->ldy * osz % 16 == 0;
   p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;
   p.clamp = l->lo != -INFINITY || l->hi != INFINITY;
+  CUtensorMap tmY = tmX;   // (not used without vec_y)
+  if (plan.form == kLinearMany && p.vec_y) {
+    const cuuint64_t ysize[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(a->rows)};
+    const cuuint64_t ystride = a->ldy * osz;
+    st = encode_map(&tmY, osz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                    static_cast<int>(osz), 2, a->y, ysize, &ystride, 32, "y");
+    if (st != CONVF_OK) return st;
+  }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
   const cudaError_t e = plan.form == kLinearFew
                             ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
                             : launch_linear_many(p, plan, e4m3, plan.tile != 256 ? l->tmW256 : e4m3 ? l->tmW64 : l->tmW128,
-                                                 tmX, strm);
+                                                 tmX, tmY, strm);
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "linear launch failed: %s", cudaGetErrorString(e));
   return record_ok();
 }

@@ -106,18 +106,20 @@ __device__ __forceinline__ RowGroup row_group(const LinearParams& p, int e) {
   return RowGroup{a, b};
 }
 
-// Tiles of `tile` rows over the experts: prefix[e] = row tiles of the experts before e.  One warp;
-// block_lead tells the CTA that reports offsets that decrease or pass the rows.
+// Tiles of `tile` rows over the experts: prefix[i] = row tiles of the experts before the i-th pair of them
+// (a prefix for each expert would not leave the room that the stages need).  One warp; block_lead tells
+// the CTA that reports offsets that decrease or pass the rows.
+__device__ __forceinline__ int expert_pairs(const LinearParams& p) { return (p.experts + 1) >> 1; }
 __device__ __forceinline__ void build_schedule(const LinearParams& p, int tile, int* prefix, bool block_lead) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, pairs = expert_pairs(p);
   int sum = 0;
   bool bad = false;
-  for (int base = 0; base < p.experts; base += 32) {
-    const int e = base + lane;
+  for (int base = 0; base < pairs; base += 32) {
+    const int i = base + lane;
     int n = 0;
-    if (e < p.experts) {
+    for (int e = 2 * i; e < min(2 * i + 2, p.experts); ++e) {
       const RowGroup g = row_group(p, e);
-      n = (g.last - g.first + tile - 1) / tile;
+      n += (g.last - g.first + tile - 1) / tile;
       if (block_lead && p.offsets) {
         const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
         bad = bad || a < 0 || b < a || b > p.rows;
@@ -129,24 +131,28 @@ __device__ __forceinline__ void build_schedule(const LinearParams& p, int tile, 
       const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += t;
     }
-    if (e < p.experts) prefix[e] = sum + incl - n;
+    if (i < pairs) prefix[i] = sum + incl - n;
     sum += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  if (lane == 0) prefix[p.experts] = sum;
+  if (lane == 0) prefix[pairs] = sum;
   if (bad) atomicOr(p.status, kStatusOffsets);
 }
+constexpr int kScheduleBytes = (kMaxExperts / 2 + 4) * 4;   // of prefix
 
 // One output tile: `rows` rows of x from row0, weight rows from n0, of an expert.
 struct LinearTile {
   int e, row0, rows, n0;
 };
-// Tile t of prefix[experts] * n_tiles.  Within an expert the row tiles run fastest, in groups of
-// kRasterRows: the CTAs of a wave share weight tiles (each is then read from memory once, and again
-// from L2), and a long prompt's rows are not all passed over once per weight tile.
+__device__ __forceinline__ long long tile_count(const LinearParams& p, const int* prefix) {
+  return static_cast<long long>(prefix[expert_pairs(p)]) * p.n_tiles;
+}
+// Tile t of tile_count.  Within an expert the row tiles run fastest, in groups of kRasterRows: the CTAs
+// of a wave share weight tiles (each is then read from memory once, and again from L2), and a long
+// prompt's rows are not all passed over once per weight tile.
 constexpr int kRasterRows = 8;
 template <int TILE, int NTILE>
 __device__ __forceinline__ LinearTile tile_at(const LinearParams& p, const int* prefix, long long t) {
-  int lo = 0, hi = p.experts;   // the last expert whose tiles start at or before t
+  int lo = 0, hi = expert_pairs(p);   // the last pair whose tiles start at or before t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (static_cast<long long>(prefix[mid]) * p.n_tiles <= t)
@@ -154,15 +160,20 @@ __device__ __forceinline__ LinearTile tile_at(const LinearParams& p, const int* 
     else
       hi = mid;
   }
-  const int mt = prefix[lo + 1] - prefix[lo];
-  const long long local = t - static_cast<long long>(prefix[lo]) * p.n_tiles;
+  long long local = t - static_cast<long long>(prefix[lo]) * p.n_tiles;
+  LinearTile r;
+  r.e = 2 * lo;
+  RowGroup g = row_group(p, r.e);
+  int mt = (g.last - g.first + TILE - 1) / TILE;
+  if (local >= static_cast<long long>(mt) * p.n_tiles) {
+    local -= static_cast<long long>(mt) * p.n_tiles;
+    g = row_group(p, ++r.e);
+    mt = (g.last - g.first + TILE - 1) / TILE;
+  }
   const int group = static_cast<int>(local / (static_cast<long long>(kRasterRows) * p.n_tiles));
   const int in_group = static_cast<int>(local - static_cast<long long>(group) * kRasterRows * p.n_tiles);
   const int height = min(kRasterRows, mt - group * kRasterRows);
   const int nt = in_group / height, m = group * kRasterRows + in_group - nt * height;
-  const RowGroup g = row_group(p, lo);
-  LinearTile r;
-  r.e = lo;
   r.row0 = g.first + m * TILE;
   r.rows = min(TILE, g.last - r.row0);
   r.n0 = nt * NTILE;

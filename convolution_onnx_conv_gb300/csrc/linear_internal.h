@@ -32,7 +32,7 @@ struct LinearParams {
   int rows, N, experts;
   int num_kb;                // k-blocks of 128 bytes
   int chunk_kb;              // k-blocks that an MMA accumulator sums before its sum goes to the registers'
-  int vec_y;                 // y's 16-byte (1) or 32-byte (2) stores are aligned
+  int vec_y;                 // y's rows begin on 16 bytes
   int n_tiles;               // weight-row tiles of the chosen form
   const float* x_scale;
   long long xs_row, xs_blk;
@@ -65,9 +65,9 @@ int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
 
 
 // tmW: boxes of 128 bytes x 256 rows (on CTA pairs x 64 for e4m3, x 128 for bf16);
-// tmX: boxes of 128 bytes x 128 rows.
+// tmX: boxes of 128 bytes x 128 rows; tmY (used where vec_y): {N, rows} of y, boxes of 128 bytes x 32 rows.
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
-                               const CUtensorMap& tmX, cudaStream_t stream);
+                               const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream);
 constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile
 
 }  // namespace convf

@@ -34,9 +34,8 @@ struct FewCfg {
   static constexpr int kTmemCols = kBufs * TN;
   static constexpr int kTableBytes = F8 ? kBufs * TN * 4 : 0;
   static constexpr int kRedBytes = TN * 128 * 4;               // partial sums of this CTA's columns, by rank
-  static constexpr int kSchedBytes = (kMaxExperts + 1) * 4 + 12;
   static constexpr int kBarBytes = 512;
-  static constexpr int kFixed = 1024 + kTableBytes + kRedBytes + kSchedBytes + kBarBytes;
+  static constexpr int kFixed = 1024 + kTableBytes + kRedBytes + kScheduleBytes + kBarBytes;
   // 16 and 32 columns: two CTAs on an SM, so that one's start, exchange and end are behind the
   // other's loads (and a dependent launch's start behind this one's end)
   static constexpr int kPerSm = TN <= 32 ? 2 : 1;
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
   if (warp == 2) build_schedule(p, TN, prefix, blockIdx.x == 0);
   __syncthreads();
 
-  const long long tiles = static_cast<long long>(prefix[p.experts]) * p.n_tiles;
+  const long long tiles = tile_count(p, prefix);
 
   if (warp == 0) {
     if (lane == 0) {

@@ -19,12 +19,15 @@
 //   warps 0-7   epilogue: warp w the rows 32 (w % 4) .. and the columns 128 (w / 4) .. of the CTA's tile
 //   warp 8      TMA: x and weight tiles of each k-block
 //   warp 9      TMEM, MMA issue (of a pair: the leader's)
-//   (warps 10, 11: none; registers are handed over by warpgroups)
+//   warp 10     works out the CTA's next tiles (the divisions and lookups cost the epilogue 1000 cycles a tile)
+//   (warp 11: none; registers are handed over by warpgroups)
 #include "linear_dev.cuh"
 
 namespace convf {
 
 namespace {
+
+constexpr int kTileBatch = 16;   // tiles that the scheduler works out at a time
 
 template <bool PAIR>
 struct ManyCfg {
@@ -35,12 +38,12 @@ struct ManyCfg {
   static constexpr int kTileM = PAIR ? 256 : 128;
   static constexpr int kXBytes = 128 * kKBlockBytes;
   static constexpr int kWBytes = (PAIR ? 128 : 256) * kKBlockBytes;   // a pair's CTA holds half
-  static constexpr int kStages = PAIR ? 6 : 4;
-  static constexpr int kOutBytes = 1024;   // per epilogue warp: 8 rows of 128 bytes on the way out
+  static constexpr int kStages = PAIR ? 5 : 4;
+  // per epilogue warp on the way out: chunks of 32 rows of 128 bytes (64 bf16 columns, or 32 fp32)
+  static constexpr int kOutChunks = PAIR ? 2 : 1, kOutBytes = 4096 * kOutChunks;
   static constexpr int kBarBytes = 256;
-  static constexpr int kFixed = kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes;
-  static constexpr int kSmem = kFixed + (kMaxExperts + 4) * 4;
-  static_assert((2 * kStages + 8) * 8 + 8 <= kBarBytes, "barriers");
+  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + 8 * kOutBytes + kBarBytes + 2 * kTileBatch * 16 + kScheduleBytes;
+  static_assert((2 * kStages + 12) * 8 + 8 <= kBarBytes, "barriers");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -67,6 +70,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ uint32_t bf16_pair(f32x2 v) {
   const float2 f = split_of(v);
   return bf16_pair(f.x, f.y);
+}
+__device__ __forceinline__ void load_pairs(const float* p, f32x2& a, f32x2& b) {
+  asm volatile("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p));
 }
 __device__ __forceinline__ uint4 unit_of(f32x2 a, f32x2 b) {
   const float2 u = split_of(a), v = split_of(b);
@@ -95,22 +101,10 @@ __device__ __forceinline__ void finish4(const LinearParams& p, long long at, int
         static_cast<float*>(p.y)[at + j] = f[j];
     }
 }
-// 32 bytes: a whole sector at once where they are one
-__device__ __forceinline__ void st_global_32(uint8_t* p, uint4 a, uint4 b, bool sector) {
-  if (!sector) {
-    *reinterpret_cast<uint4*>(p) = a;
-    *reinterpret_cast<uint4*>(p + 16) = b;
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
-               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-
 template <bool F8, bool PAIR>
 __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     linear_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW,
-                       const __grid_constant__ CUtensorMap tmX) {
+                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
   using Cfg = ManyCfg<PAIR>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kElems = F8 ? 128 : 64;
@@ -122,9 +116,12 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 4);
+  uint64_t* tqfull = tempty + 4;    // a batch of tiles is worked out
+  uint64_t* tqempty = tqfull + 2;   // and read by the loads' warp and the epilogue's
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tqempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
+  LinearTile* tileq = reinterpret_cast<LinearTile*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
+  int* prefix = reinterpret_cast<int*>(tileq + 2 * kTileBatch);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -138,6 +135,10 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     for (int b = 0; b < 4; ++b) {   // accumulator b: 128 columns, of half b & 1 of a tile
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], PAIR ? 8 : 4);   // the epilogue warps of a half, of both CTAs
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tqfull[b], 1);
+      mbar_init(&tqempty[b], 9);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -163,8 +164,20 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
   if (warp == 8) build_schedule(p, Cfg::kTileM, prefix, blockIdx.x == 0);
   __syncthreads();
 
-  const long long tiles = static_cast<long long>(prefix[p.experts]) * p.n_tiles;
+  const long long tiles = tile_count(p, prefix);
   const long long t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, tstep = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;   // tiles of this CTA
+  // this CTA's j-th tile, read by one thread (the loads') or a warp in the order of j; false: give up
+  auto next_tile = [&](long long j, LinearTile& q, bool whole_warp) {
+    const int slot = static_cast<int>(j / kTileBatch) & 1, at = static_cast<int>(j % kTileBatch);
+    if (at == 0 && !mbar_wait(&tqfull[slot], static_cast<uint32_t>(j / (2 * kTileBatch)) & 1, abort_flag, p.status)) return false;
+    q = tileq[slot * kTileBatch + at];
+    if (at == kTileBatch - 1) {
+      if (whole_warp) __syncwarp();
+      if (!whole_warp || lane == 0) mbar_arrive(&tqempty[slot]);
+    }
+    return true;
+  };
 
   // every earlier MMA of this thread has completed -> an arrival on `bar`, of a pair in both CTAs
   auto commit_to = [&](uint64_t* bar) {
@@ -178,8 +191,9 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (long long t = t0; t < tiles; t += tstep) {
-        const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
+      for (long long j = 0; j < mine; ++j) {
+        LinearTile q;
+        if (!next_tile(j, q, false)) goto teardown;
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) goto teardown;
           // a pair's loads all complete on the leader's barrier, which expects both CTAs' bytes
@@ -217,7 +231,6 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(sX)), b0 = sdesc_kmajor_sw128(smem_u32(sW));
       int stage = 0, buf = 0;   // buf: 0 or 2, the first accumulator of the k-block
       uint32_t phase = 0, bphase = 0;
-      const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;
       for (long long j = 0; j < mine; ++j) {
         for (int kb = 0, in_chunk = 0; kb < p.num_kb; ++kb) {
           const bool first = F8 || in_chunk == 0;
@@ -269,6 +282,15 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
       }
     }
+  } else if (warp == 10) {
+    for (long long j = 0; j < mine; j += kTileBatch) {
+      const int slot = static_cast<int>(j / kTileBatch) & 1;
+      if (!mbar_wait(&tqempty[slot], (static_cast<uint32_t>(j / (2 * kTileBatch)) & 1) ^ 1, abort_flag, p.status)) goto teardown;
+      if (lane < kTileBatch && j + lane < mine)
+        tileq[slot * kTileBatch + lane] = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t0 + (j + lane) * tstep);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tqfull[slot]);
+    }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
     const int quad = warp & 3, half = warp >> 2;
@@ -277,23 +299,39 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     int buf = half;
     uint32_t bphase = 0;
     bool ready = false;
-    for (long long t = t0; t < tiles; t += tstep) {
-      // the scales are loaded a k-block ahead (and multiplied when they are used: a product at the load
-      // would wait for it); rows and columns past the edge read the last scale there is, and their
-      // sums are not stored
-      const float *xs = nullptr, *ws = nullptr;
-      float x1 = 1.f, w1 = 1.f;
-      if (F8) {
-        const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
-        const int nblk = (p.N + kScaleBlock - 1) / kScaleBlock;
-        xs = p.x_scale + (q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row;
-        ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(q.n0 / kScaleBlock + half, nblk - 1)) * p.num_kb;
-        x1 = __ldg(xs);
-        w1 = __ldg(ws);
-      }
+    // the scales are loaded a k-block ahead (and multiplied when they are used: a product at the load would
+    // wait for it); rows and columns past the edge read the last scale there is, and their sums are not
+    // stored
+    const float *xs = nullptr, *ws = nullptr;
+    float x1 = 1.f, w1 = 1.f;
+    const int nblk = (p.N + kScaleBlock - 1) / kScaleBlock;
+    auto first_scales = [&](const LinearTile& q) {
+      if (!F8) return;
+      xs = p.x_scale + (q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row;
+      ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(q.n0 / kScaleBlock + half, nblk - 1)) * p.num_kb;
+      x1 = __ldg(xs);
+      w1 = __ldg(ws);
+    };
+    LinearTile q, qn;
+    if (mine > 0) {
+      if (!next_tile(0, qn, true)) goto teardown;
+      first_scales(qn);
+    }
+    for (long long j = 0; j < mine; ++j) {
+      q = qn;
+      const int n0 = q.n0 + half * 128;   // this warp's first column
+      const float* bias = p.bias ? p.bias + static_cast<long long>(q.e) * p.N : nullptr;
       f32x2 acc[64];
+      // sums begin with the bias where it can be read as pairs of 16 bytes; else it is added at the end
+      const bool bias_first = bias && n0 + 128 <= p.N && (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
+      if (bias_first) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = 0;
+        for (int c = 0; c < 64; c += 2) load_pairs(bias + n0 + 2 * c, acc[c], acc[c + 1]);
+        bias = nullptr;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) acc[c] = 0;
+      }
 #pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += F8 ? 1 : p.chunk_kb) {
         if (!ready && !mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
@@ -327,38 +365,81 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) fma2(acc[32 + i], r[i], s);
       }
-      const LinearTile q = tile_at<Cfg::kTileM, kManyCols>(p, prefix, t);
-      const int n0 = q.n0 + half * 128;   // this warp's first column
+      if (j + 1 < mine) {
+        if (!next_tile(j + 1, qn, true)) goto teardown;
+        first_scales(qn);
+      }
       if (mrow >= q.rows || n0 >= p.N) continue;
-      const float* bias = p.bias ? p.bias + static_cast<long long>(q.e) * p.N : nullptr;
-      if (!bias && !p.clamp && p.vec_y && n0 + 128 <= p.N) {
-        // a thread's row, in whole 32-byte sectors where rows begin on them
+      uint8_t* out = sOut + warp * Cfg::kOutBytes;
+      // Rows of 16-byte units leave by TMA (which clips the columns past N) while the next tile's sums
+      // begin: the stores of all SMs at once, waited for, cost 4700 cycles a tile.  Only operations on
+      // whole pairs here: arithmetic on the registers' own halves has the compiler keep the halves of
+      // every pair apart, and the multiply-adds of the loop above then cost two each (800 instead of 650
+      // cycles per k-block).  So bf16 results are clamped after the rounding, which is monotonic: the
+      // bounds, rounded, give the same values.
+      const bool pairs_do = p.vec_y && !bias && (p.out_bf16 || !p.clamp);
+      const uint32_t lo = bf16_pair(p.lo, p.lo), hi = bf16_pair(p.hi, p.hi);
+      auto bf16_unit = [&](int u) {   // 8 columns
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = bf16_pair(acc[4 * u + i]);
+          if (p.clamp) asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %2;" : "+r"(w[i]) : "r"(lo), "r"(hi));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      if (pairs_do && mrow + 32 <= q.rows) {
+        auto chunk_unit = [&](int c, int u) {
+          return reinterpret_cast<uint4*>(out + (c % Cfg::kOutChunks) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4));
+        };
+        auto room = [&] {   // the chunk's place has been read by the store before
+          if (lane == 0) bulk_wait_read<Cfg::kOutChunks - 1>();
+          __syncwarp();
+        };
+        auto send = [&](int c, int n) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n < p.N) tma_store_2d(&tmY, out + (c % Cfg::kOutChunks) * 4096, n, q.row0 + mrow);
+            bulk_commit();
+          }
+        };
+        if (p.out_bf16) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            room();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) *chunk_unit(c, u) = bf16_unit(8 * c + u);
+            send(c, n0 + 64 * c);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            room();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) *chunk_unit(c, u) = unit_of(acc[16 * c + 2 * u], acc[16 * c + 2 * u + 1]);
+            send(c, n0 + 32 * c);
+          }
+        }
+      } else if (pairs_do && n0 + 128 <= p.N) {
+        // a group's last rows: each lane its own row
         if (mrow + lane < q.rows) {
           const long long at = static_cast<long long>(q.row0 + mrow + lane) * p.ldy + n0;
-          const bool sector = p.vec_y == 2;
           if (p.out_bf16) {
-            uint8_t* row = static_cast<uint8_t*>(p.y) + at * 2;
+            uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_global_32(row + 32 * u,
-                           make_uint4(bf16_pair(acc[8 * u]), bf16_pair(acc[8 * u + 1]), bf16_pair(acc[8 * u + 2]),
-                                      bf16_pair(acc[8 * u + 3])),
-                           make_uint4(bf16_pair(acc[8 * u + 4]), bf16_pair(acc[8 * u + 5]), bf16_pair(acc[8 * u + 6]),
-                                      bf16_pair(acc[8 * u + 7])),
-                           sector);
+            for (int u = 0; u < 16; ++u) row[u] = bf16_unit(u);
           } else {
-            uint8_t* row = static_cast<uint8_t*>(p.y) + at * 4;
+            uint4* row = reinterpret_cast<uint4*>(static_cast<float*>(p.y) + at);
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-              st_global_32(row + 32 * u, unit_of(acc[4 * u], acc[4 * u + 1]), unit_of(acc[4 * u + 2], acc[4 * u + 3]), sector);
+            for (int u = 0; u < 32; ++u) row[u] = unit_of(acc[2 * u], acc[2 * u + 1]);
           }
         }
       } else {
-        // A bias, a clamp, unaligned rows or the ragged edge of N: 8 rows of 32 columns at a time through
-        // shared memory, where a lane then has 4 columns of 2 rows.  (Arithmetic on the registers' own
-        // halves has the compiler keep the halves of every pair apart: the multiply-adds of the loop
-        // above then cost two each, 800 instead of 650 cycles per k-block.)
-        uint8_t* out = sOut + warp * Cfg::kOutBytes;
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        // Unaligned rows or bias, the ragged edge of N, clamped fp32: 8 rows of 32 columns at a time through
+        // shared memory, where a lane then has 4 columns of 2 rows.
         const int rows = min(32, q.rows - mrow);
         const int c4 = (lane & 7) * 4;
 #pragma unroll
@@ -387,6 +468,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_all();   // the stores have been written before the CTA ends
   }
 
 teardown:
@@ -409,7 +491,7 @@ teardown:
 
 template <bool F8, bool PAIR>
 cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                     cudaStream_t stream) {
+                     const CUtensorMap& tmY, cudaStream_t stream) {
   using Cfg = ManyCfg<PAIR>;
   static bool configured = false;
   if (!configured) {
@@ -423,16 +505,16 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
     configured = true;
   }
   return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
-                    tmW, tmX);
+                    tmW, tmX, tmY);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
-                               const CUtensorMap& tmX, cudaStream_t stream) {
+                               const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream) {
   if (plan.tile == 256)
-    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, stream) : launch_t<false, true>(p, plan, tmW, tmX, stream);
-  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, stream) : launch_t<false, false>(p, plan, tmW, tmX, stream);
+    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, true>(p, plan, tmW, tmX, tmY, stream);
+  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, false>(p, plan, tmW, tmX, tmY, stream);
 }
 
 }  // namespace convf

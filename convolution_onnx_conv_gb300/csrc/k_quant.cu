@@ -239,54 +239,60 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
   }
 }
 
-// Scales per 128 x 128 block: a CTA takes one at a time, 8 rows of 8 elements per thread, held in
-// registers between the maximum and the division; the next block is on its way meanwhile.
+// Scales per 128 x 128 block: a CTA of 512 threads takes one at a time, 4 rows of 8 elements per thread,
+// held in registers between the maximum and the division; the next block is on its way meanwhile.  (256
+// threads of 8 rows need 120 registers, 16 warps on an SM: 19.0 us for 5000 x 4100 bf16 instead of 18.2.)
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;
+  constexpr int kRows = 4, kWarps = 16;
   pdl_launch_dependents();
   pdl_wait_prior();
-  __shared__ float part[2][8];
-  const long long items = static_cast<long long>((p.rows + kScaleBlock - 1) / kScaleBlock) * p.nblk;
+  __shared__ float part[2][kWarps];
+  const int items = (p.rows + kScaleBlock - 1) / kScaleBlock;   // blocks of rows, times p.nblk
   const int sub = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-  Raw raw[8];
-  auto fetch = [&](long long item) {
-    const int rb = static_cast<int>(item / p.nblk);
-    const int cb = static_cast<int>(item - static_cast<long long>(rb) * p.nblk);
+  Raw raw[kRows];
+  // this CTA's block (rb, cb) and its step: divisions once, not per block
+  int rb = static_cast<int>(blockIdx.x / p.nblk), cb = static_cast<int>(blockIdx.x - static_cast<unsigned>(rb) * p.nblk);
+  const int dr = static_cast<int>(gridDim.x / p.nblk), dc = static_cast<int>(gridDim.x - static_cast<unsigned>(dr) * p.nblk);
+  auto fetch = [&] {
     const long long at = static_cast<long long>(rb) * kScaleBlock + row0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      raw[i] = load_lane<VEC, 16>(static_cast<const T*>(p.x) + (at + 16 * i) * p.ldx, cb * kScaleBlock, sub,
-                              item < items && at + 16 * i < p.rows ? p.cols : 0, p.wide);
+    for (int i = 0; i < kRows; ++i)
+      raw[i] = load_lane<VEC, 16>(static_cast<const T*>(p.x) + (at + 32 * i) * p.ldx, cb * kScaleBlock, sub,
+                                  rb < items && at + 32 * i < p.rows ? p.cols : 0, p.wide);
   };
-  fetch(blockIdx.x);
-  int turn = 0;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
-    const int rb = static_cast<int>(item / p.nblk);
-    const int cb = static_cast<int>(item - static_cast<long long>(rb) * p.nblk);
-    const int rows = min(p.rows - rb * kScaleBlock, kScaleBlock);
-    const long long first = static_cast<long long>(rb) * kScaleBlock + row0;
-    float v[8][8];
+  fetch();
+  for (int turn = 0; rb < items; turn ^= 1) {
+    const int rows = min(p.rows - rb * kScaleBlock, kScaleBlock), c0 = cb * kScaleBlock;
+    const long long first = static_cast<long long>(rb) * kScaleBlock + row0, scale_at = rb * p.lds + cb;
+    float v[kRows][8];
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       raw[i].floats(v[i]);
       m = max_nan(m, max8(v[i]));
     }
-    if (sizeof(Raw) == 16) fetch(item + gridDim.x);   // (fp32 has no registers for it)
+    rb += dr;
+    cb += dc;
+    if (cb >= p.nblk) {
+      cb -= p.nblk;
+      ++rb;
+    }
+    if (sizeof(Raw) == 16) fetch();   // (fp32 has no registers for it)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     // two sets of partial maxima in turn: a warp may be a block ahead of one still reading
     if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, part[turn][i]);
+    for (int i = 0; i < kWarps; ++i) m = max_nan(m, part[turn][i]);
     const float s = scale_of(m), rs = reciprocal_of(s);
-    if (threadIdx.x == 0) p.scale[rb * p.lds + cb] = s;
+    if (threadIdx.x == 0) p.scale[scale_at] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row0 + 16 * i < rows) store_lane<VEC, 16>(p.q + (first + 16 * i) * p.ldq, cb * kScaleBlock, sub, p.cols, v[i], s, rs);
-    if (sizeof(Raw) != 16) fetch(item + gridDim.x);
+    for (int i = 0; i < kRows; ++i)
+      if (row0 + 32 * i < rows) store_lane<VEC, 16>(p.q + (first + 32 * i) * p.ldq, c0, sub, p.cols, v[i], s, rs);
+    if (sizeof(Raw) != 16) fetch();
   }
 }
 
@@ -303,7 +309,7 @@ cudaError_t launch_t(const QuantParams& p, bool gated, int block_rows, int num_s
   if (block_rows != 1) {
     const long long ctas = static_cast<long long>((p.rows + kScaleBlock - 1) / kScaleBlock) * p.nblk;
     const long long cap = static_cast<long long>(num_sms) * 2;   // resident
-    return launch_pdl(quantize_tiles_kernel<T, VEC>, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0,
+    return launch_pdl(quantize_tiles_kernel<T, VEC>, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(512), 0,
                       stream, 1, p);
   }
   return gated ? launch_rows<T, true, VEC>(p, num_sms, stream) : launch_rows<T, false, VEC>(p, num_sms, stream);

@@ -412,3 +412,70 @@ def test_refusals_on_tensors():
         cf.quantize_blocks(x, index=off, block_rows=128)
     with pytest.raises(cf.ConvFusedError):
         cf.quantize_blocks(x, block_rows=64)
+
+
+# ------------------------------------------------------------------------------ every kernel form
+
+FORMS = ["few_rows tile=16x128 split=1", "few_rows tile=16x128 split=4", "few_rows tile=32x128 split=1",
+         "few_rows tile=64x128 split=1", "many_rows tile=128x256", "many_rows tile=256x256"]
+SEARCH = [(r, e, n, k) for e in (1, 3, 9, 33) for k in (1040, 2064, 130, 4112) for n in (1032, 2061, 4100)
+          for r in (1, 9, 30, 61, 130, 300, 530, 1061, 2100, 4333)]
+
+
+def layer_of_form(form, e4m3, dtype):
+    """(layer, rows, experts, n, k) of the first size whose plan is `form`."""
+    for r, e, n, k in SEARCH:
+        w = torch.zeros((e, n, -(-k // 16) * 16), dtype=dtype, device="cuda")[:, :, :k]
+        ws = torch.zeros((e, -(-n // 128), -(-k // 128)), device="cuda") if e4m3 else None
+        for out_bf16 in (True, False):
+            lin = cf.ExpertLinear(w, ws, out_bf16=out_bf16)
+            if form in lin.describe(r):
+                return lin, r, e, n, k
+            lin.close()
+    pytest.fail(f"no size of the search runs {form}")
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_every_form_is_exact_on_integers(form, e4m3):
+    """Integers whose sums are exact: each form at ragged sizes, with its own bias, clamp and row stride."""
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    lin, rows, e, n, k = layer_of_form(form, e4m3, dtype)
+    g = gen(rows + n)
+    x = torch.randint(-4, 5, (rows, k), generator=g, device="cuda").float()
+    w = torch.randint(-2, 3, (e, n, k), generator=g, device="cuda").float()
+    kb = -(-k // 128)
+    xs = 2.0 ** torch.randint(-1, 2, (rows, kb), generator=g, device="cuda").float() if e4m3 else None
+    ws = 2.0 ** torch.randint(-1, 2, (e, -(-n // 128), kb), generator=g, device="cuda").float() if e4m3 else None
+    bias = torch.randint(-3, 4, (e, n), generator=g, device="cuda").float()
+    cuts = [rows * (i + 1) // e for i in range(e - 1)]
+    off = torch.tensor([0] + cuts + [rows], dtype=torch.int32, device="cuda")
+    rx, rw = real64(x, w, xs, ws)
+    ref = torch.empty((rows, n), dtype=torch.float64, device="cuda")
+    for i in range(e):
+        a, b = int(off[i]), int(off[i + 1])
+        ref[a:b] = rx[a:b] @ rw[i].T
+    x16, w16 = rows16(x.to(dtype)), rows16(w.to(dtype))
+    for out_bf16 in (False, True):
+        out = torch.bfloat16 if out_bf16 else torch.float32
+        for b, act, clip in ((None, cf.CONVF_ACT_NONE, (0, 0)), (bias, cf.CONVF_ACT_NONE, (0, 0)),
+                             (None, cf.CONVF_ACT_CLIP, (-3.0, 5.5)), (bias, cf.CONVF_ACT_RELU, (0, 0))):
+            want = ref.clone()
+            if b is not None:
+                for i in range(e):
+                    want[int(off[i]):int(off[i + 1])] += b[i].double()
+            if act == cf.CONVF_ACT_RELU:
+                want = want.clamp(min=0)
+            elif act == cf.CONVF_ACT_CLIP:
+                want = want.clamp(*clip)
+            layer = cf.ExpertLinear(w16, ws, bias=b, act=act, clip=clip, out_bf16=out_bf16)
+            for pad, shift in ((0, 0), (8, 0), (1, 1)):   # rows of y side by side, 16-byte aligned apart, and unaligned
+                buf = torch.full((rows * (n + pad) + 8,), -7.0, dtype=out, device="cuda")
+                y = torch.as_strided(buf, (rows, n), (n + pad, 1), shift)
+                layer(x16, off, xs, y=y)
+                assert torch.equal(y.double(), want.to(out).double()), (out_bf16, b is not None, act, pad)
+                y.fill_(-7.0)
+                assert bool((buf == -7).all())   # nothing beside y
+            layer.close()
+    torch.cuda.synchronize()
+    lin.close()

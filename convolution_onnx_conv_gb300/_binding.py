@@ -662,14 +662,21 @@ class ConvChain:
             pass
 
 
-def _stream_of(t, stream):
-    """cudaStream_t of `stream` (a torch stream or an int), else the current stream of t's device."""
-    import torch
-    if stream is None:
+class _Torch:
+    """Names of torch that every call uses (the package imports torch only where it is used)."""
+    ready = False
+
+    @classmethod
+    def bind(cls):
+        import torch
+        cls.bf16, cls.f32, cls.e4m3, cls.i32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+        cls.empty, cls.empty_strided = torch.empty, torch.empty_strided
         # the public call builds a Stream object (2 us of a 10 us call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        cls.stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+        cls.quantize = load_library().conv_fused_quantize_blocks
+        cls.run = load_library().conv_fused_linear_run
+        cls.ready = True
 
 
 def _rows_2d(t, name):
@@ -694,12 +701,15 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     ``gated=True`` takes x as [rows][2*cols] and quantises g / (1 + exp(-g)) * u of its halves g and
     u.  Rows of q lie a multiple of 16 bytes apart, as the layers read them; ``q`` and ``scale`` may
     be given.  Runs on the current torch stream."""
-    import torch
+    T = _Torch
+    if not T.ready:
+        T.bind()
     rows, cols, ldx = _rows_2d(x, "x")
     xr = rows
-    if x.dtype is torch.bfloat16:
+    kind = x.dtype
+    if kind is T.bf16:
         kind = CONVF_OUT_BF16
-    elif x.dtype is torch.float32:
+    elif kind is T.f32:
         kind = CONVF_OUT_F32
     else:
         raise ValueError("x must be bf16 or fp32")
@@ -709,27 +719,33 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
         cols //= 2
     where = None
     if index is not None:
-        if not index.is_cuda or index.dtype is not torch.int32 or index.dim() != 1 or not index.is_contiguous():
+        if not index.is_cuda or index.dtype is not T.i32 or index.dim() != 1 or not index.is_contiguous():
             raise ValueError("index must be a contiguous int32 CUDA vector")
         rows, where = index.shape[0], index.data_ptr()
-    nblk, srows = -(-cols // 128), rows if block_rows == 1 else -(-rows // 128)
+    nblk = (cols + 127) // 128
+    srows = rows if block_rows == 1 else (rows + 127) // 128
+    device = x.device
     if q is None:
-        ldq = -(-cols // 16) * 16
-        q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.float8_e4m3fn, device=x.device)
+        ldq = (cols + 15) // 16 * 16
+        q = T.empty((rows, cols), dtype=T.e4m3, device=device) if ldq == cols else \
+            T.empty_strided((rows, cols), (ldq, 1), dtype=T.e4m3, device=device)
     else:
         qr, qc, ldq = _rows_2d(q, "q")
-        if q.dtype is not torch.float8_e4m3fn or qr != rows or qc != cols:
+        if q.dtype is not T.e4m3 or qr != rows or qc != cols:
             raise ValueError(f"q must be float8_e4m3fn of shape ({rows}, {cols})")
     if scale is None:
         lds = nblk
-        scale = torch.empty((srows, nblk), dtype=torch.float32, device=x.device)
+        scale = T.empty((srows, nblk), dtype=T.f32, device=device)
     else:
         sr, sc, lds = _rows_2d(scale, "scale")
-        if scale.dtype is not torch.float32 or sr != srows or sc != nblk:
+        if scale.dtype is not T.f32 or sr != srows or sc != nblk:
             raise ValueError(f"scale must be float32 of shape ({srows}, {nblk})")
-    a = QuantArgs(rows, cols, x.data_ptr(), kind, xr, ldx, where, 1 if gated else 0, block_rows, q.data_ptr(), ldq,
-                  scale.data_ptr(), lds)
-    st = (_LIB or load_library()).conv_fused_quantize_blocks(ctypes.byref(a), _stream_of(x, stream))
+    if stream is None:
+        stream = T.stream(x.get_device())
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = T.quantize(ctypes.byref(QuantArgs(rows, cols, x.data_ptr(), kind, xr, ldx, where, 1 if gated else 0, block_rows,
+                                           q.data_ptr(), ldq, scale.data_ptr(), lds)), stream)
     if st != CONVF_OK:
         _check(st)
     return q, scale
@@ -769,19 +785,20 @@ class ExpertLinear:
                        w.stride(1) if N > 1 else max(w.stride(1), -(-K // 16) * 16), w.stride(0), act, float(clip[0]), float(clip[1]),
                        CONVF_OUT_BF16 if out_bf16 else CONVF_OUT_F32)
         self.handle = conv_fused_linear_create(d, w, w_scale, bias)
+        if not _Torch.ready:
+            _Torch.bind()
 
     def _run(self, x, offsets, x_scale, y, stream):
-        import torch
         rows, K, ldx = _rows_2d(x, "x")
         if K != self.K:
             raise ValueError(f"x must have {self.K} columns")
         if x.dtype is not self.dtype:
             raise ValueError(f"x must be {self.dtype}")
         if rows <= 1:
-            ldx = -(-ldx // 16) * 16
+            ldx = (ldx + 15) // 16 * 16
         xs = xs_row = xs_blk = 0
         if self.e4m3:
-            if x_scale is None or not x_scale.is_cuda or x_scale.dtype is not torch.float32 \
+            if x_scale is None or not x_scale.is_cuda or x_scale.dtype is not _Torch.f32 \
                     or x_scale.shape != (rows, self.kblk):
                 raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows, self.kblk)}")
             xs = x_scale.data_ptr()
@@ -789,14 +806,17 @@ class ExpertLinear:
         elif x_scale is not None:
             raise ValueError("x_scale goes with float8_e4m3fn layers only")
         if y is None:
-            y, ldy = torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device), self.N
+            y, ldy = _Torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device), self.N
         else:
             yr, yc, ldy = _rows_2d(y, "y")
             if y.dtype is not self.out_dtype or yr != rows or yc != self.N:
                 raise ValueError(f"y must be {self.out_dtype} of shape ({rows}, {self.N})")
-        a = LinearArgs(rows, x.data_ptr(), ldx, xs, xs_row, xs_blk, None if offsets is None else offsets.data_ptr(),
-                       y.data_ptr(), ldy)
-        st = _LIB.conv_fused_linear_run(self.handle, ctypes.byref(a), _stream_of(x, stream))
+        if stream is None:
+            stream = _Torch.stream(x.get_device())
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
+        st = _Torch.run(self.handle, ctypes.byref(LinearArgs(rows, x.data_ptr(), ldx, xs, xs_row, xs_blk, offsets,
+                                                             y.data_ptr(), ldy)), stream)
         if st != CONVF_OK:
             _check(st)
         return y
@@ -805,11 +825,10 @@ class ExpertLinear:
         """y [rows][N] for ``x`` [rows][K] (w's type; rows a multiple of 16 bytes apart), ``offsets``
         int32 CUDA [experts+1] and, for e4m3, ``x_scale`` fp32 [rows][ceil(K/128)] (any strides).
         Rows that no expert takes are not written."""
-        import torch
-        if not offsets.is_cuda or offsets.dtype is not torch.int32 or offsets.shape != (self.experts + 1,) \
+        if not offsets.is_cuda or offsets.dtype is not _Torch.i32 or offsets.shape != (self.experts + 1,) \
                 or not offsets.is_contiguous():
             raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {self.experts + 1}")
-        return self._run(x, offsets, x_scale, y, stream)
+        return self._run(x, offsets.data_ptr(), x_scale, y, stream)
 
     def describe(self, rows: int) -> str:
         return conv_fused_linear_describe(self.handle, rows)

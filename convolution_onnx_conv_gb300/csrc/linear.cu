@@ -148,7 +148,7 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   for (int tile = 16; tile <= 64; tile *= 2) {
     // with two CTAs on an SM (16 and 32 columns), and alone
     const long long shared = tile == 16 ? (e4m3 ? 330 : 240) : (e4m3 ? 480 : 280);
-    const long long alone = tile == 16 ? (e4m3 ? 220 : 160) : tile == 32 ? (e4m3 ? 240 : 180) : (e4m3 ? 430 : 245);
+    const long long alone = tile == 16 ? (e4m3 ? 230 : 160) : tile == 32 ? (e4m3 ? 330 : 200) : (e4m3 ? 430 : 245);
     for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
       const long long tiles = row_tiles(tile) * nt;
       const int units = few_clusters(dev, num_sms, e4m3, tile, split);
@@ -158,8 +158,8 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
             split == 1 ? 700 : 1000 + 500 * split + 75 * tile);
     }
   }
-  offer(kLinearMany, 128, 1, num_sms, nt_many, e4m3 ? 440 : 375, 2000);
-  if (num_sms >= 2) offer(kLinearMany, 256, 1, num_sms / 2, nt_many, e4m3 ? 420 : 280, 2000);
+  offer(kLinearMany, 128, 1, num_sms, nt_many, e4m3 ? 420 : 360, 1800);
+  if (num_sms >= 2) offer(kLinearMany, 256, 1, num_sms / 2, nt_many, e4m3 ? 390 : 290, 1800);
   return plan;
 }
 

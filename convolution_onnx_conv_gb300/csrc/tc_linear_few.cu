@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
       const float bias = p.bias && n < p.N ? __ldg(p.bias + static_cast<long long>(q.e) * p.N + n) : 0.f;
       auto put = [&](int c, float v) {
         v = act_clamp(v + bias, p.lo, p.hi);
+        if (!CONVF_IN_BOUNDS(q.row0 + c < p.rows && n < p.N, p.status)) return;
         const long long at = static_cast<long long>(q.row0 + c) * p.ldy + n;
         if (p.out_bf16)
           static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);

@@ -21,6 +21,8 @@
 //   warp 9      TMEM, MMA issue (of a pair: the leader's)
 //   warp 10     works out the CTA's next tiles (the divisions and lookups cost the epilogue 1000 cycles a tile)
 //   (warp 11: none; registers are handed over by warpgroups)
+#include <type_traits>
+
 #include "linear_dev.cuh"
 
 namespace convf {
@@ -74,6 +76,18 @@ __device__ __forceinline__ uint32_t bf16_pair(f32x2 v) {
 __device__ __forceinline__ void load_pairs(const float* p, f32x2& a, f32x2& b) {
   asm volatile("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p));
 }
+// the first `left` of a 16-byte unit's PER elements
+template <int PER, typename E>
+__device__ __forceinline__ void store_unit(E* to, uint4 v, int left) {
+  if (left >= PER) {
+    *reinterpret_cast<uint4*>(to) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (j < left) to[j] = PER == 8 ? static_cast<E>(w[j >> 1] >> (16 * (j & 1))) : static_cast<E>(w[j & 3]);
+  }
+}
 __device__ __forceinline__ uint4 unit_of(f32x2 a, f32x2 b) {
   const float2 u = split_of(a), v = split_of(b);
   return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
@@ -101,7 +115,11 @@ __device__ __forceinline__ void finish4(const LinearParams& p, long long at, int
         static_cast<float*>(p.y)[at + j] = f[j];
     }
 }
-template <bool F8, bool PAIR>
+// PLAIN: rows of y begin on 16 bytes, and nothing is done to the sums but a bias that can be read as 16
+// bytes and the clamp of bf16 results.  The other cases have a kernel of their own:
+// their code's registers had the compiler keep the halves of the sums' pairs apart, and every multiply-
+// add of the loop then cost two (800 instead of 600 cycles per k-block).
+template <bool F8, bool PAIR, bool PLAIN>
 __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
     linear_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
@@ -322,15 +340,12 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       const int n0 = q.n0 + half * 128;   // this warp's first column
       const float* bias = p.bias ? p.bias + static_cast<long long>(q.e) * p.N : nullptr;
       f32x2 acc[64];
-      // sums begin with the bias where it can be read as pairs of 16 bytes; else it is added at the end
-      const bool bias_first = bias && n0 + 128 <= p.N && (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
-      if (bias_first) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) load_pairs(bias + n0 + 2 * c, acc[c], acc[c + 1]);
-        bias = nullptr;
-      } else {
+      for (int c = 0; c < 64; ++c) acc[c] = 0;
+      if (PLAIN && bias) {   // the sums begin with it
 #pragma unroll
-        for (int c = 0; c < 64; ++c) acc[c] = 0;
+        for (int c = 0; c < 64; c += 2)
+          if (n0 + 2 * c < p.N) load_pairs(bias + n0 + 2 * c, acc[c], acc[c + 1]);
       }
 #pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += F8 ? 1 : p.chunk_kb) {
@@ -371,13 +386,10 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       }
       if (mrow >= q.rows || n0 >= p.N) continue;
       uint8_t* out = sOut + warp * Cfg::kOutBytes;
-      // Rows of 16-byte units leave by TMA (which clips the columns past N) while the next tile's sums
-      // begin: the stores of all SMs at once, waited for, cost 4700 cycles a tile.  Only operations on
-      // whole pairs here: arithmetic on the registers' own halves has the compiler keep the halves of
-      // every pair apart, and the multiply-adds of the loop above then cost two each (800 instead of 650
-      // cycles per k-block).  So bf16 results are clamped after the rounding, which is monotonic: the
-      // bounds, rounded, give the same values.
-      const bool pairs_do = p.vec_y && !bias && (p.out_bf16 || !p.clamp);
+      // Whole warps' rows leave by TMA (which clips the columns past N) while the next tile's sums begin:
+      // the stores of all SMs at once, waited for, cost 4700 cycles a tile.  bf16 results are clamped after
+      // the rounding, which is monotonic: the bounds, rounded, give the same values, and the sums' pairs
+      // stay whole.
       const uint32_t lo = bf16_pair(p.lo, p.lo), hi = bf16_pair(p.hi, p.hi);
       auto bf16_unit = [&](int u) {   // 8 columns
         uint32_t w[4];
@@ -388,7 +400,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
       };
-      if (pairs_do && mrow + 32 <= q.rows) {
+      if (PLAIN && mrow + 32 <= q.rows) {
         auto chunk_unit = [&](int c, int u) {
           return reinterpret_cast<uint4*>(out + (c % Cfg::kOutChunks) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4));
         };
@@ -421,47 +433,103 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
             send(c, n0 + 32 * c);
           }
         }
-      } else if (pairs_do && n0 + 128 <= p.N) {
+      } else if (PLAIN) {
         // a group's last rows: each lane its own row
-        if (mrow + lane < q.rows) {
+        if (mrow + lane < q.rows && CONVF_IN_BOUNDS(q.row0 + mrow + lane < p.rows, p.status)) {
           const long long at = static_cast<long long>(q.row0 + mrow + lane) * p.ldy + n0;
           if (p.out_bf16) {
-            uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at);
+            uint16_t* row = static_cast<uint16_t*>(p.y) + at;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) row[u] = bf16_unit(u);
+            for (int u = 0; u < 16; ++u) store_unit<8>(row + 8 * u, bf16_unit(u), p.N - n0 - 8 * u);
           } else {
-            uint4* row = reinterpret_cast<uint4*>(static_cast<float*>(p.y) + at);
+            uint32_t* row = static_cast<uint32_t*>(p.y) + at;
 #pragma unroll
-            for (int u = 0; u < 32; ++u) row[u] = unit_of(acc[2 * u], acc[2 * u + 1]);
+            for (int u = 0; u < 32; ++u) store_unit<4>(row + 4 * u, unit_of(acc[2 * u], acc[2 * u + 1]), p.N - n0 - 4 * u);
           }
         }
       } else {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        // Unaligned rows or bias, the ragged edge of N, clamped fp32: 8 rows of 32 columns at a time through
-        // shared memory, where a lane then has 4 columns of 2 rows.
+        // Unaligned rows or bias, the ragged edge of N, clamped fp32: 64 columns at a time through shared
+        // memory (16-byte units swizzled by row).  A part of a sector that is written costs L2 more than a
+        // whole one, so a store's lanes are adjacent columns of one row: aligned rows 4 a lane; other bf16
+        // rows 2 a lane from the row's first even address; other fp32 rows one.
+        constexpr int kRound = Cfg::kOutBytes / 256;   // rows staged at a time
         const int rows = min(32, q.rows - mrow);
-        const int c4 = (lane & 7) * 4;
+        const long long row0 = static_cast<long long>(q.row0 + mrow) * p.ldy;
 #pragma unroll
-        for (int pass = 0; pass < 4; ++pass) {
-          const int n = n0 + 32 * pass + c4;
-          float b[4];
+        for (int pass = 0; pass < 2; ++pass) {
+          const int n = n0 + 64 * pass;
+          float b[4];   // of the lane's columns: 4 from 4 (lane % 16), or 3 from 2 lane, or lane and lane + 32
 #pragma unroll
-          for (int j = 0; j < 4; ++j) b[j] = bias ? __ldg(bias + min(n + j, p.N - 1)) : 0.f;
-          for (int r0 = 0; r0 < rows; r0 += 8) {
-            if ((lane & ~7) == r0) {
+          for (int i = 0; i < 4; ++i) {
+            const int c = p.vec_y ? 4 * (lane & 15) + i : p.out_bf16 ? 2 * lane + i : lane + 32 * i;
+            b[i] = bias ? __ldg(bias + min(n + c, p.N - 1)) : 0.f;
+          }
+          for (int r0 = 0; r0 < rows; r0 += kRound) {
+            if ((lane & ~(kRound - 1)) == r0) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(out + (lane & 7) * 128 + ((u ^ (lane & 7)) << 4)) =
-                    unit_of(acc[16 * pass + 2 * u], acc[16 * pass + 2 * u + 1]);
+              for (int u = 0; u < 16; ++u)
+                *reinterpret_cast<uint4*>(out + (lane & (kRound - 1)) * 256 + ((u ^ (lane & 7)) << 4)) =
+                    unit_of(acc[32 * pass + 2 * u], acc[32 * pass + 2 * u + 1]);
             }
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = (lane >> 3) + 4 * i;
-              const float4 v = *reinterpret_cast<const float4*>(out + r * 128 + (((lane & 7) ^ r) << 4));
-              if (r0 + r < rows && n < p.N)
-                finish4(p, static_cast<long long>(q.row0 + mrow + r0 + r) * p.ldy + n, n, v, b);
+            const int some = min(kRound, rows - r0);
+            auto staged = [&](int r, int c) {
+              return *reinterpret_cast<const float*>(out + r * 256 + (((c >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+            };
+            // AS_IS: all 64 columns, nothing to add or clamp
+            auto send_rows = [&](auto as_is) {
+              constexpr bool AS_IS = decltype(as_is)::value;
+              auto done = [&](float v, float bias_c) {
+                if (AS_IS) return v;
+                v += bias_c;
+                return p.clamp ? act_clamp(v, p.lo, p.hi) : v;
+              };
+              const int left = AS_IS ? 64 : p.N - n;   // columns of the row from n
+              const long long at = row0 + r0 * p.ldy + n;
+              if (p.out_bf16) {
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.y) + at;
+#pragma unroll 4
+                for (int r = 0; r < some; ++r, to += p.ldy) {
+                  if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
+                    const float2 v = *reinterpret_cast<const float2*>(out + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
+                    if (2 * lane + 1 < left)
+                      *reinterpret_cast<uint32_t*>(to + 2 * lane) = bf16_pair(done(v.x, b[0]), done(v.y, b[1]));
+                    else if (2 * lane < left)
+                      to[2 * lane] = __float2bfloat16_rn(done(v.x, b[0]));
+                  } else {
+                    // an even address is at column 1: pairs from there, and the first and last column alone
+                    const int c = 2 * lane + 1;
+                    const float v0 = done(staged(r, c), b[1]), v1 = done(staged(r, min(c + 1, 63)), b[2]);
+                    if (c + 1 < min(left, 64))
+                      *reinterpret_cast<uint32_t*>(to + c) = bf16_pair(v0, v1);
+                    else if (c < left)
+                      to[c] = __float2bfloat16_rn(v0);
+                    if (lane == 0 && left > 0) to[0] = __float2bfloat16_rn(done(staged(r, 0), b[0]));
+                  }
+                }
+              } else {
+                float* to = static_cast<float*>(p.y) + at;
+#pragma unroll 4
+                for (int r = 0; r < some; ++r, to += p.ldy) {
+                  if (lane < left) to[lane] = done(staged(r, lane), b[0]);
+                  if (lane + 32 < left) to[lane + 32] = done(staged(r, lane + 32), b[1]);
+                }
+              }
+            };
+            if (p.vec_y) {
+              const int n4 = n + 4 * (lane & 15);
+#pragma unroll 4
+              for (int r = lane >> 4; r < some; r += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(out + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
+                if (n4 < p.N && CONVF_IN_BOUNDS(q.row0 + mrow + r0 + r < p.rows, p.status))
+                  finish4(p, row0 + (r0 + r) * p.ldy + n4, n4, v, b);
+              }
+            } else if (!bias && !p.clamp && n + 64 <= p.N) {
+              send_rows(std::true_type{});
+            } else {
+              send_rows(std::false_type{});
             }
             __syncwarp();
           }
@@ -489,7 +557,7 @@ teardown:
   }
 }
 
-template <bool F8, bool PAIR>
+template <bool F8, bool PAIR, bool PLAIN>
 cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
                      const CUtensorMap& tmY, cudaStream_t stream) {
   using Cfg = ManyCfg<PAIR>;
@@ -497,14 +565,14 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
   if (!configured) {
     // the register split waits for ever if the kernel was given fewer registers than it shares out
     cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR>);
+    cudaError_t e = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR, PLAIN>);
     if (e == cudaSuccess && at.numRegs < Cfg::kRegs) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     configured = true;
   }
-  return launch_pdl(linear_many_kernel<F8, PAIR>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
+  return launch_pdl(linear_many_kernel<F8, PAIR, PLAIN>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
                     tmW, tmX, tmY);
 }
 
@@ -512,9 +580,17 @@ cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtens
 
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
                                const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream) {
-  if (plan.tile == 256)
-    return e4m3 ? launch_t<true, true>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, true>(p, plan, tmW, tmX, tmY, stream);
-  return e4m3 ? launch_t<true, false>(p, plan, tmW, tmX, tmY, stream) : launch_t<false, false>(p, plan, tmW, tmX, tmY, stream);
+  // (16-byte bias loads: every expert's bias begins on 16 bytes)
+  const bool bias_ok = !p.bias || ((reinterpret_cast<uintptr_t>(p.bias) & 15) == 0 && p.N % 4 == 0);
+  const bool plain = p.vec_y && bias_ok && (p.out_bf16 || !p.clamp);
+  auto go = [&](auto f8, auto pair) {
+    constexpr bool F8 = decltype(f8)::value, PAIR = decltype(pair)::value;
+    return plain ? launch_t<F8, PAIR, true>(p, plan, tmW, tmX, tmY, stream) : launch_t<F8, PAIR, false>(p, plan, tmW, tmX, tmY, stream);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if (plan.tile == 256) return e4m3 ? go(yes, yes) : go(no, yes);
+  return e4m3 ? go(yes, no) : go(no, no);
 }
 
 }  // namespace convf

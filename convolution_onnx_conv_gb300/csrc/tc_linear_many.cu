@@ -10,11 +10,13 @@
 // e4m3: a k-block's sums have to leave TMEM to be scaled, so the epilogue works all the time.  TMEM
 // holds a ring of four accumulators of 128 columns; the MMAs of a 128-value k-block fill one for each
 // half of the tile's columns, and the epilogue adds it, times x_scale * w_scale, to fp32 sums in
-// registers, as packed multiply-adds.  An accumulator has 768 cycles for the way from its last MMA over
-// the reads back to its next MMA before the tensor cores wait; sixteen warps of 64 columns each have
-// read theirs after two loads (eight warps of 128 columns took 720 cycles per k-block, and two
-// accumulators of 256 columns 1080).  bf16: an accumulator of 256 columns sums LinearParams::chunk_kb
-// k-blocks.
+// registers, as packed multiply-adds: 128 columns per thread.  An accumulator has 768 cycles for the way
+// from its last MMA over the reads back to its next MMA before the tensor cores wait.  The MMAs take 512
+// cycles per k-block, this takes 600 to 650 (tensor pipe 62% busy at 4096 x 4096 x 4096, tile ends
+// included); two accumulators of 256 columns took 1080, sixteen epilogue warps of 64 columns 900.  What
+// bounds it now is that way's latency, and, for long, the power limit: 8192 x 8192 x 8192 takes 357 us
+// (3.1 PFLOP/s) in a short run and 420 us (2.6) in a long one.  bf16: an accumulator of 256 columns sums
+// LinearParams::chunk_kb k-blocks, 512 cycles each for 64 values.
 //
 //   warps 0-7   epilogue: warp w the rows 32 (w % 4) .. and the columns 128 (w / 4) .. of the CTA's tile
 //   warp 8      TMA: x and weight tiles of each k-block

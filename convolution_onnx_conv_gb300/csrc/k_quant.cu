@@ -86,10 +86,12 @@ __device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c
   } else {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) r.w[i] = 0;
+    if (!VEC || c0 + sub * 8 < cols) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = VEC ? c0 + sub * 8 + i : c0 + sub + LANES * i;
-      if (c < cols) set(r, i, row + c);
+      for (int i = 0; i < 8; ++i) {
+        const int c = VEC ? c0 + sub * 8 + i : c0 + sub + LANES * i;
+        if (c < cols) set(r, i, row + c);
+      }
     }
   }
   return r;
@@ -149,10 +151,8 @@ __device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int co
   const uint2 o = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
   if (VEC) {
     const int c = c0 + sub * 8;
-    if (c + 8 <= cols) {
-      *reinterpret_cast<uint2*>(row + c) = o;
-      return;
-    }
+    if (c + 8 <= cols) *reinterpret_cast<uint2*>(row + c) = o;
+    if (c + 8 <= cols || c >= cols) return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -171,7 +171,7 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
 // Scales per row: 8 lanes take a block, 16 values each, and load the next before they work on this one.
 // (16 lanes of 8 values spend 3 more instructions per value on the maximum, the scale and addresses.)
 template <typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;
   pdl_launch_dependents();
   pdl_wait_prior();

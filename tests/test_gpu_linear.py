@@ -6,16 +6,12 @@ sum of n terms in float32, each step off by at most 2^-23 of what it adds up (tr
 is off by at most n 2^-23 S with S the sum of the terms' magnitudes; e4m3 sums take 128 terms, then
 the blocks, two scales and a bias, bf16 sums K terms and a bias.  A bf16 result (8 significant
 bits) is rounded once, to nearest: 2^-8 of its magnitude more.  Integer cases, whose every sum is exact, have to be equal."""
-import os
-import sys
-
 import pytest
 import torch
 
 import convolution_onnx_conv_gb300 as cf
 
 pytestmark = pytest.mark.gpu
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = 2.0 ** -23
 
 
@@ -412,6 +408,16 @@ def test_refusals_on_tensors():
         cf.quantize_blocks(x, index=off, block_rows=128)
     with pytest.raises(cf.ConvFusedError):
         cf.quantize_blocks(x, block_rows=64)
+
+
+def test_create_reports_an_injected_device_allocation_failure():
+    w = torch.zeros((32, 64), dtype=torch.bfloat16, device="cuda")
+    cf.conv_fused_debug_fail_alloc(2)   # the layer, then its device words
+    with pytest.raises(cf.ConvFusedError) as e:
+        cf.BlockLinear(w)
+    assert e.value.status == cf.CONVF_ERR_OOM and "(injected)" in str(e.value)
+    x = torch.ones((3, 64), dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(cf.BlockLinear(w)(x), torch.zeros((3, 32), device="cuda"))
 
 
 # ------------------------------------------------------------------------------ every kernel form

@@ -670,13 +670,18 @@ class _Torch:
     def bind(cls):
         import torch
         cls.bf16, cls.f32, cls.e4m3, cls.i32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
-        cls.empty, cls.empty_strided = torch.empty, torch.empty_strided
+        cls.empty, cls.empty_strided, cls.cuda = torch.empty, torch.empty_strided, torch.cuda
         # the public call builds a Stream object (2 us of a 10 us call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         cls.stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
         cls.quantize = load_library().conv_fused_quantize_blocks
         cls.run = load_library().conv_fused_linear_run
         cls.ready = True
+
+    @classmethod
+    def on(cls, stream, device):
+        """Context in which torch allocates for `stream` (a torch stream or a cudaStream_t)."""
+        return cls.cuda.stream(stream if hasattr(stream, "cuda_stream") else cls.cuda.ExternalStream(stream, device))
 
 
 def _rows_2d(t, name):
@@ -700,10 +705,14 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     ``index`` (int32, CUDA) takes the rows x[index] instead (an entry outside x gives a row of zeros);
     ``gated=True`` takes x as [rows][2*cols] and quantises g / (1 + exp(-g)) * u of its halves g and
     u.  Rows of q lie a multiple of 16 bytes apart, as the layers read them; ``q`` and ``scale`` may
-    be given.  Runs on the current torch stream."""
+    be given.  Runs on the current torch stream, or on ``stream`` (a torch stream or a cudaStream_t)."""
     T = _Torch
     if not T.ready:
         T.bind()
+    if stream is not None and (q is None or scale is None):
+        # outputs belong to the stream that writes them
+        with T.on(stream, x.device):
+            return quantize_blocks(x, index, gated, block_rows, q, scale)
     rows, cols, ldx = _rows_2d(x, "x")
     xr = rows
     kind = x.dtype
@@ -789,6 +798,9 @@ class ExpertLinear:
             _Torch.bind()
 
     def _run(self, x, offsets, x_scale, y, stream):
+        if stream is not None and y is None:
+            with _Torch.on(stream, x.device):   # y belongs to the stream that writes it
+                return self._run(x, offsets, x_scale, None, None)
         rows, K, ldx = _rows_2d(x, "x")
         if K != self.K:
             raise ValueError(f"x must have {self.K} columns")

@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
                 __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.y) + at;
 #pragma unroll 4
                 for (int r = 0; r < some; ++r, to += p.ldy) {
+                  if (!CONVF_IN_BOUNDS(q.row0 + mrow + r0 + r < p.rows, p.status)) continue;
                   if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
                     const float2 v = *reinterpret_cast<const float2*>(out + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
                     if (2 * lane + 1 < left)
@@ -515,6 +516,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
                 float* to = static_cast<float*>(p.y) + at;
 #pragma unroll 4
                 for (int r = 0; r < some; ++r, to += p.ldy) {
+                  if (!CONVF_IN_BOUNDS(q.row0 + mrow + r0 + r < p.rows, p.status)) continue;
                   if (lane < left) to[lane] = done(staged(r, lane), b[0]);
                   if (lane + 32 < left) to[lane + 32] = done(staged(r, lane + 32), b[1]);
                 }

@@ -330,6 +330,13 @@ def test_other_stream_and_graph():
         lin(x2, off, xs, y=y)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, want)
+    for stream in (side, side.cuda_stream):   # given: it writes outputs of its own
+        side.wait_stream(torch.cuda.current_stream())
+        z = lin(x, off, xs, stream=stream)
+        a, b = cf.quantize_blocks(z, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        c, d = cf.quantize_blocks(want)
+        assert torch.equal(z, want) and torch.equal(a.view(torch.uint8), c.view(torch.uint8)) and torch.equal(b, d)
     src = torch.randn((70, 640), generator=g, device="cuda").to(torch.bfloat16)
     q = torch.empty((70, 640), dtype=torch.float8_e4m3fn, device="cuda")
     s = torch.empty((70, 5), device="cuda")
@@ -482,6 +489,7 @@ def test_every_form_is_exact_on_integers(form, e4m3):
                 assert torch.equal(y.double(), want.to(out).double()), (out_bf16, b is not None, act, pad)
                 y.fill_(-7.0)
                 assert bool((buf == -7).all())   # nothing beside y
+            assert layer.status() == cf.CONVF_OK, cf.conv_fused_last_error()
             layer.close()
     torch.cuda.synchronize()
     lin.close()

@@ -7,7 +7,7 @@
 // kernel execute 34 instructions per value and bound it by those; here the block's scale has its
 // reciprocal taken once, and each value a product and two corrections by its exact remainder, 16
 // instructions per value in all.  100352 x 256 fp32: 21.5 us, 6.0 TB/s; bf16, with half the bytes per
-// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 19.5 us.
+// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 19.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
 
 // Scales per 128 x 128 block: a CTA of 512 threads takes one at a time, 4 rows of 8 elements per thread,
 // held in registers between the maximum and the division; the next block is on its way meanwhile.  (256
-// threads of 8 rows need 120 registers, 16 warps on an SM: 19.0 us for 5000 x 4100 bf16 instead of 18.2.)
+// threads of 8 rows need 120 registers, 16 warps on an SM: 1 us more of 18 for 5000 x 4100 bf16.)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;

@@ -681,7 +681,10 @@ class _Torch:
     @classmethod
     def on(cls, stream, device):
         """Context in which torch allocates for `stream` (a torch stream or a cudaStream_t)."""
-        return cls.cuda.stream(stream if hasattr(stream, "cuda_stream") else cls.cuda.ExternalStream(stream, device))
+        if not hasattr(stream, "cuda_stream"):
+            # (torch takes an external stream 0 for a new one)
+            stream = cls.cuda.ExternalStream(stream, device) if stream else cls.cuda.default_stream(device)
+        return cls.cuda.stream(stream)
 
 
 def _rows_2d(t, name):
@@ -709,7 +712,7 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     T = _Torch
     if not T.ready:
         T.bind()
-    if stream is not None and (q is None or scale is None):
+    if stream is not None and x.is_cuda and (q is None or scale is None):
         # outputs belong to the stream that writes them
         with T.on(stream, x.device):
             return quantize_blocks(x, index, gated, block_rows, q, scale)
@@ -798,7 +801,7 @@ class ExpertLinear:
             _Torch.bind()
 
     def _run(self, x, offsets, x_scale, y, stream):
-        if stream is not None and y is None:
+        if stream is not None and x.is_cuda and y is None:
             with _Torch.on(stream, x.device):   # y belongs to the stream that writes it
                 return self._run(x, offsets, x_scale, None, None)
         rows, K, ldx = _rows_2d(x, "x")

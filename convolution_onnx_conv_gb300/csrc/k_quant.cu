@@ -161,6 +161,15 @@ __device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int co
   }
 }
 
+// g / (1 + exp(-g)), for negative g as g exp(g) / (1 + exp(g)): the divisor stays within [1, 2], where the
+// approximate reciprocal is within an ulp (one of more than 2^126 is zero, which g = -88 would come to)
+__device__ __forceinline__ float gate(float g) {
+  const float e = expf(-fabsf(g));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (g >= 0.f ? g : g * e) * r;
+}
+
 __device__ __forceinline__ float max8(const float (&v)[8]) {
   float m = 0.f;
 #pragma unroll
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
         float u[8];
         up[h].floats(u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[h][i] = __fdividef(v[h][i], 1.f + expf(-v[h][i])) * u[i];   // within 2 ulp
+        for (int i = 0; i < 8; ++i) v[h][i] = gate(v[h][i]) * u[i];
       }
     }
     const long long nr = r;

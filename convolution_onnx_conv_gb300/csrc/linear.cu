@@ -32,6 +32,9 @@ bool overlap(const void* a, unsigned long long an, const void* b, unsigned long 
   return an && bn && x < y + bn && y < x + an;
 }
 
+// whether `rows` rows `ld` elements apart pass the address space (their products then pass 64 bits)
+bool too_far(long long rows, long long ld, int esz) { return ld > ((1LL << 48) / esz) / (rows > 1 ? rows : 1); }
+
 // SMs of the current device (looked up once per device), or an error
 convf_status current_device(int* dev, int* num_sms) {
   static int sms[kMaxDevices];   // 0 = not looked up; every writer stores the same value
@@ -72,6 +75,8 @@ convf_status check_linear(const convf_linear* l) {
 convf_status check_linear_desc(const convf_linear_desc* d) {
   if (!d) return record_error(CONVF_ERR_INVALID_ARG, "desc is NULL");
   if (d->N < 1 || d->K < 1) return record_error(CONVF_ERR_INVALID_ARG, "N=%d and K=%d must be >= 1", d->N, d->K);
+  if (d->N > kMaxExtent || d->K > kMaxExtent)
+    return record_error(CONVF_ERR_UNSUPPORTED, "N=%d, K=%d: at most %d are served", d->N, d->K, kMaxExtent);
   if (d->experts < 1) return record_error(CONVF_ERR_INVALID_ARG, "experts=%d must be >= 1", d->experts);
   if (d->experts > kMaxExperts)
     return record_error(CONVF_ERR_UNSUPPORTED, "experts=%d: at most %d are served", d->experts, kMaxExperts);
@@ -79,11 +84,14 @@ convf_status check_linear_desc(const convf_linear_desc* d) {
     return record_error(CONVF_ERR_INVALID_ARG, "dtype=%d is not CONVF_LINEAR_BF16 or CONVF_LINEAR_E4M3", d->dtype);
   const long long esz = d->dtype == CONVF_LINEAR_E4M3 ? 1 : 2;
   if (d->ldw < d->K) return record_error(CONVF_ERR_INVALID_ARG, "ldw=%lld is less than K=%d", d->ldw, d->K);
+  if (too_far(d->N, d->ldw, 2)) return record_error(CONVF_ERR_INVALID_ARG, "ldw=%lld: W passes the address space", d->ldw);
   if (d->ldw * esz % 16)
     return record_error(CONVF_ERR_UNSUPPORTED, "ldw=%lld: weight rows must be a multiple of 16 bytes apart", d->ldw);
   if (d->experts > 1) {
     if (d->expert_stride < (d->N - 1LL) * d->ldw + d->K)
       return record_error(CONVF_ERR_INVALID_ARG, "expert_stride=%lld: the experts' weights overlap", d->expert_stride);
+    if (too_far(d->experts, d->expert_stride, 2))
+      return record_error(CONVF_ERR_INVALID_ARG, "expert_stride=%lld: W passes the address space", d->expert_stride);
     if (d->expert_stride * esz % 16)
       return record_error(CONVF_ERR_UNSUPPORTED, "expert_stride=%lld: experts must be a multiple of 16 bytes apart",
                           d->expert_stride);
@@ -187,6 +195,8 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   if (!a) return record_error(CONVF_ERR_INVALID_ARG, "args is NULL");
   if (a->rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", a->rows);
   if (a->cols < 1) return record_error(CONVF_ERR_INVALID_ARG, "cols=%d must be >= 1", a->cols);
+  if (a->rows > kMaxExtent || a->cols > kMaxExtent)
+    return record_error(CONVF_ERR_UNSUPPORTED, "rows=%d, cols=%d: at most %d are served", a->rows, a->cols, kMaxExtent);
   if (a->x_rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "x_rows=%d must be >= 0", a->x_rows);
   if (a->x_dtype != CONVF_OUT_F32 && a->x_dtype != CONVF_OUT_BF16)
     return record_error(CONVF_ERR_INVALID_ARG, "x_dtype=%d is not CONVF_OUT_F32 or CONVF_OUT_BF16", a->x_dtype);
@@ -202,6 +212,9 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   if (a->ldx < wide) return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld is less than the row's %lld", a->ldx, wide);
   if (a->ldq < a->cols) return record_error(CONVF_ERR_INVALID_ARG, "ldq=%lld is less than cols=%d", a->ldq, a->cols);
   if (a->lds < nblk) return record_error(CONVF_ERR_INVALID_ARG, "lds=%lld is less than the row's %d scales", a->lds, nblk);
+  if (too_far(a->x_rows, a->ldx, 4) || too_far(a->rows, a->ldq, 1) || too_far(a->rows, a->lds, 4))
+    return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld, ldq=%lld, lds=%lld: the rows pass the address space", a->ldx,
+                        a->ldq, a->lds);
   if (a->rows == 0) return record_ok();
   if (!a->q || !a->scale || (!a->x && a->x_rows > 0)) return record_error(CONVF_ERR_INVALID_ARG, "x, q or scale is NULL");
   const int esz = a->x_dtype == CONVF_OUT_BF16 ? 2 : 4;
@@ -301,6 +314,10 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
   const long long esz = e4m3 ? 1 : 2, osz = d.out_dtype == CONVF_OUT_BF16 ? 2 : 4;
   if (a->rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", a->rows);
+  if (a->rows > kMaxExtent) return record_error(CONVF_ERR_UNSUPPORTED, "rows=%d: at most %d are served", a->rows, kMaxExtent);
+  if (too_far(a->rows, a->ldx, 2) || too_far(a->rows, a->ldy, 4) || too_far(a->rows, a->xs_row, 4) || too_far(d.K, a->xs_blk, 4))
+    return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld, ldy=%lld, x_scale strides (%lld, %lld): the rows pass the address space",
+                        a->ldx, a->ldy, a->xs_row, a->xs_blk);
   if (a->ldx < d.K) return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld is less than K=%d", a->ldx, d.K);
   if (a->ldx * esz % 16)
     return record_error(CONVF_ERR_UNSUPPORTED, "ldx=%lld: rows of x must be a multiple of 16 bytes apart", a->ldx);

@@ -10,6 +10,7 @@ namespace convf {
 constexpr int kStatusOffsets = 4;
 constexpr int kScaleBlock = 128;    // columns (and weight rows) that share a scale
 constexpr float kE4m3Max = 448.0f;
+constexpr int kMaxExtent = 0x7FFFFF00;   // rows, columns, N and K: the last tile's end is still an int
 constexpr int kMaxExperts = 1024;   // the tile schedule keeps a prefix of them in shared memory
 constexpr int kKBlockBytes = 128;   // bytes of a k-block's operand row: 128 e4m3 or 64 bf16 values
 

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import convolution_onnx_conv_gb300 as cf
+from convolution_onnx_conv_gb300 import _binding
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -23
@@ -134,6 +135,22 @@ def test_quantise_gated(rows, cols, dtype):
     back = q.double() * spread(s, cols)
     half = torch.maximum(v.abs() * 2.0 ** -4, spread(s, cols) * 2.0 ** -10)
     assert bool(((back - v).abs() <= half * (1 + 2.0 ** -10) + 16 * U * v.abs() + 2.0 ** -149).all())
+
+
+def test_quantise_gated_where_the_gate_is_almost_shut():
+    # exp(-g) between 2^126 and 2^128; the other factor makes normal numbers of the products
+    x = torch.empty((4, 256), device="cuda")
+    x[:, :128] = torch.linspace(-88.6, -87.4, 512, device="cuda").view(4, 128)
+    x[:, 128:] = 1e30
+    q, s = cf.quantize_blocks(x, gated=True)
+    g, u = x.double().chunk(2, 1)
+    v = g / (1 + torch.exp(-g)) * u
+    _, rs = quantised_64(v)
+    # exp(g) is held in steps of 2^-149, at least 2^21 of them; its 2 ulp, and a few roundings
+    assert bool(((s.double() - rs).abs() <= 2.0 ** -19 * rs).all())
+    back = q.double() * spread(s, 128)
+    half = torch.maximum(v.abs() * 2.0 ** -4, spread(s, 128) * 2.0 ** -10)
+    assert bool(((back - v).abs() <= half * (1 + 2.0 ** -10) + 2.0 ** -19 * v.abs()).all())
 
 
 @pytest.mark.parametrize("block_rows", [1, 128])
@@ -313,6 +330,20 @@ def test_bad_offsets_are_reported_and_reach_nothing_else():
     y = lin(x, torch.tensor([0, 10, 20, 30, 64], dtype=torch.int32, device="cuda"), xs)
     torch.cuda.synchronize()
     assert lin.status() == cf.CONVF_OK and bool(y.isfinite().all())
+
+
+def test_stream_0_is_the_default_stream(monkeypatch):
+    x, w, xs, ws = layer_inputs(gen(3), 5, 1, 64, 256, True)
+    lin = cf.BlockLinear(w[0], ws[0])
+    names, seen = _binding._Torch, []
+    run, quantize = names.run, names.quantize
+    monkeypatch.setattr(names, "run", lambda layer, args, stream: seen.append(stream) or run(layer, args, stream))
+    monkeypatch.setattr(names, "quantize", lambda args, stream: seen.append(stream) or quantize(args, stream))
+    with torch.cuda.stream(torch.cuda.Stream()):
+        y = lin(x, xs, stream=0)
+        cf.quantize_blocks(y, stream=0)
+    torch.cuda.synchronize()
+    assert seen == [0, 0] and torch.equal(y, lin(x, xs))
 
 
 def test_other_stream_and_graph():

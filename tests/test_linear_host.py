@@ -31,6 +31,10 @@ def quant(**kw):
     (dict(x_rows=-2), cf.CONVF_ERR_INVALID_ARG, "x_rows=-2"),
     (dict(x_rows=5), cf.CONVF_ERR_INVALID_ARG, "x_rows=5"),
     (dict(x_dtype=2), cf.CONVF_ERR_INVALID_ARG, "x_dtype=2"),
+    (dict(cols=2 ** 31 - 200), cf.CONVF_ERR_UNSUPPORTED, "cols=2147483448"),
+    (dict(rows=2 ** 31 - 1), cf.CONVF_ERR_UNSUPPORTED, "rows=2147483647"),
+    (dict(ldx=2 ** 62), cf.CONVF_ERR_INVALID_ARG, "address space"),
+    (dict(rows=2 ** 30, x_rows=2 ** 30, ldq=2 ** 40), cf.CONVF_ERR_INVALID_ARG, "address space"),
     (dict(gated=2), cf.CONVF_ERR_INVALID_ARG, "gated=2"),
     (dict(block_rows=64), cf.CONVF_ERR_INVALID_ARG, "block_rows=64"),
     (dict(block_rows=128, index=4 * P), cf.CONVF_ERR_UNSUPPORTED, "block_rows = 1"),
@@ -68,6 +72,10 @@ def linear(**kw):
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(N=0), cf.CONVF_ERR_INVALID_ARG, "N=0"),
     (dict(K=0), cf.CONVF_ERR_INVALID_ARG, "K=0"),
+    (dict(N=2 ** 31 - 255), cf.CONVF_ERR_UNSUPPORTED, "N=2147483393"),
+    (dict(K=2 ** 31 - 1, ldw=2 ** 31), cf.CONVF_ERR_UNSUPPORTED, "K=2147483647"),
+    (dict(ldw=2 ** 61), cf.CONVF_ERR_INVALID_ARG, "address space"),
+    (dict(expert_stride=2 ** 61), cf.CONVF_ERR_INVALID_ARG, "address space"),
     (dict(experts=0), cf.CONVF_ERR_INVALID_ARG, "experts=0"),
     (dict(experts=1025), cf.CONVF_ERR_UNSUPPORTED, "experts=1025"),
     (dict(dtype=2), cf.CONVF_ERR_INVALID_ARG, "dtype=2"),

@@ -7,7 +7,7 @@
 // kernel execute 34 instructions per value and bound it by those; here the block's scale has its
 // reciprocal taken once, and each value a product and two corrections by its exact remainder, 16
 // instructions per value in all.  100352 x 256 fp32: 21.5 us, 6.0 TB/s; bf16, with half the bytes per
-// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 19.4 us.
+// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 19.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -5,9 +5,9 @@
 //
 // The definition's quotient is the float32 one, rounded again to e4m3.  A division per value made the
 // kernel execute 34 instructions per value and bound it by those; here the block's scale has its
-// reciprocal taken once, and each value a product and two corrections by its exact remainder, 16
-// instructions per value in all.  100352 x 256 fp32: 21.5 us, 6.0 TB/s; bf16, with half the bytes per
-// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 19.3 us.
+// reciprocal taken once, and each value a product and one correction by its remainder, 13
+// instructions per value in all.  100352 x 256 fp32: 21.2 us, 6.1 TB/s; bf16, with half the bytes per
+// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 18.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -97,18 +97,27 @@ __device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c
   return r;
 }
 
-// m / 448, rounded to nearest: m * (1/448) in two parts (Brisebarre, Muller and Raina, "Accelerating
-// correctly rounded floating-point division when the divisor is known in advance", 2004); equal to the
-// quotient for every one of the 2^23 fractions where nothing is subnormal
-__device__ __forceinline__ float scale_of(float m) {
-  if (m > 0x1p-60f && m < 0x1p100f) return fmaf(m, 0x1.24924ap-9f, m * -0x1.b6db6ep-34f);
-  return m / kE4m3Max;
+// A block's scale s = m / 448, rounded to nearest, and r = 1 / s for quotients(), or 0 where a remainder
+// could be subnormal or s is no number.  m / 448 is m * (1/448) in two parts (Brisebarre, Muller and Raina,
+// "Accelerating correctly rounded floating-point division when the divisor is known in advance", 2004);
+// equal to the quotient for every one of the 2^23 fractions where nothing is subnormal.
+struct BlockScale {
+  float s, r;
+};
+__device__ __forceinline__ BlockScale scale_of(float m) {
+  if (m > 0x1p-50f && m < 0x1p60f) {
+    const float s = fmaf(m, 0x1.24924ap-9f, m * -0x1.b6db6ep-34f);
+    return BlockScale{s, __frcp_rn(s)};
+  }
+  return BlockScale{m / kE4m3Max, 0.f};
 }
 
-// v / s, rounded to nearest, given r = 1 / s rounded to nearest: v r is within 1.5 units in the last
-// place, the first correction leaves it within one, and the second then rounds correctly (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  The remainders
-// are exact while nothing is subnormal; a quotient that is, is zero in e4m3 either way.
+// v / s given r = 1 / s rounded to nearest: v r is within 1.5 units in the last place, and the correction
+// by its remainder (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) is, before its rounding, within 2^-46 of the quotient.  So it is the float32 quotient
+// unless that lies so close to the middle between two floats; for e4m3 only the middles next to a boundary
+// between two e4m3 values matter, and all 5696 pairs of significands whose quotient is within 2^-41 of one
+// of those come out right (enumerated).  Where v's remainder is subnormal the quotient is zero in e4m3.
 // Two values at a time (packed multiply-adds).
 __device__ __forceinline__ float2 quotients(float v0, float v1, float s, float r) {
   float2 t;
@@ -117,21 +126,17 @@ __device__ __forceinline__ float2 quotients(float v0, float v1, float s, float r
       "mul.rn.f32x2 t, v, r;\n\t"
       "fma.rn.f32x2 e, t, s, v;\n\t"
       "fma.rn.f32x2 t, e, r, t;\n\t"
-      "fma.rn.f32x2 e, t, s, v;\n\t"
-      "fma.rn.f32x2 t, e, r, t;\n\t"
       "mov.b64 {%0, %1}, t;\n\t}"
       : "=f"(t.x), "=f"(t.y)
       : "f"(v0), "f"(v1), "f"(r), "f"(-s));
   return t;
 }
 
-// 1 / s for quotients(), or 0 where a remainder could be subnormal or s is no number
-__device__ __forceinline__ float reciprocal_of(float s) { return s > 0x1p-60f && s < 0x1p60f ? __frcp_rn(s) : 0.f; }
-
 // the same columns of a row of q
 template <bool VEC, int LANES>
-__device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int cols, const float (&v)[8], float s,
-                                           float r) {
+__device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int cols, const float (&v)[8],
+                                           BlockScale bs) {
+  const float s = bs.s, r = bs.r;
   float t[8];
   if (r != 0.f) {
 #pragma unroll
@@ -186,11 +191,12 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
   pdl_wait_prior();
   const int sub = threadIdx.x & 7;
   // position (row, block) of this lane group and its step: divisions once, not per block
-  const long long first = static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x >> 3), step = gridDim.x * 32LL;
-  long long r = first / p.nblk;
+  const uint32_t first = blockIdx.x * 32 + (threadIdx.x >> 3), step = gridDim.x * 32;
+  uint32_t r = first / p.nblk;
   int b = static_cast<int>(first - r * p.nblk);
-  const long long dr = step / p.nblk;
+  const uint32_t dr = step / p.nblk;
   const int db = static_cast<int>(step - dr * p.nblk);
+  const uint32_t rows = p.rows;
   auto advance = [&] {
     r += dr;
     b += db;
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
       ++r;
     }
   };
-  auto source = [&] { return r >= p.rows ? -1 : p.index ? __ldg(p.index + r) : static_cast<int>(r); };
+  auto source = [&] { return r >= rows ? -1 : p.index ? __ldg(p.index + r) : static_cast<int>(r); };
   Raw raw[2], up[2];
   auto fetch = [&](int src, int fb) {
     const bool there = src >= 0 && src < p.x_rows;
@@ -212,13 +218,13 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
     }
   };
   // in turn: this block's values are here, the next one's row is known, the one's after it is looked up
-  long long cr = r;
+  uint32_t cr = r;
   int cb = b;
   fetch(source(), b);
   advance();
   int next_src = source();
   // whole warps loop together (the shuffles below name all 32 lanes): the first lane group's row decides
-  while (__shfl_sync(0xFFFFFFFFu, cr < p.rows, 0)) {
+  while (__shfl_sync(0xFFFFFFFFu, cr < rows, 0)) {
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
         for (int i = 0; i < 8; ++i) v[h][i] = gate(v[h][i]) * u[i];
       }
     }
-    const long long nr = r;
+    const uint32_t nr = r;
     const int nb = b;
     fetch(next_src, nb);
     advance();
@@ -238,12 +244,12 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
     float m = max_nan(max8(v[0]), max8(v[1]));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float s = scale_of(m), rs = reciprocal_of(s);
-    if (cr < p.rows) {
-      if (sub == 0) p.scale[cr * p.lds + cb] = s;
+    const BlockScale bs = scale_of(m);
+    if (cr < rows) {
+      if (sub == 0) p.scale[cr * p.lds + cb] = bs.s;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        store_lane<VEC, 8>(p.q + cr * p.ldq, cb * kScaleBlock + 64 * h, sub, p.cols, v[h], s, rs);
+        store_lane<VEC, 8>(p.q + cr * p.ldq, cb * kScaleBlock + 64 * h, sub, p.cols, v[h], bs);
     }
     cr = nr;
     cb = nb;
@@ -298,11 +304,11 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) m = max_nan(m, part[turn][i]);
-    const float s = scale_of(m), rs = reciprocal_of(s);
-    if (threadIdx.x == 0) p.scale[scale_at] = s;
+    const BlockScale bs = scale_of(m);
+    if (threadIdx.x == 0) p.scale[scale_at] = bs.s;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (row0 + 32 * i < rows) store_lane<VEC, 16>(p.q + (first + 32 * i) * p.ldq, c0, sub, p.cols, v[i], s, rs);
+      if (row0 + 32 * i < rows) store_lane<VEC, 16>(p.q + (first + 32 * i) * p.ldq, c0, sub, p.cols, v[i], bs);
     if (sizeof(Raw) != 16) fetch();
   }
 }

@@ -172,6 +172,31 @@ def test_quantise_extremes(block_rows):
         assert bool((back[3:129] == 0).all())
 
 
+def test_quantise_next_to_the_boundaries():
+    """Every value v whose quotient by a scale that occurs is within 2^-41 of the middle between two
+    floats next to a boundary between two e4m3 values (a quotient that is off rounds to the wrong one)."""
+    m = torch.arange(1 << 23, 1 << 24, device="cuda").double()
+    scale = (m / 448).float().double()
+    f, e = torch.frexp(scale)
+    S, unit = (f * 2.0 ** 24).long(), torch.ldexp(torch.ones((), dtype=torch.float64), (e - 24).cpu()).cuda()
+    rows = []
+    for top in range(16, 32):                                # e4m3 values and their middles, in sixteenths
+        for side in (2, -2 if top > 16 else -1):             # half a float's step up and down
+            P = S * ((top << 21) + side)                     # scale times the middle
+            j = torch.where(P < 1 << 49, 25, 26)
+            V = (P + (torch.ones_like(P) << (j - 1))) >> j   # the nearest float v
+            at = ((P - (V << j)).abs() <= 512).nonzero()[:, 0]
+            v = V[at].double() * (1 << (j[at] - 25)).double() * unit[at]
+            rows.append(torch.stack([m[at], v], 1))
+    rows = torch.cat(rows)
+    assert len(rows) > 1000 and bool((rows == rows.float().double()).all())
+    x = rows.float()
+    x = torch.cat([x, torch.nextafter(x[:, 1:], x[:, :1]), torch.nextafter(x[:, 1:], 0 * x[:, :1]), -x[:, 1:]], 1)
+    q, s = cf.quantize_blocks(x)
+    rq, rs = quantised_64(x.double())
+    assert torch.equal(q.double(), rq) and torch.equal(s.double(), rs)
+
+
 def test_quantise_no_rows():
     q, s = cf.quantize_blocks(torch.empty((0, 200), device="cuda"))
     assert q.shape == (0, 200) and s.shape == (0, 2)

@@ -56,17 +56,17 @@ __device__ __forceinline__ void set(RawBf16& r, int i, const __nv_bfloat16* p) {
 }
 __device__ __forceinline__ void set(RawF32& r, int i, const float* p) { r.w[i] = __float_as_uint(*p); }
 
-// Lane `sub` of LANES reads 8 of the 8 LANES columns that begin at c0, zero past `cols`.  VEC: columns
-// c0 + 8 sub .., in 16-byte (wide) or 8-byte loads (a chunk that ends past the row is read one element
-// at a time: the row may be the buffer's last); else columns c0 + sub + LANES i.
-template <bool VEC, int LANES, typename T>
-__device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c0, int sub, int cols, bool wide) {
+// 8 values of a row, zero past `cols`.  VEC: columns c .. c + 7, in 16-byte or 8-byte loads (a chunk that
+// ends past the row is read one element at a time: the row may be the buffer's last); else columns c,
+// c + 8, .., which lie side by side with the other lanes'.
+template <bool VEC, typename T>
+__device__ __forceinline__ typename RawOf<T>::type load_8(const T* row, int c, int cols, int align) {
   typedef typename RawOf<T>::type Raw;
   constexpr int kWords = sizeof(Raw) / 4;
   Raw r;
-  if (VEC && c0 + sub * 8 + 8 <= cols) {
-    const T* p = row + c0 + sub * 8;
-    if (wide) {
+  if (VEC && c + 8 <= cols) {
+    const T* p = row + c;
+    if (align >= 16) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
         const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
@@ -86,15 +86,39 @@ __device__ __forceinline__ typename RawOf<T>::type load_lane(const T* row, int c
   } else {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) r.w[i] = 0;
-    if (!VEC || c0 + sub * 8 < cols) {
+    if (c < cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = VEC ? c0 + sub * 8 + i : c0 + sub + LANES * i;
-        if (c < cols) set(r, i, row + c);
+        const int at = VEC ? c + i : c + 8 * i;
+        if (at < cols) set(r, i, row + at);
       }
     }
   }
   return r;
+}
+__device__ __forceinline__ void load_32_bytes(const void* p, uint32_t* w) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+      : "l"(p));
+}
+
+// Lane `sub` of 8 reads 16 of the 128 columns that begin at c0.  VEC: the 16 from c0 + 16 sub, where rows
+// begin on 32 bytes as such; else (h, i) is column c0 + 64 h + 8 i + sub.
+template <bool VEC, typename Raw, typename T>
+__device__ __forceinline__ void load_16(const T* row, int c0, int sub, int cols, int align, Raw (&r)[2]) {
+  const int c = VEC ? c0 + 16 * sub : c0 + sub;
+  if (VEC && align == 32 && (c + 16 <= cols || c >= cols)) {
+    uint32_t w[2 * sizeof(Raw) / 4] = {};
+    if (c < cols) {
+      load_32_bytes(row + c, w);
+      if (sizeof(Raw) == 32) load_32_bytes(row + c + 8, w + sizeof(Raw) / 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * sizeof(Raw) / 4; ++i) r[i / (sizeof(Raw) / 4)].w[i % (sizeof(Raw) / 4)] = w[i];
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) r[h] = load_8<VEC>(row, c + (VEC ? 8 : 64) * h, cols, align);
 }
 
 // A block's scale s = m / 448, rounded to nearest, and r = 1 / s for quotients(), or 0 where a remainder
@@ -132,37 +156,49 @@ __device__ __forceinline__ float2 quotients(float v0, float v1, float s, float r
   return t;
 }
 
-// the same columns of a row of q
-template <bool VEC, int LANES>
-__device__ __forceinline__ void store_lane(uint8_t* row, int c0, int sub, int cols, const float (&v)[8],
-                                           BlockScale bs) {
-  const float s = bs.s, r = bs.r;
+// 8 quotients as e4m3
+__device__ __forceinline__ uint2 e4m3_8(const float (&v)[8], BlockScale bs) {
   float t[8];
-  if (r != 0.f) {
+  if (bs.r != 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float2 q = quotients(v[i], v[i + 1], s, r);
+      const float2 q = quotients(v[i], v[i + 1], bs.s, bs.r);
       t[i] = q.x;
       t[i + 1] = q.y;
     }
   } else {
     // s == 0: a block of zeros (or one whose scale underflowed): zeros, not 0 / 0
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = s == 0.f ? 0.f : v[i] / s;
+    for (int i = 0; i < 8; ++i) t[i] = bs.s == 0.f ? 0.f : v[i] / bs.s;
   }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(make_float2(t[2 * i], t[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-  const uint2 o = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-  if (VEC) {
-    const int c = c0 + sub * 8;
-    if (c + 8 <= cols) *reinterpret_cast<uint2*>(row + c) = o;
-    if (c + 8 <= cols || c >= cols) return;
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// the same columns of a row of q
+template <bool VEC>
+__device__ __forceinline__ void store_16(uint8_t* row, int c0, int sub, int cols, int align, const float (&v)[2][8],
+                                         BlockScale bs) {
+  const int c = VEC ? c0 + 16 * sub : c0 + sub;
+  const uint2 o[2] = {e4m3_8(v[0], bs), e4m3_8(v[1], bs)};
+  if (VEC && align >= 16 && c + 16 <= cols) {
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+    return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = VEC ? c0 + sub * 8 + i : c0 + sub + LANES * i;
-    if (c < cols) row[c] = static_cast<uint8_t>((i < 4 ? o.x : o.y) >> (8 * (i & 3)));
+  for (int h = 0; h < 2; ++h) {
+    const int first = c + (VEC ? 8 : 64) * h;
+    if (VEC && first + 8 <= cols) {
+      *reinterpret_cast<uint2*>(row + first) = o[h];
+    } else if (first < cols) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = VEC ? first + i : first + 8 * i;
+        if (at < cols) row[at] = static_cast<uint8_t>((i < 4 ? o[h].x : o[h].y) >> (8 * (i & 3)));
+      }
+    }
   }
 }
 
@@ -182,10 +218,14 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
   return m;
 }
 
+// CTAs on an SM (gated fp32 rows spill at four: 27.1 us for 8192 x 2048 instead of 24.2)
+template <typename T, bool GATED>
+constexpr int kRowsPerSm = GATED && sizeof(T) == 4 ? 3 : 4;
+
 // Scales per row: 8 lanes take a block, 16 values each, and load the next before they work on this one.
 // (16 lanes of 8 values spend 3 more instructions per value on the maximum, the scale and addresses.)
 template <typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -211,11 +251,8 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
     const bool there = src >= 0 && src < p.x_rows;
     const T* row = static_cast<const T*>(p.x) + static_cast<long long>(there ? src : 0) * p.ldx;
     const int cols = there ? p.cols : 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      raw[h] = load_lane<VEC, 8>(row, fb * kScaleBlock + 64 * h, sub, cols, p.wide);
-      if (GATED) up[h] = load_lane<VEC, 8>(row + p.cols, fb * kScaleBlock + 64 * h, sub, cols, p.wide);
-    }
+    load_16<VEC>(row, fb * kScaleBlock, sub, cols, p.x_align, raw);
+    if (GATED) load_16<VEC>(row + p.cols, fb * kScaleBlock, sub, cols, p.x_align, up);
   };
   // in turn: this block's values are here, the next one's row is known, the one's after it is looked up
   uint32_t cr = r;
@@ -247,28 +284,26 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const QuantParams
     const BlockScale bs = scale_of(m);
     if (cr < rows) {
       if (sub == 0) p.scale[cr * p.lds + cb] = bs.s;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        store_lane<VEC, 8>(p.q + cr * p.ldq, cb * kScaleBlock + 64 * h, sub, p.cols, v[h], bs);
+      store_16<VEC>(p.q + cr * p.ldq, cb * kScaleBlock, sub, p.cols, p.q_align, v, bs);
     }
     cr = nr;
     cb = nb;
   }
 }
 
-// Scales per 128 x 128 block: a CTA of 512 threads takes one at a time, 4 rows of 8 elements per thread,
+// Scales per 128 x 128 block: a CTA of 512 threads takes one at a time, 2 rows of 16 elements per thread,
 // held in registers between the maximum and the division; the next block is on its way meanwhile.  (256
-// threads of 8 rows need 120 registers, 16 warps on an SM: 1 us more of 18 for 5000 x 4100 bf16.)
+// threads of 64 elements need 120 registers, 16 warps on an SM: 1 us more of 18 for 5000 x 4100 bf16.)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;
-  constexpr int kRows = 4, kWarps = 16;
+  constexpr int kRows = 2, kWarps = 16;
   pdl_launch_dependents();
   pdl_wait_prior();
   __shared__ float part[2][kWarps];
   const int items = (p.rows + kScaleBlock - 1) / kScaleBlock;   // blocks of rows, times p.nblk
-  const int sub = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-  Raw raw[kRows];
+  const int sub = threadIdx.x & 7, row0 = threadIdx.x >> 3;
+  Raw raw[kRows][2];
   // this CTA's block (rb, cb) and its step: divisions once, not per block
   int rb = static_cast<int>(blockIdx.x / p.nblk), cb = static_cast<int>(blockIdx.x - static_cast<unsigned>(rb) * p.nblk);
   const int dr = static_cast<int>(gridDim.x / p.nblk), dc = static_cast<int>(gridDim.x - static_cast<unsigned>(dr) * p.nblk);
@@ -276,19 +311,22 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
     const long long at = static_cast<long long>(rb) * kScaleBlock + row0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      raw[i] = load_lane<VEC, 16>(static_cast<const T*>(p.x) + (at + 32 * i) * p.ldx, cb * kScaleBlock, sub,
-                                  rb < items && at + 32 * i < p.rows ? p.cols : 0, p.wide);
+      load_16<VEC>(static_cast<const T*>(p.x) + (at + 64 * i) * p.ldx, cb * kScaleBlock, sub,
+                   rb < items && at + 64 * i < p.rows ? p.cols : 0, p.x_align, raw[i]);
   };
   fetch();
   for (int turn = 0; rb < items; turn ^= 1) {
     const int rows = min(p.rows - rb * kScaleBlock, kScaleBlock), c0 = cb * kScaleBlock;
     const long long first = static_cast<long long>(rb) * kScaleBlock + row0, scale_at = rb * p.lds + cb;
-    float v[kRows][8];
+    float v[kRows][2][8];
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      raw[i].floats(v[i]);
-      m = max_nan(m, max8(v[i]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        raw[i][h].floats(v[i][h]);
+        m = max_nan(m, max8(v[i][h]));
+      }
     }
     rb += dr;
     cb += dc;
@@ -308,7 +346,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
     if (threadIdx.x == 0) p.scale[scale_at] = bs.s;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (row0 + 32 * i < rows) store_lane<VEC, 16>(p.q + (first + 32 * i) * p.ldq, c0, sub, p.cols, v[i], bs);
+      if (row0 + 64 * i < rows) store_16<VEC>(p.q + (first + 64 * i) * p.ldq, c0, sub, p.cols, p.q_align, v[i], bs);
     if (sizeof(Raw) != 16) fetch();
   }
 }
@@ -316,7 +354,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
 template <typename T, bool GATED, bool VEC>
 cudaError_t launch_rows(const QuantParams& p, int num_sms, cudaStream_t stream) {
   const long long ctas = (static_cast<long long>(p.rows) * p.nblk + 31) / 32;
-  const long long cap = static_cast<long long>(num_sms) * 4;   // resident
+  const long long cap = static_cast<long long>(num_sms) * kRowsPerSm<T, GATED>;   // resident
   return launch_pdl(quantize_rows_kernel<T, GATED, VEC>, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0,
                     stream, 1, p);
 }
@@ -336,11 +374,12 @@ cudaError_t launch_t(const QuantParams& p, bool gated, int block_rows, int num_s
 
 cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, int block_rows, int num_sms,
                                    cudaStream_t stream) {
+  const bool vec = p.x_align >= 8 && p.q_align >= 8;
   if (bf16)
-    return p.vec ? launch_t<__nv_bfloat16, true>(p, gated, block_rows, num_sms, stream)
-                 : launch_t<__nv_bfloat16, false>(p, gated, block_rows, num_sms, stream);
-  return p.vec ? launch_t<float, true>(p, gated, block_rows, num_sms, stream)
-               : launch_t<float, false>(p, gated, block_rows, num_sms, stream);
+    return vec ? launch_t<__nv_bfloat16, true>(p, gated, block_rows, num_sms, stream)
+               : launch_t<__nv_bfloat16, false>(p, gated, block_rows, num_sms, stream);
+  return vec ? launch_t<float, true>(p, gated, block_rows, num_sms, stream)
+             : launch_t<float, false>(p, gated, block_rows, num_sms, stream);
 }
 
 }  // namespace convf

@@ -232,11 +232,11 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   p.x = a->x; p.ldx = a->ldx; p.x_rows = a->x_rows; p.index = a->index;
   p.rows = a->rows; p.cols = a->cols; p.nblk = nblk;
   p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
-  auto rows_on = [&](int bytes) {
-    return aligned(a->x, bytes) && a->ldx * esz % bytes == 0 && (!a->gated || static_cast<long long>(a->cols) * esz % bytes == 0);
-  };
-  p.vec = rows_on(8) && a->ldq % 8 == 0 && aligned(a->q, 8);
-  p.wide = rows_on(16);
+  const uintptr_t x_at = reinterpret_cast<uintptr_t>(a->x) | a->ldx * esz | (a->gated ? static_cast<long long>(a->cols) * esz : 0);
+  const uintptr_t q_at = reinterpret_cast<uintptr_t>(a->q) | a->ldq;
+  auto common = [](uintptr_t v) { return static_cast<int>((v | 32) & (~(v | 32) + 1)); };   // largest power of two of v, up to 32
+  p.x_align = common(x_at);
+  p.q_align = common(q_at);
   const cudaError_t e = launch_quantize_blocks(p, esz == 2, a->gated != 0, a->block_rows, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "quantising launch failed: %s", cudaGetErrorString(e));
   return record_ok();

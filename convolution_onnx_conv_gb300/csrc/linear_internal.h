@@ -24,7 +24,7 @@ struct QuantParams {
   long long ldq;
   float* scale;
   long long lds;
-  int vec, wide;   // rows of x (and its second half, gated) and of q begin on 8 bytes; those of x on 16
+  int x_align, q_align;      // bytes on which rows of x (and its second half, gated) and of q begin: 32, 16, 8, or less
 };
 cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, int block_rows, int num_sms,
                                    cudaStream_t stream);

@@ -1,15 +1,17 @@
 // Quantising to e4m3 with a float scale per block: s = max|v| / 448, q = e4m3(v / s).
 //
-// Bound by the bytes: x once in, one byte per value and a scale per block out.  Rows that begin on 8 or
-// 16 bytes are read as vectors, others element by element with the lanes side by side.
+// Bound by the bytes: x once in, one byte per value and a scale per block out.  Rows that begin on 8, 16 or
+// 32 bytes are read as vectors, others element by element with the lanes side by side.
 //
 // The definition's quotient is the float32 one, rounded again to e4m3.  A division per value made the
 // kernel execute 34 instructions per value and bound it by those; here the block's scale has its
-// reciprocal taken once, and each value a product and one correction by its remainder, 13
-// instructions per value in all.  100352 x 256 fp32: 21.2 us, 6.1 TB/s; bf16, with half the bytes per
-// value, is bound by the instructions (70 to 80% of the issue slots): 8192 x 2048 gated 18.2 us.
+// reciprocal taken once, and each value a product and one correction by its remainder.
+// 100352 x 256 fp32: 21.0 us, 6.1 TB/s; bf16, with half the bytes per
+// value, is bound by the instructions: 8192 x 2048 gated 17.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "convf_internal.h"
 #include "linear_internal.h"
@@ -86,7 +88,7 @@ __device__ __forceinline__ typename RawOf<T>::type load_8(const T* row, int c, i
   } else {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) r.w[i] = 0;
-    if (c < cols) {
+    if (!VEC || c < cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int at = VEC ? c + i : c + 8 * i;
@@ -102,11 +104,10 @@ __device__ __forceinline__ void load_32_bytes(const void* p, uint32_t* w) {
       : "l"(p));
 }
 
-// Lane `sub` of 8 reads 16 of the 128 columns that begin at c0.  VEC: the 16 from c0 + 16 sub, where rows
-// begin on 32 bytes as such; else (h, i) is column c0 + 64 h + 8 i + sub.
+// 16 values of a row.  VEC: columns c .. c + 15, by 32 bytes where rows begin on 32; else (h, i) is column
+// c + 64 h + 8 i, between the other lanes'.
 template <bool VEC, typename Raw, typename T>
-__device__ __forceinline__ void load_16(const T* row, int c0, int sub, int cols, int align, Raw (&r)[2]) {
-  const int c = VEC ? c0 + 16 * sub : c0 + sub;
+__device__ __forceinline__ void load_16(const T* row, int c, int cols, int align, Raw (&r)[2]) {
   if (VEC && align == 32 && (c + 16 <= cols || c >= cols)) {
     uint32_t w[2 * sizeof(Raw) / 4] = {};
     if (c < cols) {
@@ -178,10 +179,11 @@ __device__ __forceinline__ uint2 e4m3_8(const float (&v)[8], BlockScale bs) {
 }
 
 // the same columns of a row of q
-template <bool VEC>
-__device__ __forceinline__ void store_16(uint8_t* row, int c0, int sub, int cols, int align, const float (&v)[2][8],
-                                         BlockScale bs) {
-  const int c = VEC ? c0 + 16 * sub : c0 + sub;
+template <bool VEC, typename Held>
+__device__ __forceinline__ void store_16(uint8_t* row, int c, int cols, int align, const Held (&held)[2], BlockScale bs) {
+  float v[2][8];
+  held[0].floats(v[0]);
+  held[1].floats(v[1]);
   const uint2 o[2] = {e4m3_8(v[0], bs), e4m3_8(v[1], bs)};
   if (VEC && align >= 16 && c + 16 <= cols) {
     *reinterpret_cast<uint4*>(row + c) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
@@ -192,7 +194,7 @@ __device__ __forceinline__ void store_16(uint8_t* row, int c0, int sub, int cols
     const int first = c + (VEC ? 8 : 64) * h;
     if (VEC && first + 8 <= cols) {
       *reinterpret_cast<uint2*>(row + first) = o[h];
-    } else if (first < cols) {
+    } else if (!VEC || first < cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int at = VEC ? first + i : first + 8 * i;
@@ -211,27 +213,47 @@ __device__ __forceinline__ float gate(float g) {
   return (g >= 0.f ? g : g * e) * r;
 }
 
-__device__ __forceinline__ float max8(const float (&v)[8]) {
-  float m = 0.f;
+// max|v| of 16 values (a NaN stays one)
+__device__ __forceinline__ float max_abs(const RawF32 (&v)[2]) {
+  float m[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
-  return m;
+  for (int i = 0; i < 8; i += 2)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m[h]) : "f"(__uint_as_float(v[h].w[i])), "f"(__uint_as_float(v[h].w[i + 1])));
+  return max_nan(m[0], m[1]);
+}
+__device__ __forceinline__ float max_abs(const RawBf16 (&v)[2]) {
+  uint32_t m[2] = {0, 0};   // two values at a time, as they are
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tmax.NaN.bf16x2 %0, %0, a;\n\t}" : "+r"(m[h]) : "r"(v[h].w[i]));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(m[1]));
+  return max_nan(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xFFFF0000u));
 }
 
 // CTAs on an SM (gated fp32 rows spill at four: 27.1 us for 8192 x 2048 instead of 24.2)
 template <typename T, bool GATED>
 constexpr int kRowsPerSm = GATED && sizeof(T) == 4 ? 3 : 4;
 
-// Scales per row: 8 lanes take a block, 16 values each, and load the next before they work on this one.
-// (16 lanes of 8 values spend 3 more instructions per value on the maximum, the scale and addresses.)
+// Lanes that share a block.  What a lane does per block and not per value is most of its instructions, so a
+// lane takes many values: 32 where they are held as bf16, 16 as fp32 (registers).
+template <typename T, bool GATED, bool VEC>
+constexpr int kLanes = VEC && !GATED && sizeof(T) == 2 ? 4 : 8;
+
+// Scales per row: a few lanes take a block, and load the next before they work on this one.
 template <typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;
+  typedef typename std::conditional<GATED, RawF32, Raw>::type Held;   // a block's values while its scale is found
+  constexpr int kL = kLanes<T, GATED, VEC>, kGroups = 256 / kL, kPairs = 8 / kL;   // kPairs: of 8 values
   pdl_launch_dependents();
   pdl_wait_prior();
-  const int sub = threadIdx.x & 7;
+  const int sub = threadIdx.x % kL;
   // position (row, block) of this lane group and its step: divisions once, not per block
-  const uint32_t first = blockIdx.x * 32 + (threadIdx.x >> 3), step = gridDim.x * 32;
+  const uint32_t first = blockIdx.x * kGroups + threadIdx.x / kL, step = gridDim.x * kGroups;
   uint32_t r = first / p.nblk;
   int b = static_cast<int>(first - r * p.nblk);
   const uint32_t dr = step / p.nblk;
@@ -245,14 +267,18 @@ __global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kerne
       ++r;
     }
   };
+  auto column = [&](int block, int k) { return block * kScaleBlock + (VEC ? (sub * kPairs + k) * 16 : sub); };
   auto source = [&] { return r >= rows ? -1 : p.index ? __ldg(p.index + r) : static_cast<int>(r); };
-  Raw raw[2], up[2];
+  Raw raw[kPairs][2], up[kPairs][2];
   auto fetch = [&](int src, int fb) {
     const bool there = src >= 0 && src < p.x_rows;
     const T* row = static_cast<const T*>(p.x) + static_cast<long long>(there ? src : 0) * p.ldx;
     const int cols = there ? p.cols : 0;
-    load_16<VEC>(row, fb * kScaleBlock, sub, cols, p.x_align, raw);
-    if (GATED) load_16<VEC>(row + p.cols, fb * kScaleBlock, sub, cols, p.x_align, up);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      load_16<VEC>(row, column(fb, k), cols, p.x_align, raw[k]);
+      if (GATED) load_16<VEC>(row + p.cols, column(fb, k), cols, p.x_align, up[k]);
+    }
   };
   // in turn: this block's values are here, the next one's row is known, the one's after it is looked up
   uint32_t cr = r;
@@ -262,29 +288,39 @@ __global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kerne
   int next_src = source();
   // whole warps loop together (the shuffles below name all 32 lanes): the first lane group's row decides
   while (__shfl_sync(0xFFFFFFFFu, cr < rows, 0)) {
-    float v[2][8];
+    Held v[kPairs][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      raw[h].floats(v[h]);
-      if (GATED) {
-        float u[8];
-        up[h].floats(u);
+    for (int k = 0; k < kPairs; ++k) {
+      if constexpr (GATED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[h][i] = gate(v[h][i]) * u[i];
+        for (int h = 0; h < 2; ++h) {
+          float g[8], u[8];
+          raw[k][h].floats(g);
+          up[k][h].floats(u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][h].w[i] = __float_as_uint(gate(g[i]) * u[i]);
+        }
+      } else {
+        v[k][0] = raw[k][0];
+        v[k][1] = raw[k][1];
       }
     }
     const uint32_t nr = r;
     const int nb = b;
+    // (the loads before the maximum: 100352 x 256 fp32 22.0 us instead of 21.0)
+    float m = max_abs(v[0]);
+#pragma unroll
+    for (int k = 1; k < kPairs; ++k) m = max_nan(m, max_abs(v[k]));
     fetch(next_src, nb);
     advance();
     next_src = source();
-    float m = max_nan(max8(v[0]), max8(v[1]));
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int o = kL / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const BlockScale bs = scale_of(m);
     if (cr < rows) {
       if (sub == 0) p.scale[cr * p.lds + cb] = bs.s;
-      store_16<VEC>(p.q + cr * p.ldq, cb * kScaleBlock, sub, p.cols, p.q_align, v, bs);
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) store_16<VEC>(p.q + cr * p.ldq, column(cb, k), p.cols, p.q_align, v[k], bs);
     }
     cr = nr;
     cb = nb;
@@ -302,7 +338,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
   pdl_wait_prior();
   __shared__ float part[2][kWarps];
   const int items = (p.rows + kScaleBlock - 1) / kScaleBlock;   // blocks of rows, times p.nblk
-  const int sub = threadIdx.x & 7, row0 = threadIdx.x >> 3;
+  const int lane_column = VEC ? (threadIdx.x & 7) * 16 : threadIdx.x & 7, row0 = threadIdx.x >> 3;
   Raw raw[kRows][2];
   // this CTA's block (rb, cb) and its step: divisions once, not per block
   int rb = static_cast<int>(blockIdx.x / p.nblk), cb = static_cast<int>(blockIdx.x - static_cast<unsigned>(rb) * p.nblk);
@@ -311,23 +347,20 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
     const long long at = static_cast<long long>(rb) * kScaleBlock + row0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      load_16<VEC>(static_cast<const T*>(p.x) + (at + 64 * i) * p.ldx, cb * kScaleBlock, sub,
+      load_16<VEC>(static_cast<const T*>(p.x) + (at + 64 * i) * p.ldx, cb * kScaleBlock + lane_column,
                    rb < items && at + 64 * i < p.rows ? p.cols : 0, p.x_align, raw[i]);
   };
   fetch();
   for (int turn = 0; rb < items; turn ^= 1) {
     const int rows = min(p.rows - rb * kScaleBlock, kScaleBlock), c0 = cb * kScaleBlock;
     const long long first = static_cast<long long>(rb) * kScaleBlock + row0, scale_at = rb * p.lds + cb;
-    float v[kRows][2][8];
-    float m = 0.f;
+    Raw v[kRows][2];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        raw[i][h].floats(v[i][h]);
-        m = max_nan(m, max8(v[i][h]));
-      }
+      v[i][0] = raw[i][0];
+      v[i][1] = raw[i][1];
     }
+    float m = max_nan(max_abs(v[0]), max_abs(v[1]));
     rb += dr;
     cb += dc;
     if (cb >= p.nblk) {
@@ -346,14 +379,15 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParam
     if (threadIdx.x == 0) p.scale[scale_at] = bs.s;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (row0 + 64 * i < rows) store_16<VEC>(p.q + (first + 64 * i) * p.ldq, c0, sub, p.cols, p.q_align, v[i], bs);
+      if (row0 + 64 * i < rows) store_16<VEC>(p.q + (first + 64 * i) * p.ldq, c0 + lane_column, p.cols, p.q_align, v[i], bs);
     if (sizeof(Raw) != 16) fetch();
   }
 }
 
 template <typename T, bool GATED, bool VEC>
 cudaError_t launch_rows(const QuantParams& p, int num_sms, cudaStream_t stream) {
-  const long long ctas = (static_cast<long long>(p.rows) * p.nblk + 31) / 32;
+  constexpr int kGroups = 256 / kLanes<T, GATED, VEC>;
+  const long long ctas = (static_cast<long long>(p.rows) * p.nblk + kGroups - 1) / kGroups;
   const long long cap = static_cast<long long>(num_sms) * kRowsPerSm<T, GATED>;   // resident
   return launch_pdl(quantize_rows_kernel<T, GATED, VEC>, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0,
                     stream, 1, p);

@@ -172,6 +172,17 @@ def test_quantise_extremes(block_rows):
         assert bool((back[3:129] == 0).all())
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantise_tiny_bf16(block_rows):
+    """Values and scales among float32's subnormal numbers."""
+    x = (torch.randn((130, 300), generator=gen(3), device="cuda").double() * 2.0 ** torch.arange(-130, 0, device="cuda")[:, None])
+    x = x.to(torch.bfloat16)
+    x[0, :128] = 2.0 ** -133   # bf16's smallest
+    q, s = cf.quantize_blocks(x, block_rows=block_rows)
+    rq, rs = quantised_64(x.double(), block_rows)
+    assert torch.equal(q.double(), rq) and torch.equal(s.double(), rs)
+
+
 def test_quantise_next_to_the_boundaries():
     """Every value v whose quotient by a scale that occurs is within 2^-41 of the middle between two
     floats next to a boundary between two e4m3 values (a quotient that is off rounds to the wrong one)."""

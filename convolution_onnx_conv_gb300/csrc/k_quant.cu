@@ -28,6 +28,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// x and the index are read as ordinary loads: they may be the output of the kernel before, which still runs
+// when this one begins.  Read-only loads ask for data that nothing writes while the kernel runs: the compiler
+// may take them above the wait for that kernel, and L1 may hold lines from before it.
+
 // 8 elements as they are in memory, and as floats
 struct RawBf16 {
   uint32_t w[4];
@@ -71,7 +75,7 @@ __device__ __forceinline__ typename RawOf<T>::type load_8(const T* row, int c, i
     if (align >= 16) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        const uint4 t = reinterpret_cast<const uint4*>(p)[i / 4];
         r.w[i] = t.x;
         r.w[i + 1] = t.y;
         r.w[i + 2] = t.z;
@@ -80,7 +84,7 @@ __device__ __forceinline__ typename RawOf<T>::type load_8(const T* row, int c, i
     } else {
 #pragma unroll
       for (int i = 0; i < kWords; i += 2) {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(p) + i / 2);
+        const uint2 t = reinterpret_cast<const uint2*>(p)[i / 2];
         r.w[i] = t.x;
         r.w[i + 1] = t.y;
       }
@@ -99,7 +103,7 @@ __device__ __forceinline__ typename RawOf<T>::type load_8(const T* row, int c, i
   return r;
 }
 __device__ __forceinline__ void load_32_bytes(const void* p, uint32_t* w) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
       : "l"(p));
 }
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kerne
     }
   };
   auto column = [&](int block, int k) { return block * kScaleBlock + (VEC ? (sub * kPairs + k) * 16 : sub); };
-  auto source = [&] { return r >= rows ? -1 : p.index ? __ldg(p.index + r) : static_cast<int>(r); };
+  auto source = [&] { return r >= rows ? -1 : p.index ? p.index[r] : static_cast<int>(r); };
   Raw raw[kPairs][2], up[kPairs][2];
   auto fetch = [&](int src, int fb) {
     const bool there = src >= 0 && src < p.x_rows;

@@ -1,5 +1,10 @@
 // Device-side parts shared by the linear kernels: the tile schedule over ragged row groups, the
 // e4m3 MMA, and the last step of an output element.
+//
+// The linear kernels read offsets, scales and biases as ordinary loads after pdl_wait_prior(): the kernel
+// before may write them, and still runs when these begin.  Read-only loads (ld.global.nc) ask for data that
+// nothing writes while the kernel runs: the compiler may take them above the wait, and L1 may hold lines
+// from before it.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -101,8 +106,8 @@ struct RowGroup {
 };
 __device__ __forceinline__ RowGroup row_group(const LinearParams& p, int e) {
   if (!p.offsets) return RowGroup{0, p.rows};
-  const int a = min(max(__ldg(p.offsets + e), 0), p.rows);
-  const int b = min(max(__ldg(p.offsets + e + 1), a), p.rows);
+  const int a = min(max(p.offsets[e], 0), p.rows);
+  const int b = min(max(p.offsets[e + 1], a), p.rows);
   return RowGroup{a, b};
 }
 
@@ -121,7 +126,7 @@ __device__ __forceinline__ void build_schedule(const LinearParams& p, int tile, 
       const RowGroup g = row_group(p, e);
       n += (g.last - g.first + tile - 1) / tile;
       if (block_lead && p.offsets) {
-        const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+        const int a = p.offsets[e], b = p.offsets[e + 1];
         bad = bad || a < 0 || b < a || b > p.rows;
       }
     }

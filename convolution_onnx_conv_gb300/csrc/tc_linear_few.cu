@@ -201,11 +201,11 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
         const float* ws = p.w_scale + (static_cast<long long>(q.e) * nblk + q.n0 / kScaleBlock) * p.num_kb;
         float v[kAhead][kPer], w[kAhead];
         auto fetch = [&](int kb, float (&vs)[kPer], float& wv) {
-          wv = kb < kb_end ? __ldg(ws + kb) : 0.f;
+          wv = kb < kb_end ? ws[kb] : 0.f;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
             const int c = lane + 32 * j;
-            vs[j] = kb < kb_end && c < q.rows ? __ldg(p.x_scale + (q.row0 + c) * p.xs_row + kb * p.xs_blk) : 0.f;
+            vs[j] = kb < kb_end && c < q.rows ? p.x_scale[(q.row0 + c) * p.xs_row + kb * p.xs_blk] : 0.f;
           }
         };
 #pragma unroll
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
       }
       const int nrow = quad * 32 + lane;   // this thread's weight row of the tile
       const int n = q.n0 + nrow;
-      const float bias = p.bias && n < p.N ? __ldg(p.bias + static_cast<long long>(q.e) * p.N + n) : 0.f;
+      const float bias = p.bias && n < p.N ? p.bias[static_cast<long long>(q.e) * p.N + n] : 0.f;
       auto put = [&](int c, float v) {
         v = act_clamp(v + bias, p.lo, p.hi);
         if (!CONVF_IN_BOUNDS(q.row0 + c < p.rows && n < p.N, p.status)) return;

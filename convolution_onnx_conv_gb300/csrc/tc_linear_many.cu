@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t bf16_pair(f32x2 v) {
   return bf16_pair(f.x, f.y);
 }
 __device__ __forceinline__ void load_pairs(const float* p, f32x2& a, f32x2& b) {
-  asm volatile("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p));
+  asm volatile("ld.global.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p));
 }
 // the first `left` of a 16-byte unit's PER elements
 template <int PER, typename E>
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       if (!F8) return;
       xs = p.x_scale + (q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row;
       ws = p.w_scale + (static_cast<long long>(q.e) * nblk + min(q.n0 / kScaleBlock + half, nblk - 1)) * p.num_kb;
-      x1 = __ldg(xs);
-      w1 = __ldg(ws);
+      x1 = *xs;
+      w1 = *ws;
     };
     LinearTile q, qn;
     if (mine > 0) {
@@ -358,12 +358,6 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         tmem_ld_64_wait(from, r);
         const float both = x1 * w1;
         const f32x2 s = pair_of(__float_as_uint(both), __float_as_uint(both));
-        if (F8 && kb + 1 < p.num_kb) {
-          xs += p.xs_blk;
-          ++ws;
-          x1 = __ldg(xs);
-          w1 = __ldg(ws);
-        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) fma2(acc[i], r[i], s);
         tmem_ld_64_wait(from + 64, r);
@@ -377,6 +371,14 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
         buf ^= 2;
         if (buf == half) bphase ^= 1;
+        // (here and not before the sums: there the kernel of pairs without PLAIN spilled, 101 us instead of 93
+        // for 4096 x 4097 x 4096)
+        if (F8 && kb + 1 < p.num_kb) {
+          xs += p.xs_blk;
+          ++ws;
+          x1 = *xs;
+          w1 = *ws;
+        }
         // asked before the last sums, so that the answer is not waited for
         ready = mbar_test_wait(&tfull[buf], bphase);
 #pragma unroll
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = p.vec_y ? 4 * (lane & 15) + i : p.out_bf16 ? 2 * lane + i : lane + 32 * i;
-            b[i] = bias ? __ldg(bias + min(n + c, p.N - 1)) : 0.f;
+            b[i] = bias ? bias[min(n + c, p.N - 1)] : 0.f;
           }
           for (int r0 = 0; r0 < rows; r0 += kRound) {
             if ((lane & ~(kRound - 1)) == r0) {

@@ -46,3 +46,40 @@ def test_gated_zeros_keep_their_sign():
     x[0, 128:132] = torch.tensor([1.0, -1.0, -1.0, 1.0])
     q, _ = cf.quantize_blocks(x, gated=True)
     assert q.view(torch.uint8)[0, :4].tolist() == [0x80, 0x80, 0, 0]
+
+
+# ------------------------------------------------------------------------------ memory shared with the neighbours in the stream
+
+@pytest.mark.parametrize("rows", [5, 40, 300])
+def test_a_run_reads_what_the_runs_before_it_wrote(rows):
+    """Quantiser and layer in turn over the same q, scales and index, without a wait between them: each begins
+    while the one before still runs, and has to read what that one writes."""
+    g, k, n = gen(rows), 640, 384
+    src = [torch.randn((rows, k), generator=g, device="cuda").to(torch.bfloat16) * 4.0 ** i for i in range(4)]
+    perm = [torch.randperm(rows, generator=g, device="cuda").to(torch.int32) for _ in range(4)]
+    w = [torch.randn((n, k), generator=g, device="cuda") for _ in range(2)]
+    wq, ws = cf.quantize_blocks(w[0], block_rows=128)
+    lin = cf.BlockLinear(wq, ws, out_bf16=True)
+    want = {}
+    for j in range(2):
+        cf.quantize_blocks(w[j], block_rows=128, q=wq, scale=ws)
+        for i in range(4):
+            torch.cuda.synchronize()
+            a = cf.quantize_blocks(src[i], index=perm[i])
+            torch.cuda.synchronize()
+            want[i, j] = lin(*a)
+            torch.cuda.synchronize()
+    q, s = cf.quantize_blocks(src[0])
+    where = torch.empty_like(perm[0])
+    got = []
+    for t in range(200):
+        i, j = (t * 7 + t // 5) % 4, t // 3 % 2
+        if t % 3 == 0:
+            cf.quantize_blocks(w[j], block_rows=128, q=wq, scale=ws)   # the layer reads its weights in place
+        where.copy_(perm[i])
+        cf.quantize_blocks(src[i], index=where, q=q, scale=s)
+        got.append((i, j, lin(q, s)))
+    torch.cuda.synchronize()
+    for t, (i, j, y) in enumerate(got):
+        assert torch.equal(y, want[i, j]), t
+    assert lin.status() == cf.CONVF_OK

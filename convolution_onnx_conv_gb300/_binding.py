@@ -674,9 +674,18 @@ class _Torch:
         # the public call builds a Stream object (2 us of a 10 us call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         cls.stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+        raw = getattr(torch._C, "_cuda_getDevice", None)
+        cls.current_device = raw if raw is not None else torch.cuda.current_device
         cls.quantize = load_library().conv_fused_quantize_blocks
         cls.run = load_library().conv_fused_linear_run
         cls.ready = True
+
+    @staticmethod
+    def refuse_apart(device, **tensors):
+        """Refuses tensors of another device than `device`: a kernel would use their addresses as its own."""
+        for name, t in tensors.items():
+            if t is not None and t.get_device() != device:
+                raise ValueError(f"{name} is on device {t.get_device()}, the other operands on device {device}")
 
     @classmethod
     def on(cls, stream, device):
@@ -717,6 +726,12 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
         with T.on(stream, x.device):
             return quantize_blocks(x, index, gated, block_rows, q, scale)
     rows, cols, ldx = _rows_2d(x, "x")
+    on = x.get_device()
+    if on != T.current_device():
+        raise ValueError(f"x is on device {on}, the current device is {T.current_device()}")
+    if (q is not None and q.get_device() != on) or (scale is not None and scale.get_device() != on) \
+            or (index is not None and index.get_device() != on):
+        T.refuse_apart(on, index=index, q=q, scale=scale)
     xr = rows
     kind = x.dtype
     if kind is T.bf16:
@@ -753,7 +768,7 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
         if scale.dtype is not T.f32 or sr != srows or sc != nblk:
             raise ValueError(f"scale must be float32 of shape ({srows}, {nblk})")
     if stream is None:
-        stream = T.stream(x.get_device())
+        stream = T.stream(on)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     st = T.quantize(ctypes.byref(QuantArgs(rows, cols, x.data_ptr(), kind, xr, ldx, where, 1 if gated else 0, block_rows,
@@ -774,6 +789,8 @@ class ExpertLinear:
 
     def __init__(self, w, w_scale=None, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
         import torch
+        if not _Torch.ready:
+            _Torch.bind()
         if not w.is_cuda or w.dim() != 3:
             raise ValueError("w must be a CUDA tensor [experts][N][K]")
         if w.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
@@ -788,6 +805,10 @@ class ExpertLinear:
         for name, t, shape in (("w_scale", w_scale, blocks), ("bias", bias, (E, N))):
             if t is not None and (not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape):
                 raise ValueError(f"{name} must be a CUDA fp32 tensor of shape {shape}")
+        self.device = w.get_device()
+        if self.device != _Torch.current_device():
+            raise ValueError(f"w is on device {self.device}, the current device is {_Torch.current_device()}")
+        _Torch.refuse_apart(self.device, w_scale=w_scale, bias=bias)
         w_scale = None if w_scale is None else w_scale.contiguous()
         bias = None if bias is None else bias.contiguous()
         self._keep = (w, w_scale, bias)   # the layer reads them in place
@@ -797,8 +818,6 @@ class ExpertLinear:
                        w.stride(1) if N > 1 else max(w.stride(1), -(-K // 16) * 16), w.stride(0), act, float(clip[0]), float(clip[1]),
                        CONVF_OUT_BF16 if out_bf16 else CONVF_OUT_F32)
         self.handle = conv_fused_linear_create(d, w, w_scale, bias)
-        if not _Torch.ready:
-            _Torch.bind()
 
     def _run(self, x, offsets, x_scale, y, stream):
         if stream is not None and x.is_cuda and y is None:
@@ -809,6 +828,11 @@ class ExpertLinear:
             raise ValueError(f"x must have {self.K} columns")
         if x.dtype is not self.dtype:
             raise ValueError(f"x must be {self.dtype}")
+        if x.get_device() != self.device:   # (the library compares it with the current one)
+            raise ValueError(f"x is on device {x.get_device()}, the layer on device {self.device}")
+        if (y is not None and y.get_device() != self.device) \
+                or (x_scale is not None and x_scale.get_device() != self.device):
+            _Torch.refuse_apart(self.device, x_scale=x_scale, y=y)
         if rows <= 1:
             ldx = (ldx + 15) // 16 * 16
         xs = xs_row = xs_blk = 0
@@ -827,7 +851,7 @@ class ExpertLinear:
             if y.dtype is not self.out_dtype or yr != rows or yc != self.N:
                 raise ValueError(f"y must be {self.out_dtype} of shape ({rows}, {self.N})")
         if stream is None:
-            stream = _Torch.stream(x.get_device())
+            stream = _Torch.stream(self.device)
         elif hasattr(stream, "cuda_stream"):
             stream = stream.cuda_stream
         st = _Torch.run(self.handle, ctypes.byref(LinearArgs(rows, x.data_ptr(), ldx, xs, xs_row, xs_blk, offsets,
@@ -843,6 +867,8 @@ class ExpertLinear:
         if not offsets.is_cuda or offsets.dtype is not _Torch.i32 or offsets.shape != (self.experts + 1,) \
                 or not offsets.is_contiguous():
             raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {self.experts + 1}")
+        if offsets.get_device() != self.device:
+            raise ValueError(f"offsets is on device {offsets.get_device()}, the layer on device {self.device}")
         return self._run(x, offsets.data_ptr(), x_scale, y, stream)
 
     def describe(self, rows: int) -> str:

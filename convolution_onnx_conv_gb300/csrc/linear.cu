@@ -19,7 +19,6 @@ namespace {
 
 constexpr uint32_t kLinearMagic = 0x11EA4001u;
 constexpr uint32_t kLinearDead = 0xDEAD11EAu;
-constexpr int kMaxDevices = 64;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -405,6 +404,9 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
                          l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : "bf16", rows,
                          l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
   if (rows > 0 && n > 0 && static_cast<size_t>(n) < len) {
+    int dev = -1;   // the plan asks the current device how many clusters it runs at once
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
+      return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
     snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.form == kLinearFew ? "few_rows" : "many_rows",
              plan.tile, plan.form == kLinearFew ? 128 : kManyCols, plan.split, plan.grid);

@@ -14,6 +14,25 @@ constexpr int kMaxExtent = 0x7FFFFF00;   // rows, columns, N and K: the last til
 constexpr int kMaxExperts = 1024;   // the tile schedule keeps a prefix of them in shared memory
 constexpr int kKBlockBytes = 128;   // bytes of a k-block's operand row: 128 e4m3 or 64 bf16 values
 
+// What is set or looked up once for each device, not once for a process, by the current device (an
+// attribute of a kernel, the dynamic shared memory that it may ask for, belongs to a device).
+constexpr int kMaxDevices = 64;
+struct OncePerDevice {
+  bool done[kMaxDevices] = {};
+  // runs set() unless it has succeeded on the current device before
+  template <typename Set>
+  cudaError_t operator()(Set set) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (known && done[dev]) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && known) done[dev] = true;
+    return e;
+  }
+};
+
 struct QuantParams {
   const void* x;
   long long ldx;

@@ -335,12 +335,11 @@ teardown:
 
 template <bool F8, int TN>
 cudaError_t configure() {
-  static bool done = false;
-  if (done) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<F8, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       FewCfg<F8, TN>::kSmem);
-  if (e == cudaSuccess) done = true;
-  return e;
+  static OncePerDevice once;
+  return once([] {
+    return cudaFuncSetAttribute(linear_few_kernel<F8, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                FewCfg<F8, TN>::kSmem);
+  });
 }
 
 template <bool F8, int TN>

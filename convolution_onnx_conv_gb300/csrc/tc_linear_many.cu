@@ -567,17 +567,16 @@ template <bool F8, bool PAIR, bool PLAIN>
 cudaError_t launch_t(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
                      const CUtensorMap& tmY, cudaStream_t stream) {
   using Cfg = ManyCfg<PAIR>;
-  static bool configured = false;
-  if (!configured) {
+  static OncePerDevice once;
+  const cudaError_t e = once([] {
     // the register split waits for ever if the kernel was given fewer registers than it shares out
     cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR, PLAIN>);
-    if (e == cudaSuccess && at.numRegs < Cfg::kRegs) e = cudaErrorInvalidKernelImage;
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_many_kernel<F8, PAIR, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+    const cudaError_t got = cudaFuncGetAttributes(&at, linear_many_kernel<F8, PAIR, PLAIN>);
+    if (got != cudaSuccess) return got;
+    if (at.numRegs < Cfg::kRegs) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(linear_many_kernel<F8, PAIR, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  });
+  if (e != cudaSuccess) return e;
   return launch_pdl(linear_many_kernel<F8, PAIR, PLAIN>, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, PAIR ? 2 : 1, p,
                     tmW, tmX, tmY);
 }

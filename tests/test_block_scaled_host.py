@@ -120,3 +120,78 @@ def test_layers_take_tensors_of_their_device_only(calls):
         with pytest.raises(ValueError, match="device 1"):
             layer(**{**run(), name: run(1)[name]})
     assert len(calls) == 2
+
+
+# ------------------------------------------------------------------------------ two devices in a process
+
+TWO_DEVICES = r"""
+#include <cuda_runtime.h>
+#include <cstdio>
+#include <cstring>
+#include <map>
+#include <utility>
+// a runtime of two devices, each with its own limit of dynamic shared memory per kernel (48 KB at first)
+static int device = 0;
+static std::map<std::pair<int, const void*>, size_t> limit;
+template <typename F> const void* address(F f) { const void* p; memcpy(&p, &f, sizeof p); return p; }
+static cudaError_t fake_get_device(int* d) { *d = device; return cudaSuccess; }
+template <typename F> cudaError_t fake_set(F f, cudaFuncAttribute, int bytes) {
+  limit[{device, address(f)}] = bytes;
+  return cudaSuccess;
+}
+template <typename F> cudaError_t fake_attributes(cudaFuncAttributes* a, F) { a->numRegs = 168; return cudaSuccess; }
+template <typename F> bool fits(size_t bytes, F f) {
+  const auto at = limit.find({device, address(f)});
+  return bytes <= (at == limit.end() ? 49152 : at->second);
+}
+template <typename F, typename... A> cudaError_t fake_launch(const cudaLaunchConfig_t* c, F f, A&&...) {
+  return fits(c->dynamicSmemBytes, f) ? cudaSuccess : cudaErrorInvalidValue;
+}
+template <typename F> cudaError_t fake_clusters(int* n, F f, const cudaLaunchConfig_t* c) {
+  *n = 18;
+  return fits(c->dynamicSmemBytes, f) ? cudaSuccess : cudaErrorInvalidValue;
+}
+#define cudaGetDevice fake_get_device
+#define cudaFuncSetAttribute fake_set
+#define cudaFuncGetAttributes fake_attributes
+#define cudaLaunchKernelEx fake_launch
+#define cudaOccupancyMaxActiveClusters fake_clusters
+#include SOURCE
+int main() {
+  convf::LinearParams p{};
+  CUtensorMap m{};
+  int bad = 0;
+  for (device = 0; device < 2; ++device)
+    for (int e4m3 = 0; e4m3 < 2; ++e4m3)
+      for (int turn = 0; turn < 2; ++turn)
+        for (int i = 0; i < 3; ++i) {
+#ifdef FEW
+          const convf::LinearPlan plan{convf::kLinearFew, 16 << i, 1, 152};
+          bad += convf::launch_linear_few(p, plan, e4m3, m, m, nullptr) != cudaSuccess;
+          bad += convf::linear_few_max_clusters(e4m3, 16 << i, 4, 152) != 18;
+#else
+          const convf::LinearPlan plan{convf::kLinearMany, i ? 256 : 128, 1, 152};
+          p.vec_y = i == 2;
+          bad += convf::launch_linear_many(p, plan, e4m3, m, m, m, nullptr) != cudaSuccess;
+#endif
+        }
+  printf("%d refused\n", bad);
+  return bad != 0;
+}
+"""
+
+
+@pytest.mark.parametrize("name", ["tc_linear_few", "tc_linear_many"])
+def test_kernels_are_set_up_on_every_device(name, tmp_path):
+    """The host side of the launches, on a runtime that keeps a kernel's shared-memory limit per device."""
+    import subprocess
+    from convolution_onnx_conv_gb300 import _build
+    main = tmp_path / "main.cu"
+    main.write_text(TWO_DEVICES)
+    exe = str(tmp_path / "main")
+    subprocess.run([_build._nvcc(), "-gencode", "arch=compute_103a,code=compute_103a", "-Xcicc", "-O0", "-std=c++17",
+                    "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+                    f'-DSOURCE="{name}.cu"', *(["-DFEW"] if name == "tc_linear_few" else []), str(main), "-o", exe, "-lcuda"],
+                   check=True, capture_output=True)
+    res = subprocess.run([exe], capture_output=True, text=True)
+    assert res.returncode == 0 and res.stdout == "0 refused\n", res.stdout + res.stderr

@@ -100,47 +100,49 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-// The rows of x that expert e takes: [first, last), inside [0, rows) whatever the offsets hold.
+// The rows of x that expert e takes: [first, last).  (Read where there are tiles, that is, where build_schedule
+// has found the offsets in order.)
 struct RowGroup {
   int first, last;
 };
 __device__ __forceinline__ RowGroup row_group(const LinearParams& p, int e) {
   if (!p.offsets) return RowGroup{0, p.rows};
-  const int a = min(max(p.offsets[e], 0), p.rows);
-  const int b = min(max(p.offsets[e + 1], a), p.rows);
-  return RowGroup{a, b};
+  return RowGroup{p.offsets[e], p.offsets[e + 1]};
 }
 
 // Tiles of `tile` rows over the experts: prefix[i] = row tiles of the experts before the i-th pair of them
-// (a prefix for each expert would not leave the room that the stages need).  One warp; block_lead tells
-// the CTA that reports offsets that decrease or pass the rows.
+// (a prefix for each expert would not leave the room that the stages need).  One warp.  Offsets that
+// decrease or pass the rows give no tiles at all (the tiles of such groups can be more than an int counts);
+// block_lead tells the CTA that reports them.
 __device__ __forceinline__ int expert_pairs(const LinearParams& p) { return (p.experts + 1) >> 1; }
 __device__ __forceinline__ void build_schedule(const LinearParams& p, int tile, int* prefix, bool block_lead) {
   const int lane = threadIdx.x & 31, pairs = expert_pairs(p);
-  int sum = 0;
+  uint32_t sum = 0;
   bool bad = false;
   for (int base = 0; base < pairs; base += 32) {
     const int i = base + lane;
-    int n = 0;
+    uint32_t n = 0;
     for (int e = 2 * i; e < min(2 * i + 2, p.experts); ++e) {
       const RowGroup g = row_group(p, e);
-      n += (g.last - g.first + tile - 1) / tile;
-      if (block_lead && p.offsets) {
-        const int a = p.offsets[e], b = p.offsets[e + 1];
-        bad = bad || a < 0 || b < a || b > p.rows;
-      }
+      if (g.first < 0 || g.last < g.first || g.last > p.rows)
+        bad = true;
+      else
+        n += (g.last - g.first + tile - 1) / tile;
     }
-    int incl = n;
+    uint32_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += t;
     }
-    if (i < pairs) prefix[i] = sum + incl - n;
+    if (i < pairs) prefix[i] = static_cast<int>(sum + incl - n);
     sum += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  if (lane == 0) prefix[pairs] = sum;
-  if (bad) atomicOr(p.status, kStatusOffsets);
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (lane == 0) {
+    prefix[pairs] = bad ? 0 : static_cast<int>(sum);
+    if (bad && block_lead) atomicOr(p.status, kStatusOffsets);
+  }
 }
 constexpr int kScheduleBytes = (kMaxExperts / 2 + 4) * 4;   // of prefix
 

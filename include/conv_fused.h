@@ -520,8 +520,8 @@ typedef struct {
                               up to offsets[e+1] (possibly none).  NULL: one expert takes all
                               rows (experts == 1 only).  Rows outside [offsets[0],
                               offsets[experts]) are not written.  Offsets that decrease or pass
-                              `rows` reach no memory outside x and y, leave what rows they name
-                              unspecified, and are reported by conv_fused_linear_status.       */
+                              `rows` make a run that writes nothing; conv_fused_linear_status
+                              reports them.                                                    */
   void* y;                 /* device [rows][N], element aligned; must not overlap x            */
   long long ldy;           /* elements between rows of y                                       */
 } convf_linear_args;

@@ -83,3 +83,33 @@ def test_a_run_reads_what_the_runs_before_it_wrote(rows):
     for t, (i, j, y) in enumerate(got):
         assert torch.equal(y, want[i, j]), t
     assert lin.status() == cf.CONVF_OK
+
+
+# ------------------------------------------------------------------------------ offsets out of order
+
+@pytest.mark.parametrize("rows", [64, 900])
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_offsets_out_of_order_write_nothing(rows, e4m3):
+    """The tiles of groups that overlap can be more than an int counts (every second one of 1024 experts taking
+    2^27 rows), so that a run with such offsets has no tiles at all."""
+    g, e, n, k = gen(rows), 5, 300, 256
+    x = torch.randn((rows, k), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn((e, n, k), generator=g, device="cuda").to(torch.bfloat16)
+    xs = ws = None
+    if e4m3:
+        x, xs = cf.quantize_blocks(x)
+        parts = [cf.quantize_blocks(m, block_rows=128) for m in w]
+        w = torch.stack([p[0].view(torch.uint8) for p in parts]).view(torch.float8_e4m3fn)
+        ws = torch.stack([p[1] for p in parts])
+    lin = cf.ExpertLinear(w, ws)
+    y = torch.full((rows, n), -7.0, device="cuda")
+    for off in ([0, rows, 0, rows, 0, rows], [0, 10, 20, 30, 40, rows + 1], [-1, 10, 20, 30, 40, rows], [0, 10, 9, 30, 40, rows],
+                [0, 0, 0, 0, 2 ** 31 - 1, -2 ** 31]):
+        lin(x, torch.tensor(off, dtype=torch.int32, device="cuda"), xs, y=y)
+        torch.cuda.synchronize()
+        assert lin.status() == cf.CONVF_ERR_INVALID_ARG and "offsets" in cf.conv_fused_last_error()
+        lin.clear_status()
+        assert bool((y == -7).all())
+    lin(x, torch.tensor([0, 10, 20, 30, 40, rows], dtype=torch.int32, device="cuda"), xs, y=y)
+    torch.cuda.synchronize()
+    assert lin.status() == cf.CONVF_OK and bool((y != -7).all())

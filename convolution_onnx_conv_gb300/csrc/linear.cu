@@ -22,15 +22,6 @@ constexpr uint32_t kLinearDead = 0xDEAD11EAu;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// bytes that rows of `row` bytes, `stride` bytes apart, span from their first
-unsigned long long span(long long rows, long long stride, long long row) {
-  return rows > 0 ? static_cast<unsigned long long>(rows - 1) * stride + row : 0;
-}
-bool overlap(const void* a, unsigned long long an, const void* b, unsigned long long bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return an && bn && x < y + bn && y < x + an;
-}
-
 // whether `rows` rows `ld` elements apart pass the address space (their products then pass 64 bits)
 bool too_far(long long rows, long long ld, int esz) { return ld > ((1LL << 48) / esz) / (rows > 1 ? rows : 1); }
 
@@ -219,10 +210,9 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   const int esz = a->x_dtype == CONVF_OUT_BF16 ? 2 : 4;
   if (!aligned(a->x, esz) || !aligned(a->scale, 4) || !aligned(a->index, 4))
     return record_error(CONVF_ERR_INVALID_ARG, "x, index and scale must be aligned to their elements");
-  const unsigned long long xb = span(a->x_rows, a->ldx * esz, wide * esz), qb = span(a->rows, a->ldq, a->cols);
-  const unsigned long long sb =
-      span((a->rows - 1LL) / a->block_rows + 1, a->lds * 4, static_cast<long long>(nblk) * 4);
-  if (overlap(a->x, xb, a->q, qb) || overlap(a->x, xb, a->scale, sb) || overlap(a->q, qb, a->scale, sb))
+  const Region x_at{a->x, a->x_rows, wide * esz, a->ldx * esz}, q_at{a->q, a->rows, a->cols, a->ldq};
+  const Region scale_at{a->scale, (a->rows - 1LL) / a->block_rows + 1, nblk * 4LL, a->lds * 4};
+  if (overlap(x_at, q_at) || overlap(x_at, scale_at) || overlap(q_at, scale_at))
     return record_error(CONVF_ERR_INVALID_ARG, "x, q and scale overlap");
   int dev = -1, sms = 0;
   convf_status st = current_device(&dev, &sms);
@@ -231,11 +221,11 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   p.x = a->x; p.ldx = a->ldx; p.x_rows = a->x_rows; p.index = a->index;
   p.rows = a->rows; p.cols = a->cols; p.nblk = nblk;
   p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
-  const uintptr_t x_at = reinterpret_cast<uintptr_t>(a->x) | a->ldx * esz | (a->gated ? static_cast<long long>(a->cols) * esz : 0);
-  const uintptr_t q_at = reinterpret_cast<uintptr_t>(a->q) | a->ldq;
+  const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a->x) | a->ldx * esz | (a->gated ? static_cast<long long>(a->cols) * esz : 0);
+  const uintptr_t q_bits = reinterpret_cast<uintptr_t>(a->q) | a->ldq;
   auto common = [](uintptr_t v) { return static_cast<int>((v | 32) & (~(v | 32) + 1)); };   // largest power of two of v, up to 32
-  p.x_align = common(x_at);
-  p.q_align = common(q_at);
+  p.x_align = common(x_bits);
+  p.q_align = common(q_bits);
   const cudaError_t e = launch_quantize_blocks(p, esz == 2, a->gated != 0, a->block_rows, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "quantising launch failed: %s", cudaGetErrorString(e));
   return record_ok();
@@ -331,7 +321,8 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   if (!aligned(a->x, 16)) return record_error(CONVF_ERR_INVALID_ARG, "x must be 16-byte aligned");
   if (!aligned(a->y, osz) || !aligned(a->x_scale, 4) || !aligned(a->offsets, 4))
     return record_error(CONVF_ERR_INVALID_ARG, "y, x_scale and offsets must be aligned to their elements");
-  if (overlap(a->x, span(a->rows, a->ldx * esz, d.K * esz), a->y, span(a->rows, a->ldy * osz, d.N * osz)))
+  const Region y_at{a->y, a->rows, d.N * osz, a->ldy * osz};
+  if (overlap(Region{a->x, a->rows, d.K * esz, a->ldx * esz}, y_at))
     return record_error(CONVF_ERR_INVALID_ARG, "x and y overlap");
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)

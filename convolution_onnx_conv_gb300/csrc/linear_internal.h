@@ -33,6 +33,28 @@ struct OncePerDevice {
   }
 };
 
+// Memory of a call: `rows` rows of `row` bytes, `stride` bytes apart.
+struct Region {
+  const void* p;
+  long long rows, row, stride;
+};
+// Whether two of them share a byte.  Rows at the same distance may lie between each other's (columns of one
+// buffer); other pairs go by the bytes from their first to their last.
+inline bool overlap(Region a, Region b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.row < 1 || b.row < 1) return false;
+  const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  if (d >= (a.rows - 1) * a.stride + a.row || -d >= (b.rows - 1) * b.stride + b.row) return false;
+  if (a.rows == 1) a.stride = b.stride;
+  if (b.rows == 1) b.stride = a.stride;
+  const long long s = a.stride;
+  if (s != b.stride || s < a.row || s < b.row) return true;
+  // row i of a and row j of b are d + (j - i) s apart: of the differences that can share a byte, there are
+  // two at most, around -d / s
+  const long long r = (d % s + s) % s, m = (r - d) / s;   // d + m s = r, in [0, s)
+  auto there = [&](long long k) { return k > -a.rows && k < b.rows; };
+  return (r < a.row && there(m)) || (s - r < b.row && there(m - 1));
+}
+
 struct QuantParams {
   const void* x;
   long long ldx;

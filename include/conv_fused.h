@@ -485,7 +485,8 @@ typedef struct {
 
 /* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row
  * stride of at least a row is served; rows that begin on 16 bytes are read and written as vectors.
- * q and scale must not overlap x. */
+ * q and scale must not overlap x or each other; rows of two of them that are the same
+ * distance apart may lie between each other's (columns of one buffer). */
 convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
 
 /* A linear layer, or one per expert: y[m][n] = act(sum_k x[m][k] W[e(m)][n][k] + bias[e(m)][n]),

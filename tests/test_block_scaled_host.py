@@ -195,3 +195,55 @@ def test_kernels_are_set_up_on_every_device(name, tmp_path):
                    check=True, capture_output=True)
     res = subprocess.run([exe], capture_output=True, text=True)
     assert res.returncode == 0 and res.stdout == "0 refused\n", res.stdout + res.stderr
+
+
+# ------------------------------------------------------------------------------ operands that overlap
+
+REGIONS = r"""
+#include "linear_internal.h"
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+using convf::Region;
+static void mark(std::vector<int>& bytes, Region g, int bit) {
+  for (long long i = 0; i < g.rows; ++i)
+    for (long long k = 0; k < g.row; ++k) bytes[reinterpret_cast<uintptr_t>(g.p) + i * g.stride + k] |= bit;
+}
+int main() {
+  srand(1);
+  int met = 0, free_inside = 0, wrong = 0;
+  for (int n = 0; n < 200000; ++n) {
+    auto any = [&](bool same, long long stride) {
+      const long long row = 1 + rand() % 8, rows = rand() % 5;
+      return Region{reinterpret_cast<const void*>(uintptr_t(1 + rand() % 60)), rows, row,
+                    same ? stride : row + rand() % 8};
+    };
+    const bool same = rand() % 4 != 0;
+    const long long stride = 8 + rand() % 8;
+    const Region a = any(same, stride), b = any(same, stride);
+    std::vector<int> bytes(400);
+    mark(bytes, a, 1);
+    mark(bytes, b, 2);
+    bool share = false;
+    for (int v : bytes) share |= v == 3;
+    const bool said = convf::overlap(a, b);
+    // exact at equal strides; else what shares a byte is never let through
+    wrong += (same || a.rows == 1 || b.rows == 1) && a.row <= b.stride && b.row <= a.stride ? said != share : share && !said;
+    wrong += said != convf::overlap(b, a);
+    met += share;
+    free_inside += !said && same && a.rows > 1 && b.rows > 1;
+  }
+  printf("%d wrong, %d\n", wrong, met > 1000 && free_inside > 1000);
+  return wrong;
+}
+"""
+
+
+def test_overlap_of_strided_rows_against_their_bytes(tmp_path):
+    import subprocess
+    from convolution_onnx_conv_gb300 import _build
+    main, exe = tmp_path / "main.cpp", str(tmp_path / "main")
+    main.write_text(REGIONS)
+    subprocess.run([_build._nvcc(), "-std=c++17", "-I", CSRC, str(main), "-o", exe], check=True, capture_output=True)
+    res = subprocess.run([exe], capture_output=True, text=True)
+    assert res.stdout == "0 wrong, 1\n"

@@ -113,3 +113,27 @@ def test_offsets_out_of_order_write_nothing(rows, e4m3):
     lin(x, torch.tensor([0, 10, 20, 30, 40, rows], dtype=torch.int32, device="cuda"), xs, y=y)
     torch.cuda.synchronize()
     assert lin.status() == cf.CONVF_OK and bool((y != -7).all())
+
+
+# ------------------------------------------------------------------------------ operands that overlap
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_columns_of_one_buffer(rows):
+    """x, y and a quantiser's operands as columns of the same rows, as a program that keeps its features side by
+    side has them."""
+    g, n, k = gen(rows), 96, 64
+    w = torch.randn((n, k), generator=g, device="cuda").to(torch.bfloat16)
+    lin = cf.BlockLinear(w, out_bf16=True)
+    both = torch.randn((rows, k + n + 8), generator=g, device="cuda").to(torch.bfloat16)
+    before = both.clone()
+    want = lin(before[:, :k].contiguous())
+    lin(both[:, :k], y=both[:, k:k + n])
+    assert torch.equal(both[:, k:k + n], want)
+    assert torch.equal(both[:, :k], before[:, :k]) and torch.equal(both[:, k + n:], before[:, k + n:])
+    raw = both.view(torch.uint8)   # the quantised y in the bytes of x
+    q, s = cf.quantize_blocks(want)
+    out = raw[:, :n].view(torch.float8_e4m3fn)
+    cf.quantize_blocks(both[:, k:k + n], q=out)
+    assert torch.equal(out.view(torch.uint8), q.view(torch.uint8)) and torch.equal(both[:, k:k + n], want)
+    with pytest.raises(cf.ConvFusedError):
+        lin(both[:, :k], y=both[:, k - 8:k - 8 + n])

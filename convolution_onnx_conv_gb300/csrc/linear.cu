@@ -212,8 +212,11 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
     return record_error(CONVF_ERR_INVALID_ARG, "x, index and scale must be aligned to their elements");
   const Region x_at{a->x, a->x_rows, wide * esz, a->ldx * esz}, q_at{a->q, a->rows, a->cols, a->ldq};
   const Region scale_at{a->scale, (a->rows - 1LL) / a->block_rows + 1, nblk * 4LL, a->lds * 4};
+  const Region index_at{a->index, 1, a->rows * 4LL, a->rows * 4LL};
   if (overlap(x_at, q_at) || overlap(x_at, scale_at) || overlap(q_at, scale_at))
     return record_error(CONVF_ERR_INVALID_ARG, "x, q and scale overlap");
+  if (overlap(index_at, q_at) || overlap(index_at, scale_at))   // (rows are looked up while others are written)
+    return record_error(CONVF_ERR_INVALID_ARG, "index and q or scale overlap");
   int dev = -1, sms = 0;
   convf_status st = current_device(&dev, &sms);
   if (st != CONVF_OK) return st;
@@ -321,9 +324,25 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   if (!aligned(a->x, 16)) return record_error(CONVF_ERR_INVALID_ARG, "x must be 16-byte aligned");
   if (!aligned(a->y, osz) || !aligned(a->x_scale, 4) || !aligned(a->offsets, 4))
     return record_error(CONVF_ERR_INVALID_ARG, "y, x_scale and offsets must be aligned to their elements");
+  // y against all that the run reads (its tiles are written while others are read)
   const Region y_at{a->y, a->rows, d.N * osz, a->ldy * osz};
+  const long long nblk = ceil_div(d.K, kScaleBlock), wblk = ceil_div(d.N, kScaleBlock);
+  const long long apart = d.experts > 1 ? d.expert_stride * esz : 0;
+  const Region w_at = d.experts == 1 || apart == d.N * d.ldw * esz
+                          ? Region{l->w, static_cast<long long>(d.experts) * d.N, d.K * esz, d.ldw * esz}
+                          : Region{l->w, 1, (d.experts - 1) * apart + ((d.N - 1) * d.ldw + d.K) * esz, 0};
+  const Region xs_at = !e4m3 ? Region{}
+                       : a->xs_blk == 1 ? Region{a->x_scale, a->rows, nblk * 4, a->xs_row * 4}
+                       : a->xs_row == 1 ? Region{a->x_scale, nblk, a->rows * 4LL, a->xs_blk * 4}
+                                        : Region{a->x_scale, 1, ((a->rows - 1) * a->xs_row + (nblk - 1) * a->xs_blk + 1) * 4, 0};
   if (overlap(Region{a->x, a->rows, d.K * esz, a->ldx * esz}, y_at))
     return record_error(CONVF_ERR_INVALID_ARG, "x and y overlap");
+  if (overlap(w_at, y_at)) return record_error(CONVF_ERR_INVALID_ARG, "the weights and y overlap");
+  if (overlap(xs_at, y_at)) return record_error(CONVF_ERR_INVALID_ARG, "x_scale and y overlap");
+  if (overlap(Region{l->w_scale, 1, d.experts * wblk * nblk * 4, 0}, y_at) ||
+      overlap(Region{l->bias, 1, static_cast<long long>(d.experts) * d.N * 4, 0}, y_at) ||
+      overlap(Region{a->offsets, 1, (d.experts + 1) * 4LL, 0}, y_at))
+    return record_error(CONVF_ERR_INVALID_ARG, "w_scale, bias or offsets overlap y");
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
     return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);

@@ -485,7 +485,7 @@ typedef struct {
 
 /* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row
  * stride of at least a row is served; rows that begin on 16 bytes are read and written as vectors.
- * q and scale must not overlap x or each other; rows of two of them that are the same
+ * q and scale must not overlap x, index or each other; rows of two of them that are the same
  * distance apart may lie between each other's (columns of one buffer). */
 convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
 
@@ -523,7 +523,8 @@ typedef struct {
                               offsets[experts]) are not written.  Offsets that decrease or pass
                               `rows` make a run that writes nothing; conv_fused_linear_status
                               reports them.                                                    */
-  void* y;                 /* device [rows][N], element aligned; must not overlap x            */
+  void* y;                 /* device [rows][N], element aligned; must not overlap what the run
+                              reads: x, x_scale, offsets, W, w_scale, bias                     */
   long long ldy;           /* elements between rows of y                                       */
 } convf_linear_args;
 

@@ -247,3 +247,18 @@ def test_overlap_of_strided_rows_against_their_bytes(tmp_path):
     subprocess.run([_build._nvcc(), "-std=c++17", "-I", CSRC, str(main), "-o", exe], check=True, capture_output=True)
     res = subprocess.run([exe], capture_output=True, text=True)
     assert res.stdout == "0 wrong, 1\n"
+
+
+@pytest.mark.parametrize("where", ["q", "scale"])
+def test_an_index_that_overlaps_an_output_is_refused(where):
+    import convolution_onnx_conv_gb300 as cf
+    from convolution_onnx_conv_gb300 import _build
+    from convolution_onnx_conv_gb300._binding import QuantArgs
+    _build.build()
+    P = 0x10000000   # addresses that nothing reads: the call is refused before any CUDA call
+    a = QuantArgs(rows=4, cols=200, x=P, x_dtype=cf.CONVF_OUT_BF16, x_rows=9, ldx=200, index=4 * P, gated=0, block_rows=1,
+                  q=2 * P, ldq=208, scale=3 * P, lds=2)
+    setattr(a, where, 4 * P + 8)
+    with pytest.raises(cf.ConvFusedError) as e:
+        cf.conv_fused_quantize_blocks(a)
+    assert e.value.status == cf.CONVF_ERR_INVALID_ARG and "index and q or scale overlap" in str(e.value)

@@ -117,6 +117,31 @@ def test_offsets_out_of_order_write_nothing(rows, e4m3):
 
 # ------------------------------------------------------------------------------ operands that overlap
 
+def test_y_over_anything_that_the_run_reads_is_refused():
+    e, n, k, rows = 2, 128, 256, 64
+    buf = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def at(byte, shape, dtype):
+        size = torch.empty((), dtype=dtype).element_size()
+        count = 1
+        for s in shape:
+            count *= s
+        return buf[byte:byte + count * size].view(dtype).view(shape)
+
+    w, ws, bias = at(0, (e, n, k), torch.float8_e4m3fn), at(65536, (e, 1, 2), torch.float32), at(66048, (e, n), torch.float32)
+    x, xs, off = at(131072, (rows, k), torch.float8_e4m3fn), at(196608, (rows, 2), torch.float32), at(197632, (e + 1,), torch.int32)
+    lin = cf.ExpertLinear(w, ws, bias=bias)
+    size = rows * n * 4
+    for name, first, length in (("weights", 0, e * n * k), ("w_scale", 65536, e * 8), ("bias", 66048, e * n * 4), ("x and", 131072, rows * k),
+                                ("x_scale", 196608, rows * 8), ("offsets", 197632, (e + 1) * 4)):
+        for byte in (first, first + length - 4, first - size + 4):
+            if byte >= 0:
+                with pytest.raises(cf.ConvFusedError) as err:
+                    lin(x, off, xs, y=at(byte, (rows, n), torch.float32))
+                assert err.value.status == cf.CONVF_ERR_INVALID_ARG and "overlap" in str(err.value), (name, byte)
+    lin(x, off, xs, y=at(262144, (rows, n), torch.float32))
+
+
 @pytest.mark.parametrize("rows", [3, 200])
 def test_columns_of_one_buffer(rows):
     """x, y and a quantiser's operands as columns of the same rows, as a program that keeps its features side by

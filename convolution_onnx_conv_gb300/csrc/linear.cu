@@ -357,9 +357,11 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
   p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
   p.n_tiles = static_cast<int>(ceil_div(d.N, plan.form == kLinearMany ? kManyCols : 128));
-  // fp32 results of bf16 operands: the MMA's own accumulator truncates (1.2e-6 of the result at K =
-  // 1000, against 3e-7 when every 256 values are added in registers); bf16 results cannot tell
-  p.chunk_kb = e4m3 ? 1 : osz == 2 ? p.num_kb : 4;
+  // bf16 operands: the MMA's own accumulator truncates, so its sums go to registers every 256 values where
+  // the result is fp32 (1.2e-6 of the result at K = 1000 without it, 3e-7 with it), and every 4096 values
+  // where it is bf16: terms of one sign then lose 1e-5 of their sum at most, whatever K is (without it 8e-4
+  // at K = 131072, and a whole step of bf16 from about 10^6)
+  p.chunk_kb = e4m3 ? 1 : osz == 2 ? 64 : 4;
   p.vec_y = aligned(a->y, 16) && a->ldy * osz % 16 == 0;
   p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;

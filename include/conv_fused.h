@@ -490,8 +490,11 @@ typedef struct {
 convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
 
 /* A linear layer, or one per expert: y[m][n] = act(sum_k x[m][k] W[e(m)][n][k] + bias[e(m)][n]),
- * with the act of a conv.  Sums are held in float32 (e4m3: each block's sum of products, then
- * times its two scales into a float32 sum over the blocks); y is rounded once. */
+ * with the act of a conv.  Sums are held in float32.  e4m3: each block's sum of products, times the
+ * product of its two scales (a float32 number: scales whose product leaves float32's normal range lose
+ * digits), is added to a float32 sum over the blocks.  bf16: the tensor core sums 256 products (float32
+ * results) or 4096 (bf16 results), truncating where it adds, and those sums are added in float32 to
+ * nearest.  y is rounded once. */
 typedef struct {
   int N, K;                /* W[e]: [N][K]                                                     */
   int experts;             /* >= 1, at most 1024                                               */

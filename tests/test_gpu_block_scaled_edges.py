@@ -162,3 +162,28 @@ def test_columns_of_one_buffer(rows):
     assert torch.equal(out.view(torch.uint8), q.view(torch.uint8)) and torch.equal(both[:, k:k + n], want)
     with pytest.raises(cf.ConvFusedError):
         lin(both[:, :k], y=both[:, k - 8:k - 8 + n])
+
+
+# ------------------------------------------------------------------------------ long reductions
+
+def half_step(t):
+    """Half the distance between bf16 numbers (8 significant bits) at t."""
+    return torch.ldexp(torch.ones((), dtype=torch.float64), (torch.frexp(t.cpu().abs())[1] - 9)).cuda()
+
+
+@pytest.mark.parametrize("rows,n,k,form", [(2100, 512, 1 << 17, "few_rows"), (2100, 2048, 1 << 16, "many_rows"), (3, 640, 1 << 19, "few_rows")])
+def test_bf16_results_of_long_sums_of_one_sign(rows, n, k, form):
+    """The tensor core adds 16 products at a time and truncates: 4096 / 16 = 256 additions, each off by at most
+    2^-23 of the sum, then k / 4096 additions to nearest (2^-24 each), then the one rounding to bf16.  (Summed
+    in its accumulator alone, 8 10^-4 at k = 2^17, every result is short by up to 1/2 of half a step.)"""
+    g = gen(k)
+    x = (1 + torch.rand((rows, k), generator=g, device="cuda")).to(torch.bfloat16)
+    w = (1 + torch.rand((n, k), generator=g, device="cuda")).to(torch.bfloat16)
+    lin = cf.BlockLinear(w, out_bf16=True)
+    assert form in lin.describe(rows)
+    y = lin(x).double()
+    ref = torch.zeros((rows, n), dtype=torch.float64, device="cuda")
+    for i in range(0, k, 1 << 14):
+        ref += x[:, i:i + (1 << 14)].double() @ w[:, i:i + (1 << 14)].double().T
+    off = ((y - ref).abs() - half_step(ref)) / ref
+    assert float(off.max()) <= 256 * 2.0 ** -23 + k / 4096 * 2.0 ** -24, float(off.max())

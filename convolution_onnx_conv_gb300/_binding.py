@@ -706,7 +706,7 @@ def _rows_2d(t, name):
     ld, adjacent = t.stride()
     if adjacent != 1 and c > 1:
         raise ValueError(f"{name}'s columns must be adjacent (stride 1)")
-    return r, c, (ld if r > 1 or ld > c else c)   # one row has no stride of its own
+    return r, c, (ld if r > 1 else (c + 31) // 32 * 32)   # one row has no stride of its own: an aligned one
 
 
 def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None, stream=None):
@@ -815,7 +815,7 @@ class ExpertLinear:
         self.experts, self.N, self.K, self.kblk, self.dtype = E, N, K, blocks[2], w.dtype
         self.out_dtype = torch.bfloat16 if out_bf16 else torch.float32
         d = LinearDesc(N, K, E, CONVF_LINEAR_E4M3 if self.e4m3 else CONVF_LINEAR_BF16,
-                       w.stride(1) if N > 1 else max(w.stride(1), -(-K // 16) * 16), w.stride(0), act, float(clip[0]), float(clip[1]),
+                       w.stride(1) if N > 1 else -(-K // 16) * 16, w.stride(0), act, float(clip[0]), float(clip[1]),
                        CONVF_OUT_BF16 if out_bf16 else CONVF_OUT_F32)
         self.handle = conv_fused_linear_create(d, w, w_scale, bias)
 
@@ -833,8 +833,6 @@ class ExpertLinear:
         if (y is not None and y.get_device() != self.device) \
                 or (x_scale is not None and x_scale.get_device() != self.device):
             _Torch.refuse_apart(self.device, x_scale=x_scale, y=y)
-        if rows <= 1:
-            ldx = (ldx + 15) // 16 * 16
         xs = xs_row = xs_blk = 0
         if self.e4m3:
             if x_scale is None or not x_scale.is_cuda or x_scale.dtype is not _Torch.f32 \

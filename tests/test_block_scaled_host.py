@@ -262,3 +262,18 @@ def test_an_index_that_overlaps_an_output_is_refused(where):
     with pytest.raises(cf.ConvFusedError) as e:
         cf.conv_fused_quantize_blocks(a)
     assert e.value.status == cf.CONVF_ERR_INVALID_ARG and "index and q or scale overlap" in str(e.value)
+
+
+# ------------------------------------------------------------------------------ one row has no stride
+
+def test_the_stride_of_one_row_is_not_asked_about(calls):
+    """A row out of a wider buffer, whose rows are an odd number of elements apart."""
+    import torch
+    import convolution_onnx_conv_gb300 as cf
+    bf16 = torch.bfloat16
+    layer = cf.BlockLinear(FakeCuda((1, 17), bf16, strides=(33, 1)))           # N = 1
+    assert calls[-1].ldw >= 17 and calls[-1].ldw * 2 % 16 == 0
+    layer(FakeCuda((1, 17), bf16, strides=(35, 1)), y=FakeCuda((1, 1), torch.float32, strides=(7, 1)))
+    assert calls[-1].ldx >= 17 and calls[-1].ldx * 2 % 16 == 0
+    cf.quantize_blocks(FakeCuda((1, 256), bf16, strides=(257, 1)), q=FakeCuda((1, 256), torch.float8_e4m3fn, strides=(259, 1)))
+    assert calls[-1].ldx * 2 % 32 == 0 and calls[-1].ldq % 16 == 0             # (read and written as vectors)

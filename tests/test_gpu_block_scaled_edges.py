@@ -187,3 +187,19 @@ def test_bf16_results_of_long_sums_of_one_sign(rows, n, k, form):
         ref += x[:, i:i + (1 << 14)].double() @ w[:, i:i + (1 << 14)].double().T
     off = ((y - ref).abs() - half_step(ref)) / ref
     assert float(off.max()) <= 256 * 2.0 ** -23 + k / 4096 * 2.0 ** -24, float(off.max())
+
+
+# ------------------------------------------------------------------------------ one row has no stride
+
+def test_one_row_out_of_a_buffer_of_odd_rows():
+    g = gen(2)
+    buf = torch.randn((4, 345), generator=g, device="cuda").to(torch.bfloat16)
+    base = torch.cat([buf.flatten(), buf.flatten()])
+    x = torch.as_strided(base, (1, 136), (345, 1), 8)
+    w = torch.as_strided(base, (1, 136), (345, 1), 512)
+    y = cf.BlockLinear(w)(x)
+    ref = x.double() @ w.double().T
+    assert float((y - ref).abs()) <= 140 * 2.0 ** -23 * float(x.double().abs() @ w.double().abs().T)
+    q, s = cf.quantize_blocks(x)
+    q2, s2 = cf.quantize_blocks(x.clone())
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)

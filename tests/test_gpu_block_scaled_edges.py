@@ -203,3 +203,63 @@ def test_one_row_out_of_a_buffer_of_odd_rows():
     q, s = cf.quantize_blocks(x)
     q2, s2 = cf.quantize_blocks(x.clone())
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("k", [1000, 4096])
+@pytest.mark.parametrize("rows,n", [(5, 512), (300, 512), (2100, 2048)])
+def test_fp32_results_of_bf16_operands_in_the_norm(rows, n, k):
+    """256 products in the tensor core (16 additions, each off by at most 2^-23 of what is there: with signs at
+    random and sizes that grow as the root, (1/2 + ... )^(1/2) of that in the mean square), the sums of 256
+    added to nearest: 3e-7 of the result is seen, 6e-7 asked for.  Without the sums of 256: 1.2e-6."""
+    g = gen(k + rows)
+    wide = -(-k // 8) * 8
+    x = torch.randn((rows, wide), generator=g, device="cuda").to(torch.bfloat16)[:, :k]
+    w = torch.randn((n, wide), generator=g, device="cuda").to(torch.bfloat16)[:, :k]
+    ref = x.double() @ w.double().T
+    y = cf.BlockLinear(w)(x).double()
+    assert float((y - ref).norm() / ref.norm()) < 6e-7
+
+
+# ------------------------------------------------------------------------------ every split of the few-rows kernel
+
+# a size (rows, experts, N, K) whose plan is each form that the plan can give
+PLANS = {(True, 16, 1): (61, 1, 300, 520), (True, 16, 2): (300, 1, 136, 4112), (True, 16, 4): (9, 1, 72, 4112),
+         (True, 16, 8): (5, 1, 72, 14352), (True, 32, 1): (530, 1, 2061, 130), (True, 32, 2): (1061, 8, 136, 8208),
+         (True, 32, 4): (530, 1, 136, 14352), (True, 32, 8): (130, 1, 136, 30000), (True, 64, 1): (530, 1, 1032, 130),
+         (True, 64, 2): (530, 1, 520, 8208), (True, 64, 4): (300, 1, 520, 8208), (True, 64, 8): (300, 1, 136, 14352),
+         (False, 16, 1): (61, 1, 300, 264), (False, 16, 2): (300, 1, 136, 2064), (False, 16, 4): (9, 1, 72, 2064),
+         (False, 16, 8): (5, 1, 72, 8208), (False, 32, 1): (530, 1, 520, 130), (False, 32, 2): (300, 1, 520, 4112),
+         (False, 32, 4): (300, 1, 136, 8208), (False, 32, 8): (130, 1, 136, 14352), (False, 64, 1): (530, 1, 1032, 130),
+         (False, 64, 2): (530, 1, 520, 8208), (False, 64, 4): (300, 1, 520, 8208), (False, 64, 8): (300, 1, 136, 16400)}
+
+
+@pytest.mark.parametrize("e4m3,tile,split", PLANS)
+def test_every_split_is_exact_on_integers(e4m3, tile, split):
+    """Integers times powers of two, whose every sum is exact: 4 * 2 * 30000 * 4 below 2^20, in quarters."""
+    rows, e, n, k = PLANS[e4m3, tile, split]
+    g = gen(rows + k)
+    dtype, kb = (torch.float8_e4m3fn if e4m3 else torch.bfloat16), -(-k // 128)
+    x = torch.randint(-4, 5, (rows, k), generator=g, device="cuda").float()
+    w = torch.randint(-2, 3, (e, n, k), generator=g, device="cuda").float()
+    bias = torch.randint(-3, 4, (e, n), generator=g, device="cuda").float()
+    rx, rw, xs, ws = x.double(), w.double(), None, None
+    if e4m3:
+        xs = 2.0 ** torch.randint(-1, 2, (rows, kb), generator=g, device="cuda").float()
+        ws = 2.0 ** torch.randint(-1, 2, (e, -(-n // 128), kb), generator=g, device="cuda").float()
+        rx = rx * xs.double().repeat_interleave(128, 1)[:, :k]
+        rw = rw * ws.double().repeat_interleave(128, 2)[..., :k].repeat_interleave(128, 1)[:, :n]
+
+    def aligned(t):
+        wide = torch.zeros((*t.shape[:-1], -(-k // 16) * 16), device="cuda")
+        wide[..., :k] = t
+        return wide.to(dtype)[..., :k]
+
+    off = torch.tensor([rows * i // e for i in range(e + 1)], dtype=torch.int32, device="cuda")
+    ref = torch.cat([rx[int(off[i]):int(off[i + 1])] @ rw[i].T + bias[i].double() for i in range(e)])
+    for out_bf16 in (False, True):
+        lin = cf.ExpertLinear(aligned(w), ws, bias=bias, act=cf.CONVF_ACT_RELU, out_bf16=out_bf16)
+        assert f"few_rows tile={tile}x128 split={split} " in lin.describe(rows)
+        y = lin(aligned(x), off, xs)
+        torch.cuda.synchronize()
+        assert lin.status() == cf.CONVF_OK, cf.conv_fused_last_error()
+        assert torch.equal(y.double(), ref.clamp(min=0).to(lin.out_dtype).double())

@@ -24,9 +24,13 @@ class ExpertFeedForward:
 
     def __init__(self, w_gate_up, w_down):
         def layer(w):
-            parts = [cf.quantize_blocks(m, block_rows=128) for m in w]
-            q = torch.stack([p[0].view(torch.uint8) for p in parts]).view(torch.float8_e4m3fn)
-            return cf.ExpertLinear(q, torch.stack([p[1] for p in parts]), out_bf16=True)
+            experts, n, k = w.shape
+            wide = -(-k // 16) * 16   # rows of a layer's weights lie a multiple of 16 bytes apart
+            q = torch.empty_strided((experts, n, k), (n * wide, wide, 1), dtype=torch.float8_e4m3fn, device=w.device)
+            scale = torch.empty((experts, -(-n // 128), -(-k // 128)), device=w.device)
+            for e in range(experts):
+                cf.quantize_blocks(w[e], block_rows=128, q=q[e], scale=scale[e])
+            return cf.ExpertLinear(q, scale, out_bf16=True)
 
         self.experts = w_gate_up.shape[0]
         self.up, self.down = layer(w_gate_up), layer(w_down)

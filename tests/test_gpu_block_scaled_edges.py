@@ -263,3 +263,18 @@ def test_every_split_is_exact_on_integers(e4m3, tile, split):
         torch.cuda.synchronize()
         assert lin.status() == cf.CONVF_OK, cf.conv_fused_last_error()
         assert torch.equal(y.double(), ref.clamp(min=0).to(lin.out_dtype).double())
+
+
+# ------------------------------------------------------------------------------ the experts' example
+
+@pytest.mark.parametrize("tokens,experts,width,hidden,top", [(9, 3, 100, 75, 2), (200, 4, 1000, 333, 1)])
+def test_expert_example_at_odd_sizes(tokens, experts, width, hidden, top):
+    """Widths that are no multiple of 16: the weights' rows are padded.  (The bound is that of the quantising:
+    four operands of 3 fraction bits, 2.6% each in the norm, 5.2% together; 10% is asked for.)"""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from expert_feed_forward import example
+    y, ref, layer, args = example(tokens, experts, width, hidden, top, seed=tokens)
+    assert layer.up.status() == cf.CONVF_OK and layer.down.status() == cf.CONVF_OK
+    assert float((y - ref).norm() / ref.norm()) < 0.10

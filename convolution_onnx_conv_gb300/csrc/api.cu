@@ -58,13 +58,6 @@ bool injected_alloc_failure() {
   return false;
 }
 
-struct LiveHandleCount {
-  LiveHandleCount() { g_live_handles.fetch_add(1); }
-  LiveHandleCount(const LiveHandleCount&) { g_live_handles.fetch_add(1); }
-  LiveHandleCount& operator=(const LiveHandleCount&) = default;
-  ~LiveHandleCount() { g_live_handles.fetch_sub(1); }
-};
-
 convf_status fail(convf_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -2182,6 +2175,9 @@ convf_status record_error(convf_status st, const char* fmt, ...) {
 }
 convf_status record_ok() { return ok(); }
 bool take_injected_alloc_failure() { return injected_alloc_failure(); }
+LiveHandleCount::LiveHandleCount() { g_live_handles.fetch_add(1); }
+LiveHandleCount::LiveHandleCount(const LiveHandleCount&) { g_live_handles.fetch_add(1); }
+LiveHandleCount::~LiveHandleCount() { g_live_handles.fetch_sub(1); }
 
 bool tensor_map_encoders(EncodeTiledFn* tiled, EncodeIm2colFn* im2col) {
   if (!load_encoders()) return false;

@@ -42,6 +42,7 @@ convf_status current_device(int* dev, int* num_sms) {
 }  // namespace
 
 struct convf_linear {
+  LiveHandleCount live;
   uint32_t magic;
   CUtensorMap tmW64, tmW128, tmW256;   // boxes of 64, 128 and 256 weight rows
   int device, num_sms;

@@ -334,8 +334,8 @@ convf_status conv_fused_watchdog_selftest(int32_t* status_dev, long long budget_
  * conv_fused_last_error message ends in "(injected)".  The hook then disarms itself; n = 0
  * disarms it at once; a negative n is CONVF_ERR_INVALID_ARG.  Process-wide, for tests: calls
  * on other threads in the meantime draw on the same count.
- * conv_fused_debug_live_handles returns how many convf_handles exist (created and not yet
- * destroyed), so a test can check that a failed create left nothing behind. */
+ * conv_fused_debug_live_handles returns how many convf_handles and convf_linears exist (created
+ * and not yet destroyed), so a test can check that a failed create left nothing behind. */
 convf_status conv_fused_debug_fail_alloc(int n);
 int conv_fused_debug_live_handles(void);
 

@@ -278,3 +278,20 @@ def test_expert_example_at_odd_sizes(tokens, experts, width, hidden, top):
     y, ref, layer, args = example(tokens, experts, width, hidden, top, seed=tokens)
     assert layer.up.status() == cf.CONVF_OK and layer.down.status() == cf.CONVF_OK
     assert float((y - ref).norm() / ref.norm()) < 0.10
+
+
+# ------------------------------------------------------------------------------ layers in existence
+
+def test_a_failed_create_leaves_no_layer_behind():
+    w = torch.zeros((32, 64), dtype=torch.bfloat16, device="cuda")
+    live = cf.conv_fused_debug_live_handles()
+    lin = cf.BlockLinear(w)
+    assert cf.conv_fused_debug_live_handles() == live + 1
+    for n in (1, 2):   # the layer, its device words
+        cf.conv_fused_debug_fail_alloc(n)
+        with pytest.raises(cf.ConvFusedError) as e:
+            cf.BlockLinear(w)
+        assert e.value.status == cf.CONVF_ERR_OOM and "(injected)" in str(e.value)
+        assert cf.conv_fused_debug_live_handles() == live + 1
+    lin.close()
+    assert cf.conv_fused_debug_live_handles() == live

@@ -295,3 +295,42 @@ def test_a_failed_create_leaves_no_layer_behind():
         assert cf.conv_fused_debug_live_handles() == live + 1
     lin.close()
     assert cf.conv_fused_debug_live_handles() == live
+
+
+# ------------------------------------------------------------------------------ behind a conv
+
+def test_a_conv_feeds_the_quantiser_and_a_layer():
+    """conv -> quantise -> linear over the same buffers without a wait between them: a conv's channels-last
+    output is a matrix of rows, and each kernel begins while the one before still runs."""
+    g = torch.Generator().manual_seed(9)
+    N, C, H, K, n = 2, 32, 20, 64, 200
+    wc = (torch.randn((K, C, 3, 3), generator=g) / 17).to(torch.bfloat16)
+    xs = [torch.randn((N, C, H, H), generator=g).to(torch.bfloat16).contiguous(memory_format=torch.channels_last).cuda()
+          for _ in range(3)]
+    for out_bf16 in (False, True):
+        conv = cf.FusedConv(N, C, H, H, K, 3, 3, wc, None, pads=(1, 1, 1, 1), act=cf.CONVF_ACT_RELU, out_bf16=out_bf16)
+        wq, ws = cf.quantize_blocks(torch.randn((n, K), generator=g).cuda(), block_rows=128)
+        lin = cf.BlockLinear(wq, ws, out_bf16=True)
+        y = conv.new_output()
+        rows = y.permute(0, 2, 3, 1).reshape(N * H * H, K)
+        assert rows.data_ptr() == y.data_ptr()
+        want = []
+        for x in xs:
+            conv(x, y)
+            torch.cuda.synchronize()
+            q, s = cf.quantize_blocks(rows)
+            torch.cuda.synchronize()
+            want.append(lin(q, s))
+            torch.cuda.synchronize()
+            ref = torch.nn.functional.conv2d(x.float(), wc.cuda().float(), padding=1).clamp(min=0)
+            ref = ref.permute(0, 2, 3, 1).reshape(-1, K).double()
+            back = q.double() * s.double().repeat_interleave(128, 1)[:, :K]
+            # half a step of e4m3, of the value or of the smallest, and a bf16 rounding before
+            assert bool(((back - ref).abs() <= ref * (2.0 ** -4 + 2.0 ** -7) + s.double() * 2.0 ** -9 + 1e-5).all())
+        got = []
+        for t in range(90):
+            conv(xs[t % 3], y)
+            cf.quantize_blocks(rows, q=q, scale=s)
+            got.append(lin(q, s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[t], want[t % 3]) for t in range(90))

@@ -717,7 +717,8 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     ``index`` (int32, CUDA) takes the rows x[index] instead (an entry outside x gives a row of zeros);
     ``gated=True`` takes x as [rows][2*cols] and quantises g / (1 + exp(-g)) * u of its halves g and
     u.  Rows of q lie a multiple of 16 bytes apart, as the layers read them; ``q`` and ``scale`` may
-    be given.  Runs on the current torch stream, or on ``stream`` (a torch stream or a cudaStream_t)."""
+    be given; all tensors are on the current device.  Runs on the current torch stream, or on ``stream``
+    (a torch stream or a cudaStream_t)."""
     T = _Torch
     if not T.ready:
         T.bind()
@@ -784,7 +785,7 @@ class ExpertLinear:
 
     ``w``: CUDA [experts][N][K], bf16 or float8_e4m3fn, read in place (rows and experts a multiple
     of 16 bytes apart); ``w_scale`` (e4m3) fp32 [experts][ceil(N/128)][ceil(K/128)]; ``bias`` fp32
-    [experts][N] or None; ``act`` and ``clip`` as for a conv; y is fp32, or bf16 with ``out_bf16``.
+    [experts][N] or None (both in place too where they are contiguous); all on the current device; ``act`` and ``clip`` as for a conv; y is fp32, or bf16 with ``out_bf16``.
     Calling it runs on the current torch stream."""
 
     def __init__(self, w, w_scale=None, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
@@ -861,7 +862,8 @@ class ExpertLinear:
     def __call__(self, x, offsets, x_scale=None, y=None, stream=None):
         """y [rows][N] for ``x`` [rows][K] (w's type; rows a multiple of 16 bytes apart), ``offsets``
         int32 CUDA [experts+1] and, for e4m3, ``x_scale`` fp32 [rows][ceil(K/128)] (any strides).
-        Rows that no expert takes are not written."""
+        Rows that no expert takes are not written, and none at all with offsets that decrease or pass
+        the rows (``status`` reports those)."""
         if not offsets.is_cuda or offsets.dtype is not _Torch.i32 or offsets.shape != (self.experts + 1,) \
                 or not offsets.is_contiguous():
             raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {self.experts + 1}")

@@ -6,8 +6,9 @@
 // The definition's quotient is the float32 one, rounded again to e4m3.  A division per value made the
 // kernel execute 34 instructions per value and bound it by those; here the block's scale has its
 // reciprocal taken once, and each value a product and one correction by its remainder: 9 to 11
-// instructions per value, more than half of them per block.  100352 x 256 fp32: 21.0 us, 6.1 TB/s; bf16,
-// with half the bytes per value, is bound by the instructions: 8192 x 2048 gated 17.2 us.
+// instructions per value, more than half of them per block.  100352 x 256 fp32: 20.8 us, 6.2 TB/s; bf16,
+// with half the bytes per value, is bound by the instructions: 8192 x 2048 gated 17.4 us (calls one behind
+// another; 20.3 and 15.3 from a graph).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -336,7 +337,8 @@ __global__ void __launch_bounds__(256, kRowsPerSm<T, GATED>) quantize_rows_kerne
 
 // Scales per 128 x 128 block: a CTA of 512 threads takes one at a time, 2 rows of 16 elements per thread,
 // held in registers between the maximum and the division; the next block is on its way meanwhile.  (256
-// threads of 64 elements need 120 registers, 16 warps on an SM: 1 us more.  5000 x 4100 bf16: 12.2 us.)
+// threads of 64 elements need 120 registers, 16 warps on an SM: 1 us more.  5000 x 4100 bf16: 13.8 us, 11.4
+// from a graph.)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const QuantParams p) {
   typedef typename RawOf<T>::type Raw;

@@ -128,7 +128,8 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   // 1024 to 4096: waves of tiles, each its k-blocks' time and a start and end, behind a launch; or the
   // bytes, at 6.3 TB/s, if that is more.  (2048 x 2048 layers, 16 experts, e4m3: 64 rows few/16 15.4 us,
   // many/128 16.2; 512 rows 21.3, 16.6; 4096 x 4096 layer: 48 rows few/16 12.5 us, few/64 14.0, many/256
-  // 15.7; 2048 rows of 2048 x 2048 few/64 29 us, many/128 12.5.)
+  // 15.7; 2048 rows of 2048 x 2048 few/64 29 us, many/128 12.5.)  Over 34 sizes the choice takes at most 5%
+  // more than the best form.
   LinearPlan plan{};
   long long best = -1;
   const long long esz = e4m3 ? 1 : 2;

@@ -36,7 +36,9 @@ constexpr int kTileBatch = 16;   // tiles that the scheduler works out at a time
 template <bool PAIR>
 struct ManyCfg {
   static constexpr int kThreads = 384;
-  // registers: 168 per thread at launch; the epilogue's two warpgroups take what the third gives up
+  // registers: 168 per thread at launch; the epilogue's two warpgroups take what the third gives up.  (The
+  // PLAIN kernels spill 8 to 16 bytes of the tile ends' state: 12 thousand local loads for the 256 tiles of
+  // 4096 x 4096 in e4m3, whether K is 1024 or 4096, so none of them in the loop over k.)
   static constexpr int kRegs = 168, kRegsEpi = 224, kRegsOther = 56;
   static_assert(256 * kRegsEpi + 128 * kRegsOther <= kThreads * kRegs, "register split");
   static constexpr int kTileM = PAIR ? 256 : 128;

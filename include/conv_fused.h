@@ -462,7 +462,8 @@ typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1 } convf_linear_dtype
  * with s(r) = index[r], or r without an index,
  *   scale[i][b] = max |v| over the block / 448        (float32, round to nearest)
  *   q[r][c] = e4m3(clamp(v[r][c] / scale, -448, 448)) (float32 quotient, then nearest, ties to even)
- * and q = 0 where the scale is 0 (a block of zeros, or of values so small that it underflows).
+ * and q = +0 where the scale is 0 (a block of zeros, or of values so small that it underflows);
+ * other zeros have the quotient's sign.
  * A NaN in a block makes its scale and its values NaN; an infinity makes the scale infinite, so
  * that every value of the block reads back as NaN. */
 typedef struct {
@@ -484,7 +485,8 @@ typedef struct {
 } convf_quant_args;
 
 /* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row
- * stride of at least a row is served; rows that begin on 16 bytes are read and written as vectors.
+ * stride of at least a row is served; rows that begin on 8 bytes are read and written as vectors (of
+ * 32 and 16 bytes where they begin on those).
  * q and scale must not overlap x, index or each other; rows of two of them that are the same
  * distance apart may lie between each other's (columns of one buffer). */
 convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
@@ -535,11 +537,11 @@ typedef struct {
  * order of every sum depends on the sizes and the row groups only: results repeat bit for bit. */
 convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, void* stream);
 /* Device status of earlier runs (read after the caller synchronised): CONVF_OK, CONVF_ERR_TIMEOUT,
- * or CONVF_ERR_INVALID_ARG for offsets that decreased or passed the rows; sticky until
+ * (bounds-checking build) CONVF_ERR_BOUNDS, or CONVF_ERR_INVALID_ARG for offsets that decreased or passed the rows; sticky until
  * conv_fused_linear_clear_status. */
 convf_status conv_fused_linear_status(convf_linear* l);
 convf_status conv_fused_linear_clear_status(convf_linear* l);
-/* One line: what a run of this many rows launches. */
+/* One line: what a run of this many rows launches (asked on the layer's device). */
 convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* buf, size_t len);
 /* Frees the layer's device memory (the caller must have synchronised); NULL is ignored. */
 void conv_fused_linear_destroy(convf_linear* l);

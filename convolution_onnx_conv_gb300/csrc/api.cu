@@ -19,6 +19,7 @@
 #include "../../include/conv_fused.h"
 #include "api_internal.h"
 #include "convf_internal.h"
+#include "live_handles.h"
 
 namespace convf {
 // defined once per tile width in tc_conv_inst.cu

@@ -15,13 +15,6 @@ convf_status record_error(convf_status st, const char* fmt, ...);
 convf_status record_ok();
 // conv_fused_debug_fail_alloc's countdown: true when the allocation about to be made is to fail.
 bool take_injected_alloc_failure();
-// A member of every handle and layer, which counts those in existence (conv_fused_debug_live_handles).
-struct LiveHandleCount {
-  LiveHandleCount();
-  LiveHandleCount(const LiveHandleCount&);
-  LiveHandleCount& operator=(const LiveHandleCount&) = default;
-  ~LiveHandleCount();
-};
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

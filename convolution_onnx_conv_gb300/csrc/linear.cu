@@ -12,6 +12,7 @@
 #include "api_internal.h"
 #include "convf_internal.h"
 #include "linear_internal.h"
+#include "live_handles.h"
 
 using namespace convf;
 

@@ -366,6 +366,7 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   // at K = 131072, and a whole step of bf16 from about 10^6)
   p.chunk_kb = e4m3 ? 1 : osz == 2 ? 64 : 4;
   p.vec_y = aligned(a->y, 16) && a->ldy * osz % 16 == 0;
+  p.whole_units = p.vec_y && d.N * osz % 16 == 0;
   p.x_scale = a->x_scale; p.xs_row = a->xs_row; p.xs_blk = a->xs_blk; p.w_scale = l->w_scale; p.bias = l->bias;
   p.offsets = a->offsets; p.y = a->y; p.ldy = a->ldy; p.out_bf16 = d.out_dtype == CONVF_OUT_BF16;
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;

@@ -75,6 +75,7 @@ struct LinearParams {
   int num_kb;                // k-blocks of 128 bytes
   int chunk_kb;              // k-blocks that an MMA accumulator sums before its sum goes to the registers'
   int vec_y;                 // y's rows begin on 16 bytes
+  int whole_units;           // and end on 16 bytes too
   int n_tiles;               // weight-row tiles of the chosen form
   const float* x_scale;
   long long xs_row, xs_blk;

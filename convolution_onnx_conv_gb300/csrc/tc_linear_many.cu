@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       }
       if (mrow >= q.rows || n0 >= p.N) continue;
       uint8_t* out = sOut + warp * Cfg::kOutBytes;
-      // Whole warps' rows leave by TMA (which clips the columns past N) while the next tile's sums begin:
-      // the stores of all SMs at once, waited for, cost 4700 cycles a tile.  bf16 results are clamped after
+      // Whole warps' rows leave by TMA while the next tile's sums begin: the stores of all SMs at once, waited
+      // for, cost 4700 cycles a tile.  (A TMA store clips the columns past N by units of 16 bytes and would
+      // write over what follows rows that end inside one.)  bf16 results are clamped after
       // the rounding, which is monotonic: the bounds, rounded, give the same values, and the sums' pairs
       // stay whole.
       const uint32_t lo = bf16_pair(p.lo, p.lo), hi = bf16_pair(p.hi, p.hi);
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
       };
-      if (PLAIN && mrow + 32 <= q.rows) {
+      if (PLAIN && mrow + 32 <= q.rows && (p.whole_units || n0 + 128 <= p.N)) {
         auto chunk_unit = [&](int c, int u) {
           return reinterpret_cast<uint4*>(out + (c % Cfg::kOutChunks) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4));
         };
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
           }
         }
       } else if (PLAIN) {
-        // a group's last rows: each lane its own row
+        // a group's last rows, or rows that end inside 16 bytes: each lane its own row
         if (mrow + lane < q.rows && CONVF_IN_BOUNDS(q.row0 + mrow + lane < p.rows, p.status)) {
           const long long at = static_cast<long long>(q.row0 + mrow + lane) * p.ldy + n0;
           if (p.out_bf16) {

@@ -459,6 +459,7 @@ typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1 } convf_linear_dtype
  * in float32:
  *   v[r][c] = x[s(r)][c]                              (gated = 0)
  *   v[r][c] = g / (1 + exp(-g)) * u, g = x[s(r)][c], u = x[s(r)][cols + c]   (gated = 1)
+ *             (float32 operations, the reciprocal within a unit in the last place)
  * with s(r) = index[r], or r without an index,
  *   scale[i][b] = max |v| over the block / 448        (float32, round to nearest)
  *   q[r][c] = e4m3(clamp(v[r][c] / scale, -448, 448)) (float32 quotient, then nearest, ties to even)

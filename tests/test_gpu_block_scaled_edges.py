@@ -334,3 +334,47 @@ def test_a_conv_feeds_the_quantiser_and_a_layer():
             got.append(lin(q, s))
         torch.cuda.synchronize()
         assert all(torch.equal(got[t], want[t % 3]) for t in range(90))
+
+
+# ------------------------------------------------------------------------------ what lies beside y's rows
+
+@pytest.mark.parametrize("n", [1003, 2049, 2061, 2056])
+@pytest.mark.parametrize("rows", [5, 70, 4100])
+@pytest.mark.parametrize("out_bf16", [True, False])
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_columns_beside_aligned_rows_of_y_are_kept(n, rows, out_bf16, e4m3):
+    """Rows of y that begin on 16 bytes and end inside 16: whole tiles leave by TMA, whose stores are clipped by
+    units of 16 bytes only."""
+    g, k = gen(n + rows), 272
+    x = torch.randint(-4, 5, (rows, k), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randint(-2, 3, (n, k), generator=g, device="cuda").to(torch.bfloat16)
+    ref, xs, ws = x.double() @ w.double().T, None, None
+    if e4m3:
+        x, w = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+        xs, ws = torch.ones((rows, 3), device="cuda"), torch.ones((-(-n // 128), 3), device="cuda")
+    for bias in (None, torch.randint(-3, 4, (n,), generator=g, device="cuda").float()):
+        lin = cf.BlockLinear(w, ws, bias=bias, out_bf16=out_bf16)
+        wide = (n + 15) // 16 * 16 + 16
+        buf = torch.full((rows + 2, wide), -7.0, dtype=lin.out_dtype, device="cuda")
+        lin(x, xs, y=buf[1:rows + 1, :n])
+        torch.cuda.synchronize()
+        assert lin.status() == cf.CONVF_OK
+        want = ref if bias is None else ref + bias.double()
+        assert torch.equal(buf[1:rows + 1, :n].double(), want.to(lin.out_dtype).double())
+        assert bool((buf[:, n:] == -7).all()) and bool((buf[0] == -7).all()) and bool((buf[-1] == -7).all())
+
+
+@pytest.mark.parametrize("cols", [203, 209, 1000, 1017])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_columns_beside_aligned_rows_of_q_are_kept(cols, dtype, block_rows):
+    rows, wide = 131, (cols + 31) // 32 * 32 + 32
+    x = torch.randn((rows, wide), generator=gen(cols), device="cuda").to(dtype)[:, :cols]
+    qb = torch.full((rows + 2, wide), 0x55, dtype=torch.uint8, device="cuda")
+    sb = torch.full((rows + 2, -(-cols // 128) + 1), -7.0, device="cuda")
+    srows, nb = -(-rows // block_rows), -(-cols // 128)
+    cf.quantize_blocks(x, block_rows=block_rows, q=qb[1:rows + 1, :cols].view(torch.float8_e4m3fn), scale=sb[1:srows + 1, :nb])
+    q, s = cf.quantize_blocks(x.contiguous(), block_rows=block_rows)
+    assert torch.equal(qb[1:rows + 1, :cols], q.view(torch.uint8)) and torch.equal(sb[1:srows + 1, :nb], s)
+    assert bool((qb[:, cols:] == 0x55).all()) and bool((qb[0] == 0x55).all()) and bool((qb[-1] == 0x55).all())
+    assert bool((sb[:, nb:] == -7).all()) and bool((sb[0] == -7).all()) and bool((sb[srows + 1:] == -7).all())

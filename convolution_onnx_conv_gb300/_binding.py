@@ -27,7 +27,7 @@ CONVF_VARIANT_AUTO, CONVF_VARIANT_IMPLICIT_GEMM, CONVF_VARIANT_GEMM_1X1, CONVF_V
 VARIANT_NAMES = {0: "auto", 1: "implicit_gemm_im2col", 2: "gemm_1x1", 3: "depthwise",
                  4: "int8_mma", 5: "implicit_gemm_gather", 6: "implicit_gemm_window", 7: "implicit_gemm_halo",
                  8: "int8_tcgen05_exact", 9: "grouped_direct", 10: "mbv2_block"}
-CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3 = 0, 1
+CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3, CONVF_LINEAR_INT8 = 0, 1, 2
 AUTO_PAD = {"NOTSET": 0, "SAME_UPPER": 1, "SAME_LOWER": 2, "VALID": 3}
 
 EXPORTED = ["conv_fused_output_shape", "conv_fused_resolve_pads", "conv_bn_scale_shift",
@@ -41,7 +41,7 @@ EXPORTED = ["conv_fused_output_shape", "conv_fused_resolve_pads", "conv_bn_scale
             "conv_fused_chain_clear_status", "conv_fused_chain_describe", "conv_fused_chain_destroy",
             "conv_fused_quantize_blocks", "conv_fused_linear_create", "conv_fused_linear_run",
             "conv_fused_linear_status", "conv_fused_linear_clear_status", "conv_fused_linear_describe",
-            "conv_fused_linear_destroy"]
+            "conv_fused_linear_destroy", "conv_fused_quantize_rows", "conv_fused_rms_norm_quantize"]
 
 
 class ConvDesc(ctypes.Structure):
@@ -74,6 +74,23 @@ class QuantArgs(ctypes.Structure):
                 ("x_rows", ctypes.c_int), ("ldx", ctypes.c_longlong), ("index", ctypes.c_void_p),
                 ("gated", ctypes.c_int), ("block_rows", ctypes.c_int), ("q", ctypes.c_void_p),
                 ("ldq", ctypes.c_longlong), ("scale", ctypes.c_void_p), ("lds", ctypes.c_longlong)]
+
+
+class QuantRowsArgs(ctypes.Structure):
+    """convf_quant_rows_args: what conv_fused_quantize_rows reads and writes."""
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int),
+                ("x_rows", ctypes.c_int), ("ldx", ctypes.c_longlong), ("index", ctypes.c_void_p),
+                ("gated", ctypes.c_int), ("q", ctypes.c_void_p), ("ldq", ctypes.c_longlong), ("scale", ctypes.c_void_p)]
+
+
+class NormArgs(ctypes.Structure):
+    """convf_norm_args: what conv_fused_rms_norm_quantize reads and writes."""
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int),
+                ("ldx", ctypes.c_longlong), ("residual", ctypes.c_void_p), ("residual_dtype", ctypes.c_int),
+                ("ldr", ctypes.c_longlong), ("h", ctypes.c_void_p), ("ldh", ctypes.c_longlong),
+                ("weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("out", ctypes.c_int), ("q", ctypes.c_void_p), ("ldq", ctypes.c_longlong), ("scale", ctypes.c_void_p),
+                ("lds", ctypes.c_longlong)]
 
 
 class LinearDesc(ctypes.Structure):
@@ -191,6 +208,8 @@ def load_library(build_if_missing: bool = False):
     lib.conv_fused_chain_destroy.argtypes = [vp]
     lib.conv_fused_chain_destroy.restype = None
     lib.conv_fused_quantize_blocks.argtypes = [P(QuantArgs), vp]
+    lib.conv_fused_quantize_rows.argtypes = [P(QuantRowsArgs), vp]
+    lib.conv_fused_rms_norm_quantize.argtypes = [P(NormArgs), vp]
     lib.conv_fused_linear_create.argtypes = [P(LinearDesc), vp, vp, vp, P(vp)]
     lib.conv_fused_linear_run.argtypes = [vp, P(LinearArgs), vp]
     lib.conv_fused_linear_status.argtypes = [vp]
@@ -416,6 +435,16 @@ def conv_fused_chain_destroy(chain: int):
 def conv_fused_quantize_blocks(args: QuantArgs, stream=None):
     s = stream.cuda_stream if stream is not None and hasattr(stream, "cuda_stream") else stream
     _check(load_library().conv_fused_quantize_blocks(ctypes.byref(args), s))
+
+
+def conv_fused_quantize_rows(args: QuantRowsArgs, stream=None):
+    s = stream.cuda_stream if stream is not None and hasattr(stream, "cuda_stream") else stream
+    _check(load_library().conv_fused_quantize_rows(ctypes.byref(args), s))
+
+
+def conv_fused_rms_norm_quantize(args: NormArgs, stream=None):
+    s = stream.cuda_stream if stream is not None and hasattr(stream, "cuda_stream") else stream
+    _check(load_library().conv_fused_rms_norm_quantize(ctypes.byref(args), s))
 
 
 def conv_fused_linear_create(desc: LinearDesc, W, w_scale=None, bias=None) -> int:
@@ -670,6 +699,7 @@ class _Torch:
     def bind(cls):
         import torch
         cls.bf16, cls.f32, cls.e4m3, cls.i32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+        cls.i8 = torch.int8
         cls.empty, cls.empty_strided, cls.cuda = torch.empty, torch.empty_strided, torch.cuda
         # the public call builds a Stream object (2 us of a 10 us call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -677,6 +707,8 @@ class _Torch:
         raw = getattr(torch._C, "_cuda_getDevice", None)
         cls.current_device = raw if raw is not None else torch.cuda.current_device
         cls.quantize = load_library().conv_fused_quantize_blocks
+        cls.quantize_rows = load_library().conv_fused_quantize_rows
+        cls.norm = load_library().conv_fused_rms_norm_quantize
         cls.run = load_library().conv_fused_linear_run
         cls.ready = True
 
@@ -777,6 +809,143 @@ def quantize_blocks(x, index=None, gated=False, block_rows=1, q=None, scale=None
     if st != CONVF_OK:
         _check(st)
     return q, scale
+
+
+def _kind(t, name):
+    """convf_out_dtype of a tensor."""
+    if t.dtype is _Torch.bf16:
+        return CONVF_OUT_BF16
+    if t.dtype is _Torch.f32:
+        return CONVF_OUT_F32
+    raise ValueError(f"{name} must be bf16 or fp32")
+
+
+def _bytes_like(q, rows, cols, dtype, device):
+    """(tensor, row stride) of the 8-bit values [rows][cols]: `q` if given, or new rows a multiple of 16 bytes apart."""
+    if q is None:
+        ldq = (cols + 15) // 16 * 16
+        return (_Torch.empty((rows, cols), dtype=dtype, device=device) if ldq == cols else
+                _Torch.empty_strided((rows, cols), (ldq, 1), dtype=dtype, device=device)), ldq
+    qr, qc, ldq = _rows_2d(q, "q")
+    if q.dtype is not dtype or qr != rows or qc != cols:
+        raise ValueError(f"q must be {dtype} of shape ({rows}, {cols})")
+    return q, ldq
+
+
+def _row_scales(scale, rows, device):
+    """A scale per row: `scale` if given, or a new vector."""
+    if scale is None:
+        return _Torch.empty((rows,), dtype=_Torch.f32, device=device)
+    if not scale.is_cuda or scale.dtype is not _Torch.f32 or scale.shape != (rows,) or not scale.is_contiguous():
+        raise ValueError(f"scale must be a contiguous CUDA float32 vector of {rows}")
+    return scale
+
+
+def quantize_rows(x, index=None, gated=False, q=None, scale=None, stream=None):
+    """(q, scale): the rows of ``x`` (CUDA, bf16 or fp32, [rows][cols], any row stride) as int8 values in
+    -127 .. 127 and a float scale per row; x is about q * scale[:, None].  A layer's weights [N][K] are
+    quantised by the same call: a scale per output channel.
+
+    ``index``, ``gated``, ``q`` and ``stream`` as for quantize_blocks; ``scale`` [rows] may be given."""
+    T = _Torch
+    if not T.ready:
+        T.bind()
+    if stream is not None and x.is_cuda and (q is None or scale is None):
+        with T.on(stream, x.device):   # outputs belong to the stream that writes them
+            return quantize_rows(x, index, gated, q, scale)
+    rows, cols, ldx = _rows_2d(x, "x")
+    on = x.get_device()
+    if on != T.current_device():
+        raise ValueError(f"x is on device {on}, the current device is {T.current_device()}")
+    if (q is not None and q.get_device() != on) or (scale is not None and scale.get_device() != on) \
+            or (index is not None and index.get_device() != on):
+        T.refuse_apart(on, index=index, q=q, scale=scale)
+    xr, kind = rows, _kind(x, "x")
+    if gated:
+        if cols % 2:
+            raise ValueError("gated rows have an even number of columns")
+        cols //= 2
+    where = None
+    if index is not None:
+        if not index.is_cuda or index.dtype is not T.i32 or index.dim() != 1 or not index.is_contiguous():
+            raise ValueError("index must be a contiguous int32 CUDA vector")
+        rows, where = index.shape[0], index.data_ptr()
+    device = x.device
+    q, ldq = _bytes_like(q, rows, cols, T.i8, device)
+    scale = _row_scales(scale, rows, device)
+    if stream is None:
+        stream = T.stream(on)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = T.quantize_rows(ctypes.byref(QuantRowsArgs(rows, cols, x.data_ptr(), kind, xr, ldx, where, 1 if gated else 0,
+                                                    q.data_ptr(), ldq, scale.data_ptr())), stream)
+    if st != CONVF_OK:
+        _check(st)
+    return q, scale
+
+
+def rms_norm_quantize(x, weight=None, eps=1e-6, residual=None, int8=False, q=None, scale=None, h=None, stream=None):
+    """(q, scale), or (q, scale, h) with a ``residual``: with h = x + residual (x without one), the rows
+    h / sqrt(mean(h^2) + eps) * weight as e4m3 values with a scale per row and 128 columns, or with
+    ``int8=True`` as int8 values with a scale per row; h, in the residual's type, is the sum for the next
+    residual.
+
+    ``x`` and ``residual``: CUDA, bf16 or fp32 (each its own), [rows][cols], any row stride; ``weight``
+    [cols] bf16 or fp32, or None.  ``q``, ``scale`` and ``h`` may be given; ``h`` may be the residual itself
+    (or x, of the residual's type), to be overwritten.  All tensors are on the current device.  Runs on the
+    current torch stream, or on ``stream``."""
+    T = _Torch
+    if not T.ready:
+        T.bind()
+    if stream is not None and x.is_cuda and (q is None or scale is None or (residual is not None and h is None)):
+        with T.on(stream, x.device):   # outputs belong to the stream that writes them
+            return rms_norm_quantize(x, weight, eps, residual, int8, q, scale, h)
+    rows, cols, ldx = _rows_2d(x, "x")
+    on = x.get_device()
+    if on != T.current_device():
+        raise ValueError(f"x is on device {on}, the current device is {T.current_device()}")
+    T.refuse_apart(on, weight=weight, residual=residual, q=q, scale=scale, h=h)
+    device = x.device
+    wp = wk = rp = rk = hp = ldr = ldh = 0
+    if weight is not None:
+        if not weight.is_cuda or weight.shape != (cols,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous CUDA vector of {cols}")
+        wp, wk = weight.data_ptr(), _kind(weight, "weight")
+    if residual is not None:
+        rr, rc, ldr = _rows_2d(residual, "residual")
+        if rr != rows or rc != cols:
+            raise ValueError(f"residual must be of shape ({rows}, {cols})")
+        rp, rk = residual.data_ptr(), _kind(residual, "residual")
+        if h is None:
+            h, ldh = T.empty((rows, cols), dtype=residual.dtype, device=device), cols
+        else:
+            hr, hc, ldh = _rows_2d(h, "h")
+            if h.dtype is not residual.dtype or hr != rows or hc != cols:
+                raise ValueError(f"h must be {residual.dtype} of shape ({rows}, {cols})")
+        hp = h.data_ptr()
+    elif h is not None:
+        raise ValueError("h goes with a residual (without one it is x)")
+    q, ldq = _bytes_like(q, rows, cols, T.i8 if int8 else T.e4m3, device)
+    if int8:
+        scale, lds = _row_scales(scale, rows, device), 1
+    else:
+        lds = nblk = (cols + 127) // 128
+        if scale is None:
+            scale = T.empty((rows, nblk), dtype=T.f32, device=device)
+        else:
+            sr, sc, lds = _rows_2d(scale, "scale")
+            if scale.dtype is not T.f32 or sr != rows or sc != nblk:
+                raise ValueError(f"scale must be float32 of shape ({rows}, {nblk})")
+    if stream is None:
+        stream = T.stream(on)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = T.norm(ctypes.byref(NormArgs(rows, cols, x.data_ptr(), _kind(x, "x"), ldx, rp, rk, ldr, hp, ldh, wp, wk, eps,
+                                      CONVF_LINEAR_INT8 if int8 else CONVF_LINEAR_E4M3, q.data_ptr(), ldq,
+                                      scale.data_ptr(), lds)), stream)
+    if st != CONVF_OK:
+        _check(st)
+    return (q, scale) if residual is None else (q, scale, h)
 
 
 class ExpertLinear:

@@ -11,6 +11,7 @@
 #include "../../include/conv_fused.h"
 #include "api_internal.h"
 #include "convf_internal.h"
+#include "linear_host.h"
 #include "linear_internal.h"
 #include "live_handles.h"
 
@@ -20,25 +21,6 @@ namespace {
 
 constexpr uint32_t kLinearMagic = 0x11EA4001u;
 constexpr uint32_t kLinearDead = 0xDEAD11EAu;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// whether `rows` rows `ld` elements apart pass the address space (their products then pass 64 bits)
-bool too_far(long long rows, long long ld, int esz) { return ld > ((1LL << 48) / esz) / (rows > 1 ? rows : 1); }
-
-// SMs of the current device (looked up once per device), or an error
-convf_status current_device(int* dev, int* num_sms) {
-  static int sms[kMaxDevices];   // 0 = not looked up; every writer stores the same value
-  if (cudaGetDevice(dev) != cudaSuccess) return record_error(CONVF_ERR_CUDA, "no current CUDA device");
-  const bool known = *dev >= 0 && *dev < kMaxDevices;
-  *num_sms = known ? sms[*dev] : 0;
-  if (*num_sms == 0) {
-    if (cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess || *num_sms < 1)
-      return record_error(CONVF_ERR_CUDA, "the SM count of device %d could not be read", *dev);
-    if (known) sms[*dev] = *num_sms;
-  }
-  return CONVF_OK;
-}
 
 }  // namespace
 
@@ -229,9 +211,8 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
   p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
   const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a->x) | a->ldx * esz | (a->gated ? static_cast<long long>(a->cols) * esz : 0);
   const uintptr_t q_bits = reinterpret_cast<uintptr_t>(a->q) | a->ldq;
-  auto common = [](uintptr_t v) { return static_cast<int>((v | 32) & (~(v | 32) + 1)); };   // largest power of two of v, up to 32
-  p.x_align = common(x_bits);
-  p.q_align = common(q_bits);
+  p.x_align = common_alignment(x_bits);
+  p.q_align = common_alignment(q_bits);
   const cudaError_t e = launch_quantize_blocks(p, esz == 2, a->gated != 0, a->block_rows, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_error(CONVF_ERR_CUDA, "quantising launch failed: %s", cudaGetErrorString(e));
   return record_ok();

@@ -70,6 +70,35 @@ struct QuantParams {
 cudaError_t launch_quantize_blocks(const QuantParams& p, bool bf16, bool gated, int block_rows, int num_sms,
                                    cudaStream_t stream);
 
+// Rows to 8 bits with a scale, or a norm's factor, of the whole row (k_rows.cu).
+enum RowsKind : int { kRowsPlain = 0, kRowsGated = 1, kRowsNormInt8 = 2, kRowsNormE4m3 = 3 };
+struct RowsParams {
+  const void* x;
+  long long ldx;
+  int x_rows;
+  const int32_t* index;
+  int rows, cols, nblk;      // nblk = ceil(cols / 128)
+  const void* residual;      // added to x, or null; residual_bf16: its type and h's
+  long long ldr;
+  int residual_bf16;
+  void* h;                   // where x + residual goes, or null; may be the residual or x themselves
+  long long ldh;
+  const void* weight;        // [cols] or null
+  int weight_bf16;
+  float eps;
+  uint8_t* q;
+  long long ldq;
+  float* scale;              // [rows]; e4m3: [rows][lds]
+  long long lds;
+  int x_align, r_align, w_align, q_align;   // as QuantParams' (r_align: the residual's and h's, 32 without them)
+};
+template <int KIND>
+cudaError_t launch_rows(const RowsParams& p, bool bf16, int num_sms, cudaStream_t stream);
+template <> cudaError_t launch_rows<kRowsPlain>(const RowsParams&, bool, int, cudaStream_t);
+template <> cudaError_t launch_rows<kRowsGated>(const RowsParams&, bool, int, cudaStream_t);
+template <> cudaError_t launch_rows<kRowsNormInt8>(const RowsParams&, bool, int, cudaStream_t);
+template <> cudaError_t launch_rows<kRowsNormE4m3>(const RowsParams&, bool, int, cudaStream_t);
+
 struct LinearParams {
   int rows, N, experts;
   int num_kb;                // k-blocks of 128 bytes

@@ -453,7 +453,7 @@ void conv_fused_chain_destroy(convf_chain* c);
  * read in place (no prepack), and the row count is an argument of the run. */
 
 /* Operand type of a linear layer. */
-typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1 } convf_linear_dtype;
+typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1, CONVF_LINEAR_INT8 = 2 } convf_linear_dtype;
 
 /* What conv_fused_quantize_blocks reads and writes.  With v the values to quantise, [rows][cols]
  * in float32:
@@ -491,6 +491,71 @@ typedef struct {
  * q and scale must not overlap x, index or each other; rows of two of them that are the same
  * distance apart may lie between each other's (columns of one buffer). */
 convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * 8-bit integers with a scale per row (a token, or a weight matrix's output channel), and the
+ * root-mean-square norm in front of 8-bit layers. */
+
+/* What conv_fused_quantize_rows reads and writes.  With v the values to quantise, [rows][cols] in
+ * float32: x, rows of x by an index, or gated rows, as convf_quant_args has them (gated values here
+ * with every operation rounded to nearest: g / (1 + exp(-g)) * u);
+ *   scale[r] = max |v[r]| / 127                        (float32, round to nearest)
+ *   q[r][c] = rint(v[r][c] / scale[r])                 (float32 quotient, then nearest, ties to even)
+ * and q = 0 where the scale is 0 (a row of zeros, or of values so small that it underflows).  q is in
+ * -127 .. 127.  A row that holds a NaN has a NaN scale, one that holds an infinity an infinite one; its q
+ * are zeros then, so that every value of the row reads back as NaN. */
+typedef struct {
+  int rows, cols;          /* of q; rows may be 0; at most 2^30 columns                        */
+  const void* x;           /* device [x_rows][cols], or [x_rows][2*cols] when gated            */
+  int x_dtype;             /* convf_out_dtype of x: CONVF_OUT_F32 or CONVF_OUT_BF16            */
+  int x_rows;              /* rows of x (== rows without an index)                             */
+  long long ldx;           /* elements between rows of x                                       */
+  const int32_t* index;    /* device [rows] or NULL; an entry outside [0, x_rows) makes its row
+                              zeros with scale 0 (a padding row)                               */
+  int gated;               /* 1: the gated form                                                */
+  void* q;                 /* device int8 [rows][cols]; columns past cols are not written      */
+  long long ldq;           /* bytes between rows of q                                          */
+  float* scale;            /* device [rows]                                                    */
+} convf_quant_rows_args;
+
+/* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row stride of
+ * at least a row is served; rows that begin on 8 bytes are read and written as vectors.  q and scale
+ * must not overlap x, index or each other (rows at the same distance may lie between each other's). */
+convf_status conv_fused_quantize_rows(const convf_quant_rows_args* a, void* stream);
+
+/* What conv_fused_rms_norm_quantize reads and writes, in float32:
+ *   h[r][c] = x[r][c] + residual[r][c]                 (x without a residual)
+ *   t[r][c] = h[r][c] * weight[c]                      (h without a weight)
+ *   f[r]    = 1 / sqrt(mean over c of h[r][c]^2 + eps)
+ * and q, scale stand for t * f: CONVF_LINEAR_INT8 quantises rows t as conv_fused_quantize_rows does,
+ * CONVF_LINEAR_E4M3 blocks of 128 columns of t as conv_fused_quantize_blocks does (block_rows = 1),
+ * and each scale is multiplied by f[r], once.  (f is positive: the 8-bit values of t and of t * f are the
+ * same.)  h, rounded to the residual's type, is written where h is given; the norm goes by h before that
+ * rounding.  t has to stay within float32's range; a row whose squares' sum leaves it has f = 0. */
+typedef struct {
+  int rows, cols;          /* rows may be 0; at most 2^30 columns                              */
+  const void* x;           /* device [rows][cols]                                              */
+  int x_dtype;             /* convf_out_dtype of x: CONVF_OUT_F32 or CONVF_OUT_BF16            */
+  long long ldx;           /* elements between rows                                            */
+  const void* residual;    /* device [rows][cols], or NULL                                     */
+  int residual_dtype;      /* convf_out_dtype of residual and h                                */
+  long long ldr;
+  void* h;                 /* device [rows][cols], or NULL (always without a residual).  May be the
+                              residual itself (same address, ldh == ldr), or x itself if of its type */
+  long long ldh;
+  const void* weight;      /* device [cols], or NULL                                           */
+  int weight_dtype;        /* convf_out_dtype of weight                                        */
+  float eps;               /* positive and finite                                              */
+  int out;                 /* CONVF_LINEAR_E4M3 or CONVF_LINEAR_INT8                           */
+  void* q;                 /* device [rows][cols] bytes; columns past cols are not written     */
+  long long ldq;           /* bytes between rows of q                                          */
+  float* scale;            /* device [rows] (int8), or [rows][ceil(cols/128)] (e4m3)           */
+  long long lds;           /* e4m3: elements between rows of scale (ignored for int8)          */
+} convf_norm_args;
+
+/* On `stream`, asynchronous, no allocation, one launch; alignment, strides and overlaps as
+ * conv_fused_quantize_rows (the outputs are q, scale and h). */
+convf_status conv_fused_rms_norm_quantize(const convf_norm_args* a, void* stream);
 
 /* A linear layer, or one per expert: y[m][n] = act(sum_k x[m][k] W[e(m)][n][k] + bias[e(m)][n]),
  * with the act of a conv.  Sums are held in float32.  e4m3: each block's sum of products, times the

@@ -27,7 +27,7 @@ CONVF_VARIANT_AUTO, CONVF_VARIANT_IMPLICIT_GEMM, CONVF_VARIANT_GEMM_1X1, CONVF_V
 VARIANT_NAMES = {0: "auto", 1: "implicit_gemm_im2col", 2: "gemm_1x1", 3: "depthwise",
                  4: "int8_mma", 5: "implicit_gemm_gather", 6: "implicit_gemm_window", 7: "implicit_gemm_halo",
                  8: "int8_tcgen05_exact", 9: "grouped_direct", 10: "mbv2_block"}
-CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3, CONVF_LINEAR_INT8 = 0, 1, 2
+CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3, CONVF_LINEAR_INT8 = 0, 1, 3
 AUTO_PAD = {"NOTSET": 0, "SAME_UPPER": 1, "SAME_LOWER": 2, "VALID": 3}
 
 EXPORTED = ["conv_fused_output_shape", "conv_fused_resolve_pads", "conv_bn_scale_shift",
@@ -952,9 +952,9 @@ class ExpertLinear:
     """Linear layers, one per expert, over rows sorted by expert: rows offsets[e] up to offsets[e+1]
     of x times ``w[e]``.
 
-    ``w``: CUDA [experts][N][K], bf16 or float8_e4m3fn, read in place (rows and experts a multiple
-    of 16 bytes apart); ``w_scale`` (e4m3) fp32 [experts][ceil(N/128)][ceil(K/128)]; ``bias`` fp32
-    [experts][N] or None (both in place too where they are contiguous); all on the current device; ``act`` and ``clip`` as for a conv; y is fp32, or bf16 with ``out_bf16``.
+    ``w``: CUDA [experts][N][K], bf16, float8_e4m3fn or int8, read in place (rows and experts a multiple
+    of 16 bytes apart); ``w_scale`` fp32 [experts][ceil(N/128)][ceil(K/128)] (e4m3) or [experts][N]
+    (int8: K at most 131071); ``bias`` fp32 [experts][N] or None (both in place too where they are contiguous); all on the current device; ``act`` and ``clip`` as for a conv; y is fp32, or bf16 with ``out_bf16``.
     Calling it runs on the current torch stream."""
 
     def __init__(self, w, w_scale=None, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
@@ -963,16 +963,16 @@ class ExpertLinear:
             _Torch.bind()
         if not w.is_cuda or w.dim() != 3:
             raise ValueError("w must be a CUDA tensor [experts][N][K]")
-        if w.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-            raise ValueError("w must be bf16 or float8_e4m3fn")
+        if w.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.int8):
+            raise ValueError("w must be bf16, float8_e4m3fn or int8")
         E, N, K = w.shape
         if K > 1 and w.stride(2) != 1:
             raise ValueError("w's columns must be adjacent (stride 1)")
-        self.e4m3 = w.dtype == torch.float8_e4m3fn
-        if self.e4m3 != (w_scale is not None):
-            raise ValueError("w_scale goes with float8_e4m3fn weights, and with those only")
+        self.e4m3, self.int8 = w.dtype == torch.float8_e4m3fn, w.dtype == torch.int8
+        if (self.e4m3 or self.int8) != (w_scale is not None):
+            raise ValueError("w_scale goes with float8_e4m3fn or int8 weights, and with those only")
         blocks = (E, -(-N // 128), -(-K // 128))
-        for name, t, shape in (("w_scale", w_scale, blocks), ("bias", bias, (E, N))):
+        for name, t, shape in (("w_scale", w_scale, (E, N) if self.int8 else blocks), ("bias", bias, (E, N))):
             if t is not None and (not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape):
                 raise ValueError(f"{name} must be a CUDA fp32 tensor of shape {shape}")
         self.device = w.get_device()
@@ -984,7 +984,7 @@ class ExpertLinear:
         self._keep = (w, w_scale, bias)   # the layer reads them in place
         self.experts, self.N, self.K, self.kblk, self.dtype = E, N, K, blocks[2], w.dtype
         self.out_dtype = torch.bfloat16 if out_bf16 else torch.float32
-        d = LinearDesc(N, K, E, CONVF_LINEAR_E4M3 if self.e4m3 else CONVF_LINEAR_BF16,
+        d = LinearDesc(N, K, E, CONVF_LINEAR_E4M3 if self.e4m3 else CONVF_LINEAR_INT8 if self.int8 else CONVF_LINEAR_BF16,
                        w.stride(1) if N > 1 else -(-K // 16) * 16, w.stride(0), act, float(clip[0]), float(clip[1]),
                        CONVF_OUT_BF16 if out_bf16 else CONVF_OUT_F32)
         self.handle = conv_fused_linear_create(d, w, w_scale, bias)
@@ -1010,8 +1010,13 @@ class ExpertLinear:
                 raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows, self.kblk)}")
             xs = x_scale.data_ptr()
             xs_row, xs_blk = x_scale.stride()
+        elif self.int8:
+            if x_scale is None or not x_scale.is_cuda or x_scale.dtype is not _Torch.f32 or x_scale.shape != (rows,):
+                raise ValueError(f"x_scale must be a CUDA fp32 tensor of shape {(rows,)}")
+            xs = x_scale.data_ptr()
+            xs_row = x_scale.stride(0)
         elif x_scale is not None:
-            raise ValueError("x_scale goes with float8_e4m3fn layers only")
+            raise ValueError("x_scale goes with float8_e4m3fn or int8 layers only")
         if y is None:
             y, ldy = _Torch.empty((rows, self.N), dtype=self.out_dtype, device=x.device), self.N
         else:
@@ -1030,7 +1035,8 @@ class ExpertLinear:
 
     def __call__(self, x, offsets, x_scale=None, y=None, stream=None):
         """y [rows][N] for ``x`` [rows][K] (w's type; rows a multiple of 16 bytes apart), ``offsets``
-        int32 CUDA [experts+1] and, for e4m3, ``x_scale`` fp32 [rows][ceil(K/128)] (any strides).
+        int32 CUDA [experts+1] and ``x_scale`` fp32, for e4m3 [rows][ceil(K/128)] and for int8 [rows] (any
+        strides).
         Rows that no expert takes are not written, and none at all with offsets that decrease or pass
         the rows (``status`` reports those)."""
         if not offsets.is_cuda or offsets.dtype is not _Torch.i32 or offsets.shape != (self.experts + 1,) \
@@ -1074,3 +1080,16 @@ class BlockLinear(ExpertLinear):
 
     def __call__(self, x, x_scale=None, y=None, stream=None):
         return self._run(x, None, x_scale, y, stream)
+
+
+class Int8Linear(BlockLinear):
+    """One linear layer on int8 operands: ``w`` int8 [N][K] with ``w_scale`` fp32 [N] (a scale per output
+    channel, as quantize_rows gives them), ``bias`` fp32 [N] or None; the rest as ExpertLinear.  Calling it
+    with x (int8 [rows][K]) and x_scale [rows], as quantize_rows or rms_norm_quantize give them, returns
+    y = act(sum * (x_scale * w_scale) + bias), the sums exact integers."""
+
+    def __init__(self, w, w_scale, bias=None, act=CONVF_ACT_NONE, clip=(0.0, 6.0), out_bf16=False):
+        import torch
+        if w.dtype != torch.int8:
+            raise ValueError("w must be int8")
+        super().__init__(w, w_scale, bias, act, clip, out_bf16)

@@ -54,9 +54,11 @@ convf_status check_linear_desc(const convf_linear_desc* d) {
   if (d->experts < 1) return record_error(CONVF_ERR_INVALID_ARG, "experts=%d must be >= 1", d->experts);
   if (d->experts > kMaxExperts)
     return record_error(CONVF_ERR_UNSUPPORTED, "experts=%d: at most %d are served", d->experts, kMaxExperts);
-  if (d->dtype != CONVF_LINEAR_BF16 && d->dtype != CONVF_LINEAR_E4M3)
-    return record_error(CONVF_ERR_INVALID_ARG, "dtype=%d is not CONVF_LINEAR_BF16 or CONVF_LINEAR_E4M3", d->dtype);
-  const long long esz = d->dtype == CONVF_LINEAR_E4M3 ? 1 : 2;
+  if (d->dtype != CONVF_LINEAR_BF16 && d->dtype != CONVF_LINEAR_E4M3 && d->dtype != CONVF_LINEAR_INT8)
+    return record_error(CONVF_ERR_INVALID_ARG, "dtype=%d is not CONVF_LINEAR_BF16, CONVF_LINEAR_E4M3 or CONVF_LINEAR_INT8", d->dtype);
+  if (d->dtype == CONVF_LINEAR_INT8 && d->K > kInt8MaxK)
+    return record_error(CONVF_ERR_UNSUPPORTED, "K=%d: int8 sums of more than %d products may pass 32 bits", d->K, kInt8MaxK);
+  const long long esz = d->dtype == CONVF_LINEAR_BF16 ? 2 : 1;
   if (d->ldw < d->K) return record_error(CONVF_ERR_INVALID_ARG, "ldw=%lld is less than K=%d", d->ldw, d->K);
   if (too_far(d->N, d->ldw, 2)) return record_error(CONVF_ERR_INVALID_ARG, "ldw=%lld: W passes the address space", d->ldw);
   if (d->ldw * esz % 16)
@@ -81,16 +83,17 @@ convf_status check_linear_desc(const convf_linear_desc* d) {
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// clusters of `split` CTAs of the few-rows kernel that run at once (looked up once per process and
-// device; every writer stores the same value)
-int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
-  static int known[kMaxDevices][2][3][4];
+// clusters of `split` CTAs of a few-rows kernel (of operands `dtype`) that run at once (looked up once per
+// process and device; every writer stores the same value)
+int few_clusters(int dev, int num_sms, int dtype, int tile, int split) {
+  static int known[kMaxDevices][4][3][4];
   int ti = 0, si = 0;
   while ((16 << ti) < tile) ++ti;
   while ((1 << si) < split) ++si;
-  int* at = dev >= 0 && dev < kMaxDevices ? &known[dev][e4m3][ti][si] : nullptr;
+  int* at = dev >= 0 && dev < kMaxDevices ? &known[dev][dtype][ti][si] : nullptr;
   if (at && *at) return *at;
-  const int n = linear_few_max_clusters(e4m3, tile, split, num_sms);
+  const int n = dtype == CONVF_LINEAR_INT8 ? linear_int8_max_clusters(tile, split, num_sms)
+                                           : linear_few_max_clusters(dtype == CONVF_LINEAR_E4M3, tile, split, num_sms);
   if (at) *at = n;
   return n;
 }
@@ -99,9 +102,10 @@ int few_clusters(int dev, int num_sms, bool e4m3, int tile, int split) {
 // the experts is known on the device only, so the estimate goes by their mean, with half a tile per
 // expert lost at the groups' ends (any offsets are right with any plan).
 LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows) {
-  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
+  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3, int8 = d.dtype == CONVF_LINEAR_INT8;
   const long long taken = rows < d.experts ? rows : d.experts;   // experts that can have rows
-  const int num_kb = static_cast<int>(ceil_div(static_cast<long long>(d.K) * (e4m3 ? 1 : 2), kKBlockBytes));
+  const long long esz = d.dtype == CONVF_LINEAR_BF16 ? 2 : 1;
+  const int num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
   auto row_tiles = [&](int tile) {
     if (d.experts == 1) return ceil_div(rows, tile);
     const long long n = (2LL * rows / tile + taken) / 2;
@@ -115,7 +119,6 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   // more than the best form.
   LinearPlan plan{};
   long long best = -1;
-  const long long esz = e4m3 ? 1 : 2;
   const long long bytes = taken * d.N * d.K * esz + static_cast<long long>(rows) * (d.K * esz + d.N * 2LL);
   auto offer = [&](int form, int tile, int split, long long units, long long n_tiles, long long per_kb, long long ends) {
     const long long waves = ceil_div(row_tiles(tile) * n_tiles, units);
@@ -124,17 +127,29 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
     if (best >= 0 && ns >= best) return;
     best = ns;
     const long long most = (d.experts > 1 ? rows / tile + taken : ceil_div(rows, tile)) * n_tiles;
-    const int ctas = form == kLinearMany && tile == 256 ? 2 : split;
+    const int ctas = (form == kLinearMany && tile == 256) || (form == kLinearInt8 && tile == kInt8PairRows) ? 2 : split;
     plan = LinearPlan{form, tile, split, ctas * static_cast<int>(most < units ? most : units)};
   };
   const long long nt = ceil_div(d.N, 128), nt_many = ceil_div(d.N, kManyCols);
+  if (int8) {
+    for (int tile = 16; tile <= 64; tile *= 2) {
+      for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
+        const int units = few_clusters(dev, num_sms, d.dtype, tile, split);
+        if (units < 1 || (split > 1 && row_tiles(tile) * nt > units)) continue;   // sharing a tile pays in a single wave
+        offer(kLinearInt8, tile, split, units, nt, tile == 16 ? 300 : tile == 32 ? 400 : 350,
+              split == 1 ? 700 : 1000 + 500 * split + 75 * tile);
+      }
+    }
+    if (num_sms >= 2) offer(kLinearInt8, kInt8PairRows, 1, num_sms / 2, nt_many, 500, 2500);
+    return plan;
+  }
   for (int tile = 16; tile <= 64; tile *= 2) {
     // with two CTAs on an SM (16 and 32 columns), and alone
     const long long shared = tile == 16 ? (e4m3 ? 330 : 240) : (e4m3 ? 480 : 280);
     const long long alone = tile == 16 ? (e4m3 ? 230 : 160) : tile == 32 ? (e4m3 ? 330 : 200) : (e4m3 ? 430 : 245);
     for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
       const long long tiles = row_tiles(tile) * nt;
-      const int units = few_clusters(dev, num_sms, e4m3, tile, split);
+      const int units = few_clusters(dev, num_sms, d.dtype, tile, split);
       if (units < 1 || (split > 1 && tiles > units)) continue;   // sharing a tile pays in a single wave
       const bool one_each = tiles * split <= num_sms;
       offer(kLinearFew, tile, split, units, nt, one_each || tile == 64 ? (tile == 64 && one_each && e4m3 ? 330 : alone) : shared,
@@ -226,8 +241,8 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
   if (st != CONVF_OK) return st;
   if (!W) return record_error(CONVF_ERR_INVALID_ARG, "W is NULL");
   if (!aligned(W, 16)) return record_error(CONVF_ERR_INVALID_ARG, "W must be 16-byte aligned");
-  if ((desc->dtype == CONVF_LINEAR_E4M3) != (w_scale != nullptr))
-    return record_error(CONVF_ERR_INVALID_ARG, "w_scale goes with e4m3 weights, and with those only");
+  if ((desc->dtype != CONVF_LINEAR_BF16) != (w_scale != nullptr))
+    return record_error(CONVF_ERR_INVALID_ARG, "w_scale goes with e4m3 weights or int8 ones, and with those only");
   if (!aligned(w_scale, 4) || !aligned(bias, 4))
     return record_error(CONVF_ERR_INVALID_ARG, "w_scale and bias must be aligned to their elements");
   const bool host_injected = take_injected_alloc_failure();
@@ -250,13 +265,13 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
     return st;
   }
   {
-    const bool e4m3 = desc->dtype == CONVF_LINEAR_E4M3;
-    const cuuint64_t esz = e4m3 ? 1 : 2;
+    const bool bytes = desc->dtype != CONVF_LINEAR_BF16;
+    const cuuint64_t esz = bytes ? 1 : 2;
     const cuuint64_t size[3] = {static_cast<cuuint64_t>(desc->K), static_cast<cuuint64_t>(desc->N),
                                 static_cast<cuuint64_t>(desc->experts)};
     const cuuint64_t strides[2] = {desc->ldw * esz,
                                    (desc->experts > 1 ? desc->expert_stride : desc->N * desc->ldw) * esz};
-    const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType type = bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     st = encode_map(&l->tmW64, type, esz, 3, W, size, strides, 64, "W");
     if (st == CONVF_OK) st = encode_map(&l->tmW128, type, esz, 3, W, size, strides, 128, "W");
     if (st == CONVF_OK) st = encode_map(&l->tmW256, type, esz, 3, W, size, strides, 256, "W");
@@ -287,24 +302,25 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   if (st != CONVF_OK) return st;
   if (!a) return record_error(CONVF_ERR_INVALID_ARG, "args is NULL");
   const convf_linear_desc& d = l->d;
-  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3;
-  const long long esz = e4m3 ? 1 : 2, osz = d.out_dtype == CONVF_OUT_BF16 ? 2 : 4;
+  const bool e4m3 = d.dtype == CONVF_LINEAR_E4M3, int8 = d.dtype == CONVF_LINEAR_INT8, scaled = e4m3 || int8;
+  const long long esz = scaled ? 1 : 2, osz = d.out_dtype == CONVF_OUT_BF16 ? 2 : 4;
   if (a->rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", a->rows);
   if (a->rows > kMaxExtent) return record_error(CONVF_ERR_UNSUPPORTED, "rows=%d: at most %d are served", a->rows, kMaxExtent);
-  if (too_far(a->rows, a->ldx, 2) || too_far(a->rows, a->ldy, 4) || too_far(a->rows, a->xs_row, 4) || too_far(d.K, a->xs_blk, 4))
+  if (too_far(a->rows, a->ldx, 2) || too_far(a->rows, a->ldy, 4) || too_far(a->rows, a->xs_row, 4) ||
+      (!int8 && too_far(d.K, a->xs_blk, 4)))
     return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld, ldy=%lld, x_scale strides (%lld, %lld): the rows pass the address space",
                         a->ldx, a->ldy, a->xs_row, a->xs_blk);
   if (a->ldx < d.K) return record_error(CONVF_ERR_INVALID_ARG, "ldx=%lld is less than K=%d", a->ldx, d.K);
   if (a->ldx * esz % 16)
     return record_error(CONVF_ERR_UNSUPPORTED, "ldx=%lld: rows of x must be a multiple of 16 bytes apart", a->ldx);
   if (a->ldy < d.N) return record_error(CONVF_ERR_INVALID_ARG, "ldy=%lld is less than N=%d", a->ldy, d.N);
-  if (e4m3 && (a->xs_row < 0 || a->xs_blk < 0))
+  if (scaled && (a->xs_row < 0 || (e4m3 && a->xs_blk < 0)))
     return record_error(CONVF_ERR_INVALID_ARG, "x_scale strides (%lld, %lld) must be >= 0", a->xs_row, a->xs_blk);
   if (!a->offsets && d.experts > 1) return record_error(CONVF_ERR_INVALID_ARG, "%d experts need row offsets", d.experts);
   if (a->rows == 0) return record_ok();
   if (!a->x || !a->y) return record_error(CONVF_ERR_INVALID_ARG, "x or y is NULL");
-  if (e4m3 != (a->x_scale != nullptr))
-    return record_error(CONVF_ERR_INVALID_ARG, "x_scale goes with e4m3 layers, and with those only");
+  if (scaled != (a->x_scale != nullptr))
+    return record_error(CONVF_ERR_INVALID_ARG, "x_scale goes with e4m3 layers or int8 ones, and with those only");
   if (!aligned(a->x, 16)) return record_error(CONVF_ERR_INVALID_ARG, "x must be 16-byte aligned");
   if (!aligned(a->y, osz) || !aligned(a->x_scale, 4) || !aligned(a->offsets, 4))
     return record_error(CONVF_ERR_INVALID_ARG, "y, x_scale and offsets must be aligned to their elements");
@@ -315,7 +331,8 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   const Region w_at = d.experts == 1 || apart == d.N * d.ldw * esz
                           ? Region{l->w, static_cast<long long>(d.experts) * d.N, d.K * esz, d.ldw * esz}
                           : Region{l->w, 1, (d.experts - 1) * apart + ((d.N - 1) * d.ldw + d.K) * esz, 0};
-  const Region xs_at = !e4m3 ? Region{}
+  const Region xs_at = !scaled ? Region{}
+                       : int8 ? (a->xs_row ? Region{a->x_scale, a->rows, 4, a->xs_row * 4} : Region{a->x_scale, 1, 4, 0})
                        : a->xs_blk == 1 ? Region{a->x_scale, a->rows, nblk * 4, a->xs_row * 4}
                        : a->xs_row == 1 ? Region{a->x_scale, nblk, a->rows * 4LL, a->xs_blk * 4}
                                         : Region{a->x_scale, 1, ((a->rows - 1) * a->xs_row + (nblk - 1) * a->xs_blk + 1) * 4, 0};
@@ -323,7 +340,7 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
     return record_error(CONVF_ERR_INVALID_ARG, "x and y overlap");
   if (overlap(w_at, y_at)) return record_error(CONVF_ERR_INVALID_ARG, "the weights and y overlap");
   if (overlap(xs_at, y_at)) return record_error(CONVF_ERR_INVALID_ARG, "x_scale and y overlap");
-  if (overlap(Region{l->w_scale, 1, d.experts * wblk * nblk * 4, 0}, y_at) ||
+  if (overlap(Region{l->w_scale, 1, (int8 ? static_cast<long long>(d.experts) * d.N : d.experts * wblk * nblk) * 4, 0}, y_at) ||
       overlap(Region{l->bias, 1, static_cast<long long>(d.experts) * d.N * 4, 0}, y_at) ||
       overlap(Region{a->offsets, 1, (d.experts + 1) * 4LL, 0}, y_at))
     return record_error(CONVF_ERR_INVALID_ARG, "w_scale, bias or offsets overlap y");
@@ -334,13 +351,14 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   CUtensorMap tmX;
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
   const cuuint64_t stride = a->ldx * esz;
-  st = encode_map(&tmX, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
-                  a->x, size, &stride, plan.tile < 128 ? plan.tile : 128, "x");
+  const int x_box = plan.tile < 128 ? plan.tile : plan.form == kLinearInt8 ? plan.tile / 2 : 128;
+  st = encode_map(&tmX, scaled ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
+                  a->x, size, &stride, x_box, "x");
   if (st != CONVF_OK) return st;
   LinearParams p{};
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
   p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
-  p.n_tiles = static_cast<int>(ceil_div(d.N, plan.form == kLinearMany ? kManyCols : 128));
+  p.n_tiles = static_cast<int>(ceil_div(d.N, plan.tile < 128 ? 128 : kManyCols));
   // bf16 operands: the MMA's own accumulator truncates, so its sums go to registers every 256 values where
   // the result is fp32 (1.2e-6 of the result at K = 1000 without it, 3e-7 with it), and every 4096 values
   // where it is bf16: terms of one sign then lose 1e-5 of their sum at most, whatever K is (without it 8e-4
@@ -361,7 +379,8 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
     if (st != CONVF_OK) return st;
   }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = plan.form == kLinearFew
+  const cudaError_t e = plan.form == kLinearInt8 ? launch_linear_int8(p, plan, l->tmW128, tmX, strm)
+                        : plan.form == kLinearFew
                             ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
                             : launch_linear_many(p, plan, e4m3, plan.tile != 256 ? l->tmW256 : e4m3 ? l->tmW64 : l->tmW128,
                                                  tmX, tmY, strm);
@@ -398,15 +417,15 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
   if (!buf || len == 0) return record_error(CONVF_ERR_INVALID_ARG, "buf is NULL or len is 0");
   if (rows < 0) return record_error(CONVF_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
   const int n = snprintf(buf, len, "N=%d K=%d experts=%d %s rows=%d out=%s", l->d.N, l->d.K, l->d.experts,
-                         l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : "bf16", rows,
+                         l->d.dtype == CONVF_LINEAR_E4M3 ? "e4m3" : l->d.dtype == CONVF_LINEAR_INT8 ? "int8" : "bf16", rows,
                          l->d.out_dtype == CONVF_OUT_BF16 ? "bf16" : "f32");
   if (rows > 0 && n > 0 && static_cast<size_t>(n) < len) {
     int dev = -1;   // the plan asks the current device how many clusters it runs at once
     if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
       return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
-    snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.form == kLinearFew ? "few_rows" : "many_rows",
-             plan.tile, plan.form == kLinearFew ? 128 : kManyCols, plan.split, plan.grid);
+    snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.tile < 128 ? "few_rows" : "many_rows",
+             plan.tile, plan.tile < 128 ? 128 : kManyCols, plan.split, plan.grid);
   }
   return record_ok();
 }

@@ -108,7 +108,7 @@ struct LinearParams {
   int n_tiles;               // weight-row tiles of the chosen form
   const float* x_scale;
   long long xs_row, xs_blk;
-  const float* w_scale;      // [experts][nblk][num_kb]
+  const float* w_scale;      // [experts][nblk][num_kb]; int8 [experts][N]
   const float* bias;         // [experts][N] or null
   const int32_t* offsets;    // [experts + 1] or null
   void* y;
@@ -120,11 +120,12 @@ struct LinearParams {
 };
 
 // What a run launches (linear_plan): the form, its row tile, and how many CTAs share a tile's k.
-enum LinearForm : int { kLinearFew = 0, kLinearMany = 1 };
+enum LinearForm : int { kLinearFew = 0, kLinearMany = 1, kLinearInt8 = 2 };
 struct LinearPlan {
   int form;
-  int tile;     // rows of x per tile: kLinearFew 16, 32 or 64; kLinearMany 128, or 256 on CTA pairs
-  int split;    // kLinearFew: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
+  int tile;     // rows of x per tile: kLinearFew 16, 32 or 64; kLinearMany 128, or 256 on CTA pairs;
+                // kLinearInt8 16, 32 or 64, or kInt8PairRows on CTA pairs
+  int split;    // kLinearFew, kLinearInt8: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
   int grid;     // CTAs
 };
 
@@ -140,6 +141,13 @@ int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
 // tmX: boxes of 128 bytes x 128 rows; tmY (used where vec_y): {N, rows} of y, boxes of 128 bytes x 32 rows.
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
                                const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream);
+// tmW: boxes of 128 bytes x 128 rows; tmX: boxes of 128 bytes x plan.tile rows, on CTA pairs half as many.
+constexpr int kInt8PairRows = 192;
+constexpr int kInt8MaxK = (1 << 17) - 1;   // products of 2^14 at most: sums stay within 32 bits
+cudaError_t launch_linear_int8(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                               cudaStream_t stream);
+int linear_int8_max_clusters(int tile, int split, int num_sms);
+
 constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile
 
 }  // namespace convf

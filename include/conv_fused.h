@@ -453,7 +453,7 @@ void conv_fused_chain_destroy(convf_chain* c);
  * read in place (no prepack), and the row count is an argument of the run. */
 
 /* Operand type of a linear layer. */
-typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1, CONVF_LINEAR_INT8 = 2 } convf_linear_dtype;
+typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1, CONVF_LINEAR_INT8 = 3 /* 2 is no type */ } convf_linear_dtype;
 
 /* What conv_fused_quantize_blocks reads and writes.  With v the values to quantise, [rows][cols]
  * in float32:
@@ -562,9 +562,10 @@ convf_status conv_fused_rms_norm_quantize(const convf_norm_args* a, void* stream
  * product of its two scales (a float32 number: scales whose product leaves float32's normal range lose
  * digits), is added to a float32 sum over the blocks.  bf16: the tensor core sums 256 products (float32
  * results) or 4096 (bf16 results), truncating where it adds, and those sums are added in float32 to
- * nearest.  y is rounded once. */
+ * nearest.  int8: the sum is the exact integer; y = act(float(sum) * (x_scale * w_scale) + bias), in float32,
+ * each operation rounded to nearest.  y is rounded once. */
 typedef struct {
-  int N, K;                /* W[e]: [N][K]                                                     */
+  int N, K;                /* W[e]: [N][K]; int8: K at most 131071 (sums stay within 32 bits)  */
   int experts;             /* >= 1, at most 1024                                               */
   int dtype;               /* convf_linear_dtype of x and W                                    */
   long long ldw;           /* elements between rows of W; ldw * element size % 16 == 0         */
@@ -575,8 +576,8 @@ typedef struct {
 } convf_linear_desc;
 typedef struct convf_linear convf_linear;
 
-/* Validates, and keeps the pointers: W (device, 16-byte aligned), w_scale (device
- * [experts][ceil(N/128)][ceil(K/128)], NULL for bf16) and bias (device float [experts][N] or NULL)
+/* Validates, and keeps the pointers: W (device, 16-byte aligned), w_scale (device; e4m3
+ * [experts][ceil(N/128)][ceil(K/128)], int8 [experts][N], NULL for bf16) and bias (device float [experts][N] or NULL)
  * are read by every run and must outlive the layer.  One small device allocation (status). */
 convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void* W, const float* w_scale,
                                       const float* bias, convf_linear** out);
@@ -586,7 +587,7 @@ typedef struct {
   const void* x;           /* device [rows][K], 16-byte aligned                                */
   long long ldx;           /* elements between rows; ldx * element size % 16 == 0              */
   const float* x_scale;    /* device, scale of row m and block b at x_scale[m*xs_row + b*xs_blk];
-                              NULL for bf16                                                    */
+                              int8: of row m at x_scale[m*xs_row]; NULL for bf16               */
   long long xs_row, xs_blk;
   const int32_t* offsets;  /* device [experts+1], nondecreasing: expert e takes rows offsets[e]
                               up to offsets[e+1] (possibly none).  NULL: one expert takes all

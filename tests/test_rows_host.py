@@ -71,7 +71,7 @@ def norm_args(**kw):
     (dict(residual_dtype=-1), BAD, "residual_dtype=-1"),
     (dict(weight_dtype=2), BAD, "weight_dtype=2"),
     (dict(out=0), BAD, "out=0"),
-    (dict(out=3), BAD, "out=3"),
+    (dict(out=2), BAD, "out=2"),
     (dict(eps=0.0), BAD, "eps=0"),
     (dict(eps=-1.0), BAD, "eps=-1"),
     (dict(eps=float("nan")), BAD, "eps=nan"),

@@ -379,7 +379,8 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
     if (st != CONVF_OK) return st;
   }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = plan.form == kLinearInt8 ? launch_linear_int8(p, plan, l->tmW128, tmX, strm)
+  const cudaError_t e = plan.form == kLinearInt8 ? (plan.tile == kInt8PairRows ? launch_linear_int8_many(p, plan, l->tmW128, tmX, strm)
+                                                                               : launch_linear_int8_few(p, plan, l->tmW128, tmX, strm))
                         : plan.form == kLinearFew
                             ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
                             : launch_linear_many(p, plan, e4m3, plan.tile != 256 ? l->tmW256 : e4m3 ? l->tmW64 : l->tmW128,

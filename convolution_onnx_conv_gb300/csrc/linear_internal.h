@@ -144,8 +144,10 @@ cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bo
 // tmW: boxes of 128 bytes x 128 rows; tmX: boxes of 128 bytes x plan.tile rows, on CTA pairs half as many.
 constexpr int kInt8PairRows = 192;
 constexpr int kInt8MaxK = (1 << 17) - 1;   // products of 2^14 at most: sums stay within 32 bits
-cudaError_t launch_linear_int8(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                               cudaStream_t stream);
+cudaError_t launch_linear_int8_few(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                                   cudaStream_t stream);
+cudaError_t launch_linear_int8_many(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                                    cudaStream_t stream);
 int linear_int8_max_clusters(int tile, int split, int num_sms);
 
 constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile

@@ -27,7 +27,7 @@ constexpr uint32_t kLinearDead = 0xDEAD11EAu;
 struct convf_linear {
   LiveHandleCount live;
   uint32_t magic;
-  CUtensorMap tmW64, tmW128, tmW256;   // boxes of 64, 128 and 256 weight rows
+  CUtensorMap tmW64, tmW128, tmW256;   // boxes of 64 (int8: 96), 128 and 256 weight rows
   int device, num_sms;
   convf_linear_desc d;
   const void* w;
@@ -98,6 +98,9 @@ int few_clusters(int dev, int num_sms, int dtype, int tile, int split) {
   return n;
 }
 
+// weight rows of a plan's tile
+int tile_columns(const LinearPlan& plan) { return plan.tile < 128 ? 128 : plan.form == kLinearInt8 ? kInt8PairCols : kManyCols; }
+
 // What a run of `rows` rows launches: the form with the least estimated time.  How the rows fall on
 // the experts is known on the device only, so the estimate goes by their mean, with half a tile per
 // expert lost at the groups' ends (any offsets are right with any plan).
@@ -140,7 +143,7 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
               split == 1 ? 700 : 1000 + 500 * split + 75 * tile);
       }
     }
-    if (num_sms >= 2) offer(kLinearInt8, kInt8PairRows, 1, num_sms / 2, nt_many, 500, 2500);
+    if (num_sms >= 2) offer(kLinearInt8, kInt8PairRows, 1, num_sms / 2, ceil_div(d.N, kInt8PairCols), 500, 2500);
     return plan;
   }
   for (int tile = 16; tile <= 64; tile *= 2) {
@@ -161,17 +164,17 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   return plan;
 }
 
-// boxes of 128 bytes x box_rows rows in the 128-byte swizzle
+// boxes of box_bytes (128 or 64) x box_rows rows, in the swizzle of as many bytes
 convf_status encode_map(CUtensorMap* m, CUtensorMapDataType type, int esz, int dims, const void* p, const cuuint64_t* size,
-                        const cuuint64_t* strides, int box_rows, const char* what) {
+                        const cuuint64_t* strides, int box_rows, const char* what, int box_bytes = kKBlockBytes) {
   EncodeTiledFn tiled;
   EncodeIm2colFn im2col;
   if (!tensor_map_encoders(&tiled, &im2col)) return record_error(CONVF_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kKBlockBytes / esz),
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / esz),
                              static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = tiled(m, type, dims, const_cast<void*>(p), size, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return record_error(CONVF_ERR_CUDA, "encoding the tensor map of %s failed (%d)", what, (int)r);
   return CONVF_OK;
@@ -272,7 +275,7 @@ convf_status conv_fused_linear_create(const convf_linear_desc* desc, const void*
     const cuuint64_t strides[2] = {desc->ldw * esz,
                                    (desc->experts > 1 ? desc->expert_stride : desc->N * desc->ldw) * esz};
     const CUtensorMapDataType type = bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    st = encode_map(&l->tmW64, type, esz, 3, W, size, strides, 64, "W");
+    st = encode_map(&l->tmW64, type, esz, 3, W, size, strides, desc->dtype == CONVF_LINEAR_INT8 ? 96 : 64, "W");
     if (st == CONVF_OK) st = encode_map(&l->tmW128, type, esz, 3, W, size, strides, 128, "W");
     if (st == CONVF_OK) st = encode_map(&l->tmW256, type, esz, 3, W, size, strides, 256, "W");
     if (st != CONVF_OK) {
@@ -351,14 +354,14 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   CUtensorMap tmX;
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
   const cuuint64_t stride = a->ldx * esz;
-  const int x_box = plan.tile < 128 ? plan.tile : plan.form == kLinearInt8 ? plan.tile / 2 : 128;
+  const int x_box = plan.tile < 128 ? plan.tile : 128;
   st = encode_map(&tmX, scaled ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
                   a->x, size, &stride, x_box, "x");
   if (st != CONVF_OK) return st;
   LinearParams p{};
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
   p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
-  p.n_tiles = static_cast<int>(ceil_div(d.N, plan.tile < 128 ? 128 : kManyCols));
+  p.n_tiles = static_cast<int>(ceil_div(d.N, tile_columns(plan)));
   // bf16 operands: the MMA's own accumulator truncates, so its sums go to registers every 256 values where
   // the result is fp32 (1.2e-6 of the result at K = 1000 without it, 3e-7 with it), and every 4096 values
   // where it is bf16: terms of one sign then lose 1e-5 of their sum at most, whatever K is (without it 8e-4
@@ -371,15 +374,15 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   p.lo = l->lo; p.hi = l->hi; p.status = l->status;
   p.clamp = l->lo != -INFINITY || l->hi != INFINITY;
   CUtensorMap tmY = tmX;   // (not used without vec_y)
-  if (plan.form == kLinearMany && p.vec_y) {
+  if (plan.tile >= 128 && p.vec_y) {
     const cuuint64_t ysize[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(a->rows)};
     const cuuint64_t ystride = a->ldy * osz;
     st = encode_map(&tmY, osz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                    static_cast<int>(osz), 2, a->y, ysize, &ystride, 32, "y");
+                    static_cast<int>(osz), 2, a->y, ysize, &ystride, 32, "y", int8 ? 64 : kKBlockBytes);
     if (st != CONVF_OK) return st;
   }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = plan.form == kLinearInt8 ? (plan.tile == kInt8PairRows ? launch_linear_int8_many(p, plan, l->tmW128, tmX, strm)
+  const cudaError_t e = plan.form == kLinearInt8 ? (plan.tile == kInt8PairRows ? launch_linear_int8_many(p, plan, l->tmW64, tmX, tmY, strm)
                                                                                : launch_linear_int8_few(p, plan, l->tmW128, tmX, strm))
                         : plan.form == kLinearFew
                             ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
@@ -426,7 +429,7 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
       return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
     snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.tile < 128 ? "few_rows" : "many_rows",
-             plan.tile, plan.tile < 128 ? 128 : kManyCols, plan.split, plan.grid);
+             plan.tile, tile_columns(plan), plan.split, plan.grid);
   }
   return record_ok();
 }

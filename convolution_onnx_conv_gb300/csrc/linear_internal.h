@@ -141,13 +141,15 @@ int linear_few_max_clusters(bool e4m3, int tile, int split, int num_sms);
 // tmX: boxes of 128 bytes x 128 rows; tmY (used where vec_y): {N, rows} of y, boxes of 128 bytes x 32 rows.
 cudaError_t launch_linear_many(const LinearParams& p, const LinearPlan& plan, bool e4m3, const CUtensorMap& tmW,
                                const CUtensorMap& tmX, const CUtensorMap& tmY, cudaStream_t stream);
-// tmW: boxes of 128 bytes x 128 rows; tmX: boxes of 128 bytes x plan.tile rows, on CTA pairs half as many.
-constexpr int kInt8PairRows = 192;
+// Few rows: tmW: boxes of 128 bytes x 128 rows; tmX: boxes of 128 bytes x plan.tile rows.  Many: tmW: boxes of 128
+// bytes x 96 rows; tmX: of 128 bytes x 128 rows; tmY (used where vec_y): {N, rows} of y, boxes of 64 bytes x 32 rows
+// in the 64-byte swizzle.
+constexpr int kInt8PairRows = 256, kInt8PairCols = 192;
 constexpr int kInt8MaxK = (1 << 17) - 1;   // products of 2^14 at most: sums stay within 32 bits
 cudaError_t launch_linear_int8_few(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
                                    cudaStream_t stream);
 cudaError_t launch_linear_int8_many(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                                    cudaStream_t stream);
+                                    const CUtensorMap& tmY, cudaStream_t stream);
 int linear_int8_max_clusters(int tile, int split, int num_sms);
 
 constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile

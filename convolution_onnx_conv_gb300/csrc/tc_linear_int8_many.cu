@@ -1,58 +1,75 @@
-// Linear layers on int8 operands for many rows per weight matrix: y^T = W x^T with integer sums, on tcgen05 (see
-// linear_int8_dev.cuh), in tiles of 256 weight rows x 192 rows of x on CTA pairs.
+// Linear layers on int8 operands for many rows per weight matrix: y = x W^T with integer sums, on tcgen05 (see
+// linear_int8_dev.cuh), in tiles of 256 rows of x x 192 weight rows on CTA pairs.
 //
-// A unit, 64 values, takes the tensor cores 384 cycles; meanwhile each CTA of a pair has to convert 128 weight rows
-// and 96 rows of x of it (a single CTA's 128 x 192 tile: 128 and 192), 84 integer instructions at half rate for each
-// of four warps.  What a unit goes through is long (its bytes' arrival, the conversion, the pair's barrier, the MMAs,
-// their end seen in both CTAs), and TMEM holds only four units of weights beside two accumulators of 192 columns:
-// so weights are converted ahead, in registers, and wait for a place for their stores only; rows of x, with places
-// for eight units in shared memory, have warps of their own.
+// Here the rows of x are the MMA's first operand, in TMEM, so that a thread of the epilogue holds one row of y and
+// writes 16 bytes at a time (with the weights there it held a column, and its 2-byte stores took the load/store
+// units, which the conversion needs, 4 us a tile).
+//
+// A unit, 64 values, takes the tensor cores 384 cycles; meanwhile each CTA of a pair has to convert 128 rows of x
+// and 96 weight rows of it (a single CTA's 128 x 192 tile: 128 and 192), 84 integer instructions at half rate for
+// each of four warps.  What a unit goes through is long (its bytes' arrival, the conversion, the pair's barrier, the
+// MMAs, their end seen in both CTAs), and TMEM holds only four units of x beside two accumulators of 192 columns: so
+// x is converted ahead, in registers, and waits for a place for its stores only; weights, with places for six units
+// in shared memory, have warps of their own.
 //
 //   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (of a pair: the leader's)
 //   warp 2        the tile schedule
-//   warps 4-11    int8 -> fp16 of the weights: two groups of four warps, each a unit of every stage
-//   warps 12-15   int8 -> fp16 of x
-//   warps 16-23   epilogue: warp w the weight rows 32 (w % 4) .. and half of the columns
+//   warps 4-11    int8 -> fp16 of x: two groups of four warps, each a unit of every stage
+//   warps 12-19   int8 -> fp16 of the weights, in two groups as well
+//   warps 20-27   epilogue: warp w the rows 32 (w % 4) .. and half of the columns
+#include <type_traits>
+
 #include "linear_int8_dev.cuh"
 
 namespace convf {
 
 namespace {
 
-constexpr int TN = kInt8PairRows;   // columns: rows of x
+constexpr int TN = kInt8PairCols;   // an MMA's columns: weight rows
 
 struct Int8ManyCfg {
-  static constexpr int kXRows = TN / 2;              // rows of x that a CTA loads and converts
+  static constexpr int kWRows = TN / 2;              // weight rows that a CTA loads and converts
   static constexpr int kCols = TN / 2;               // columns per epilogue thread
-  static constexpr int kThreads = 768;
-  static constexpr int kWBytes = 128 * kKBlockBytes, kXBytes = kXRows * kKBlockBytes;   // of a stage, int8
-  static constexpr int kBBytes = kXRows * 2 * kUnit; // of a unit of x, fp16
-  static constexpr int kStages = 4, kAUnits = 4, kBBlocks = 4;   // places: int8 stages, units of weights, pairs of units of x
+  static constexpr int kThreads = 896;
+  static constexpr int kXBytes = 128 * kKBlockBytes, kWBytes = kWRows * kKBlockBytes;   // of a stage, int8
+  static constexpr int kBBytes = kWRows * 2 * kUnit; // of a unit of weights, fp16
+  static constexpr int kStages = 4, kAUnits = 4, kBUnits = 6;   // places: int8 stages, units of x, units of weights
   static constexpr int kDCol = kAUnits * kUnitCols;  // the accumulators' first column
-  static constexpr int kBarBytes = 256;
-  static constexpr int kSmem = kStages * (kWBytes + kXBytes) + 2 * kBBlocks * kBBytes + kBarBytes + kScheduleBytes;
-  // registers: 80 per thread at launch; the epilogue's two warpgroups take what the others give up
-  static constexpr int kRegs = 80, kRegsEpi = 136, kRegsW = 64, kRegsX = 40, kRegsOther = 40;
-  static_assert(256 * kRegsEpi + 256 * kRegsW + 128 * (kRegsX + kRegsOther) <= kThreads * kRegs, "register split");
-  static_assert((2 * kStages + 2 * kAUnits + 2 * kBBlocks + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
+  // per epilogue warp: two chunks of 32 rows of 64 bytes on their way out, its columns' scales and biases
+  static constexpr int kOutBytes = 2 * 2048, kTableBytes = 2 * kCols * 4;
+  static constexpr int kBarBytes = 512;
+  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + kBUnits * kBBytes + 8 * (kOutBytes + kTableBytes) + kBarBytes + kScheduleBytes;
+  // registers: 72 per thread at launch; the epilogue's two warpgroups take what the others give up
+  static constexpr int kRegs = 72, kRegsEpi = 128, kRegsX = 56, kRegsW = 48, kRegsOther = 40;
+  static_assert(256 * (kRegsEpi + kRegsX + kRegsW) + 128 * kRegsOther <= kThreads * kRegs, "register split");
+  static_assert((2 * kStages + 2 * kAUnits + 2 * kBUnits + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
   static_assert(kDCol + 2 * TN <= 512, "TMEM columns");
+  static_assert(2 * kStages % kAUnits == 0, "places of x go with the stages");
 };
 
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
-    linear_int8_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX) {
+    linear_int8_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                            const __grid_constant__ CUtensorMap tmY) {
   using Cfg = Int8ManyCfg;
-  constexpr int kStages = Cfg::kStages, kAUnits = Cfg::kAUnits, kBBlocks = Cfg::kBBlocks, kCols = Cfg::kCols;
+  constexpr int kStages = Cfg::kStages, kAUnits = Cfg::kAUnits, kBUnits = Cfg::kBUnits, kCols = Cfg::kCols;
   constexpr int kChunkBlocks = kInt8Chunk / kKBlockBytes;
-  extern __shared__ __align__(1024) uint8_t sW[];   // (the swizzle goes by address bits 7 to 9)
-  uint8_t* sX = sW + kStages * Cfg::kWBytes;
-  uint8_t* sB = sX + kStages * Cfg::kXBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + 2 * kBBlocks * Cfg::kBBytes);   // int8 tiles are here
+  extern __shared__ __align__(1024) uint8_t sX[];   // (the swizzle goes by address bits 7 to 9)
+  uint8_t* sW = sX + kStages * Cfg::kXBytes;
+  uint8_t* sB = sW + kStages * Cfg::kWBytes;
+  uint8_t* sOut = sB + kBUnits * Cfg::kBBytes;
+  float* sTable = reinterpret_cast<float*>(sOut + 8 * Cfg::kOutBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * (Cfg::kOutBytes + Cfg::kTableBytes));   // int8 tiles are here
   uint64_t* empty = full + kStages;     // and have been read
-  uint64_t* afull = empty + kStages;    // a unit of weights is in TMEM, of both CTAs (the leader's)
+  uint64_t* afull = empty + kStages;    // a unit of x is in TMEM, of both CTAs (the leader's)
   uint64_t* aempty = afull + kAUnits;   // and its MMAs have read it
-  uint64_t* bfull = aempty + kAUnits;   // two units of x are converted, of both CTAs (the leader's)
-  uint64_t* bempty = bfull + kBBlocks;  // and their MMAs have read them
-  uint64_t* tfull = bempty + kBBlocks;  // an accumulator holds a chunk's sums
+  uint64_t* bfull = aempty + kAUnits;   // a unit of weights is converted, of both CTAs (the leader's)
+  uint64_t* bempty = bfull + kBUnits;   // and its MMAs have read it
+  uint64_t* tfull = bempty + kBUnits;  // an accumulator holds a chunk's sums
   uint64_t* tempty = tfull + 2;         // and has been read, in both CTAs (the leader's)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -64,13 +81,13 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 12);
+      mbar_init(&empty[s], 16);
     }
     for (int u = 0; u < kAUnits; ++u) {
       mbar_init(&afull[u], 8);
       mbar_init(&aempty[u], 1);
     }
-    for (int b = 0; b < kBBlocks; ++b) {
+    for (int b = 0; b < kBUnits; ++b) {
       mbar_init(&bfull[b], 8);
       mbar_init(&bempty[b], 1);
     }
@@ -94,7 +111,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();   // after the TMEM allocation, which a dependent's CTA would otherwise take
   pdl_wait_prior();
-  if (warp == 2) build_schedule(p, TN, prefix, blockIdx.x == 0);
+  if (warp == 2) build_schedule(p, kInt8PairRows, prefix, blockIdx.x == 0);
   __syncthreads();
 
   const long long tiles = tile_count(p, prefix);
@@ -109,12 +126,12 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         for (long long t = t0; t < tiles; t += tstep) {
-          const LinearTile q = tile_at<TN, kManyCols>(p, prefix, t);
+          const LinearTile q = tile_at<kInt8PairRows, TN>(p, prefix, t);
           for (int kb = 0; kb < p.num_kb; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) goto teardown;
             mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes);
-            tma_load_3d(sW + stage * Cfg::kWBytes, &tmW, &full[stage], kb * kKBlockBytes, q.n0 + rank * 128, q.e);
-            tma_load_2d(sX + stage * Cfg::kXBytes, &tmX, &full[stage], kb * kKBlockBytes, q.row0 + rank * Cfg::kXRows);
+            tma_load_3d(sW + stage * Cfg::kWBytes, &tmW, &full[stage], kb * kKBlockBytes, q.n0 + rank * Cfg::kWRows, q.e);
+            tma_load_2d(sX + stage * Cfg::kXBytes, &tmX, &full[stage], kb * kKBlockBytes, q.row0 + rank * 128);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1;
@@ -126,9 +143,9 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
       // registers, which is where the MMA takes its descriptors from
       const bool issue = elect_one();
-      constexpr uint32_t idesc = idesc_f16_f32(256, TN);
+      constexpr uint32_t idesc = idesc_f16_f32(kInt8PairRows, TN);
       const uint64_t b0 = sdesc_kmajor_sw128(smem_u32(sB));
-      int unit = 0, block = 0, buf = 0;
+      int unit = 0, bunit = 0, buf = 0;
       uint32_t aphase = 0, bphase = 0, tphase = 0;
       for (long long j = 0; j < mine; ++j) {
         for (int kb = 0, in_chunk = 0; kb < p.num_kb; ++kb) {
@@ -138,24 +155,22 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             // the barriers are asked at once, before any is waited for
             bool ready = mbar_test_wait_cluster(&afull[unit], aphase);
-            if (h == 0) {
-              ready = mbar_test_wait_cluster(&bfull[block], bphase) & ready;
-              if (first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
-            }
+            ready = mbar_test_wait_cluster(&bfull[bunit], bphase) & ready;
+            if (h == 0 && first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
             if (!ready) {
               if (!mbar_wait_cluster(&afull[unit], aphase, abort_flag, p.status)) goto teardown;
-              if (h == 0 && !mbar_wait_cluster(&bfull[block], bphase, abort_flag, p.status)) goto teardown;
+              if (!mbar_wait_cluster(&bfull[bunit], bphase, abort_flag, p.status)) goto teardown;
               if (h == 0 && first && !mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status)) goto teardown;
             }
             tc_fence_after();
             const uint32_t a = tmem_base + unit * kUnitCols;
-            const uint64_t b = b0 + (2 * block + h) * (Cfg::kBBytes >> 4);
+            const uint64_t b = b0 + bunit * (Cfg::kBBytes >> 4);
             if (issue) {
 #pragma unroll
               for (int s = 0; s < kUnit / 16; ++s)   // 16 values: 8 columns of A, 32 bytes of B
                 tc_mma_f16_ts_pair(d, a + 8 * s, b + 2 * s, idesc, !first || h > 0 || s > 0);
               tc_commit_pair(&aempty[unit], 3);
-              if (h == 1) tc_commit_pair(&bempty[block], 3);
+              tc_commit_pair(&bempty[bunit], 3);
               if (h == 1 && last) tc_commit_pair(&tfull[buf], 3);
             }
             __syncwarp();
@@ -163,10 +178,10 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
               unit = 0;
               aphase ^= 1;
             }
-          }
-          if (++block == kBBlocks) {
-            block = 0;
-            bphase ^= 1;
+            if (++bunit == kBUnits) {
+              bunit = 0;
+              bphase ^= 1;
+            }
           }
           if (last) {
             in_chunk = 0;
@@ -177,96 +192,108 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       }
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsW));
-    const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - 4) >> 2;   // this thread's weight row; its unit of a stage
-    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    int stage = 0, unit = h;
-    uint32_t phase = 0, uphase = 0;
-    for (long long k = 0; k < blocks; ++k) {
-      if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-      const uint8_t* w = sW + stage * Cfg::kWBytes + id * kKBlockBytes;
-      uint4 v[4];
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsX));
+    const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - 4) >> 2;   // this thread's row; its unit of a stage
+    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * kUnitCols;
+    const uint8_t* from[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(w + (((id & 7) ^ j ^ (4 * h)) << 4));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      const bool room = mbar_test_wait(&aempty[unit], uphase ^ 1);   // (asked before the arithmetic)
-      uint32_t f[2][16];
+    for (int j = 0; j < 4; ++j) from[j] = sX + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
+    // (a turn of all stages, so that every address is one of these and a constant)
+    uint32_t phase = 0;
+    for (long long k = 0; k < blocks; k += kStages, phase ^= 1) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
-      if (!room && !mbar_wait(&aempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
-      tc_fence_after();
-      tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
-      tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(map_to_rank(smem_u32(&afull[unit]), 0));
-      if ((unit += 2) >= kAUnits) {
-        unit = h;
-        uphase ^= 1;
-      }
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
+      for (int s = 0; s < kStages; ++s) {
+        if (k + s >= blocks) break;
+        constexpr int kTurn = kAUnits / 2;   // stages that the places of x last
+        const uint32_t uphase = kTurn == kStages ? phase : s / kTurn & 1;
+        uint64_t* const place = &aempty[2 * (s % kTurn)] + h;
+        if (!mbar_wait(&full[s], phase, abort_flag, p.status)) goto teardown;
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + s * Cfg::kXBytes);
+        const bool room = mbar_test_wait(place, uphase ^ 1);   // (asked before the arithmetic)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        uint32_t f[2][16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
+        if (!room && !mbar_wait(place, uphase ^ 1, abort_flag, p.status)) goto teardown;
+        tc_fence_after();
+        tmem_st_32x32b_x16(to0 + 2 * (s % kTurn) * kUnitCols, f[0]);
+        tmem_st_32x32b_x16(to0 + 2 * (s % kTurn) * kUnitCols + 16, f[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(smem_u32(&afull[2 * (s % kTurn)] + h), 0));
       }
     }
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsX));
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsW));
     // 16 bytes at a time: thread id's are those of row (id + 128 i) % 96, and j = (id + 128 i) / 96 of a unit's four
-    constexpr int kPer = Cfg::kXRows * 4 / 128;
-    const int id = threadIdx.x & 127;
-    int stage = 0, block = 0;
-    uint32_t phase = 0, bphase = 0;
-    for (long long k = 0; k < blocks; ++k) {
-      if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-      const bool room = mbar_test_wait(&bempty[block], bphase ^ 1);
-      const uint8_t* x = sX + stage * Cfg::kXBytes;
-      uint8_t* b = sB + 2 * block * Cfg::kBBytes;
+    constexpr int kPer = Cfg::kWRows * 4 / 128;
+    const int id = threadIdx.x & 127, h = (warp - 12) >> 2;   // its unit of a stage
+    const uint8_t* from[kPer];
+    uint8_t* to[kPer][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < kPer; ++i) {
+      const int row = (id + 128 * i) % Cfg::kWRows, j = (id + 128 * i) / Cfg::kWRows;
+      from[i] = sW + row * kKBlockBytes + (((row & 7) ^ j ^ (4 * h)) << 4);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) to[i][e] = sB + row * 128 + (((row & 7) ^ (2 * j + e)) << 4);   // half e of the 16
+    }
+    uint32_t phase = 0, bphase = 0;
+    int place = h;
+    for (long long k = 0; k < blocks; k += kStages, phase ^= 1) {
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) {
+        if (k + s >= blocks) break;
+        if (!mbar_wait(&full[s], phase, abort_flag, p.status)) goto teardown;
         uint4 v[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int row = (id + 128 * i) % Cfg::kXRows, j = (id + 128 * i) / Cfg::kXRows;
-          v[i] = *reinterpret_cast<const uint4*>(x + row * kKBlockBytes + (((row & 7) ^ j ^ (4 * h)) << 4));
-        }
-        if (h == 0 && !room && !mbar_wait(&bempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
+        for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + s * Cfg::kWBytes);
+        const bool room = mbar_test_wait(&bempty[place], bphase ^ 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (!room && !mbar_wait(&bempty[place], bphase ^ 1, abort_flag, p.status)) goto teardown;
+        const int at = place * Cfg::kBBytes;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int row = (id + 128 * i) % Cfg::kXRows, j = (id + 128 * i) / Cfg::kXRows;
           uint32_t o[8];
           f16_of_int8_16(v[i], o);
-          uint8_t* to = b + h * Cfg::kBBytes + row * 128;
-          *reinterpret_cast<uint4*>(to + (((2 * j) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(to + (((2 * j + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(to[i][0] + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to[i][1] + at) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-      }
-      fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_remote_cta(map_to_rank(smem_u32(&bfull[block]), 0));
-        mbar_arrive(&empty[stage]);
-      }
-      if (++block == kBBlocks) {
-        block = 0;
-        bphase ^= 1;
-      }
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
+        fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(smem_u32(&bfull[place]), 0));
+        if ((place += 2) >= kBUnits) {
+          place = h;
+          bphase ^= 1;
+        }
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
-    const int quad = warp & 3;
-    const int c0 = (warp - 16) / 4 * kCols;   // this thread's columns
-    const uint32_t from0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::kDCol + c0;
+    const int quad = warp & 3, half = (warp - 20) >> 2;
+    const int mrow = rank * 128 + quad * 32;   // this warp's first row of the tile
+    const uint32_t from0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::kDCol + half * kCols;
+    uint8_t* out = sOut + (warp - 20) * Cfg::kOutBytes;
+    float* table = sTable + (warp - 20) * (Cfg::kTableBytes / 4);   // scales, then biases
     int buf = 0;
-    uint32_t tphase = 0;
+    uint32_t tphase = 0, turn = 0;
     for (long long t = t0; t < tiles; t += tstep) {
-      const LinearTile q = tile_at<TN, kManyCols>(p, prefix, t);
-      const int n = q.n0 + rank * 128 + quad * 32 + lane;   // this thread's weight row
+      const LinearTile q = tile_at<kInt8PairRows, TN>(p, prefix, t);
+      const int n0 = q.n0 + half * kCols;   // this warp's first column
+      const long long row0 = q.row0 + mrow;
+      const float xs = p.x_scale[(q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row];
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int n = n0 + 32 * i + lane;
+        const long long en = static_cast<long long>(q.e) * p.N + n;
+        table[32 * i + lane] = n < p.N ? p.w_scale[en] : 0.f;
+        table[kCols + 32 * i + lane] = p.bias && n < p.N ? p.bias[en] : 0.f;
+      }
+      __syncwarp();
       int acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0;
@@ -281,16 +308,74 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         buf ^= 1;
         if (buf == 0) tphase ^= 1;
       }
-      const long long en = static_cast<long long>(q.e) * p.N + n;
-      const Int8Finish finish{n < p.N ? p.w_scale[en] : 0.f, p.bias && n < p.N ? p.bias[en] : 0.f, p.lo, p.hi};
-      float held[kCols / 32];   // scales of the columns' rows, a lane's for its warp
+      if (mrow < q.rows && n0 < p.N) {
+        // 64 bytes of each row at a time through shared memory (16-byte units swizzled by row): whole warps' rows leave
+        // by TMA, others by the elements, lanes side by side.  (A TMA store clips the columns past N by units of 16
+        // bytes and would write over what follows rows that end inside one.)
+        auto send = [&](auto bf16) {
+          constexpr bool BF16 = decltype(bf16)::value;
+          constexpr int kEach = BF16 ? 32 : 16;   // columns
 #pragma unroll
-      for (int i = 0; i < kCols / 32; ++i) {
-        const int c = c0 + 32 * i + lane;
-        held[i] = c < q.rows ? p.x_scale[(q.row0 + c) * p.xs_row] : 0.f;
+          for (int c = 0; c < kCols; c += kEach) {
+            uint8_t* chunk = out + (turn & 1) * 2048;
+            ++turn;
+            const int n = n0 + c;
+            if (lane == 0) bulk_wait_read<1>();   // the store from this place
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              constexpr int kOf = BF16 ? 8 : 4;
+              float v[kOf];
+#pragma unroll
+              for (int i = 0; i < kOf; i += 4) {
+                const int at = c + u * kOf + i;
+                const float4 s = *reinterpret_cast<const float4*>(table + at), b = *reinterpret_cast<const float4*>(table + kCols + at);
+                v[i] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at]), __fmul_rn(xs, s.x)), b.x);
+                v[i + 1] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 1]), __fmul_rn(xs, s.y)), b.y);
+                v[i + 2] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 2]), __fmul_rn(xs, s.z)), b.z);
+                v[i + 3] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 3]), __fmul_rn(xs, s.w)), b.w);
+              }
+              if (p.clamp) {
+#pragma unroll
+                for (int i = 0; i < kOf; ++i) v[i] = act_clamp(v[i], p.lo, p.hi);
+              }
+              uint4 w;
+              if constexpr (BF16)
+                w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+              else
+                w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+              *reinterpret_cast<uint4*>(chunk + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = w;
+            }
+            if (p.vec_y && mrow + 32 <= q.rows && (p.whole_units || n + kEach <= p.N)) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && n < p.N) tma_store_2d(&tmY, chunk, n, static_cast<int>(row0));
+            } else {
+              __syncwarp();
+              constexpr int kRows = 32 / kEach;   // rows at a time
+              const int col = lane % kEach, rows = min(32, q.rows - mrow);
+              for (int r = lane / kEach; r < rows; r += kRows) {
+                if (n + col < p.N && CONVF_IN_BOUNDS(row0 + r < p.rows, p.status)) {
+                  const long long at = (row0 + r) * p.ldy + n + col;
+                  const uint8_t* from = chunk + r * 64 + (((col * 64 / kEach >> 4) ^ ((r >> 1) & 3)) << 4) + col * (64 / kEach) % 16;
+                  if constexpr (BF16)
+                    static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(from);
+                  else
+                    static_cast<uint32_t*>(p.y)[at] = *reinterpret_cast<const uint32_t*>(from);
+                }
+              }
+            }
+            if (lane == 0) bulk_commit();   // (a group each, stored by TMA or not: places are taken in turn)
+          }
+        };
+        if (p.out_bf16)
+          send(std::true_type{});
+        else
+          send(std::false_type{});
       }
-      int8_put_columns(p, finish, acc, held, q.row0 + c0, q.rows - c0, n);
+      __syncwarp();   // the table has been read
     }
+    if (lane == 0) bulk_wait_all();   // the stores have been written before the CTA ends
   }
 
 teardown:
@@ -311,7 +396,7 @@ teardown:
 }  // namespace
 
 cudaError_t launch_linear_int8_many(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                                    cudaStream_t stream) {
+                                    const CUtensorMap& tmY, cudaStream_t stream) {
   using Cfg = Int8ManyCfg;
   static OncePerDevice once;
   const cudaError_t e = once([] {
@@ -323,7 +408,7 @@ cudaError_t launch_linear_int8_many(const LinearParams& p, const LinearPlan& pla
     return cudaFuncSetAttribute(linear_int8_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(linear_int8_many_kernel, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, 2, p, tmW, tmX);
+  return launch_pdl(linear_int8_many_kernel, dim3(plan.grid), dim3(Cfg::kThreads), Cfg::kSmem, stream, 2, p, tmW, tmX, tmY);
 }
 
 }  // namespace convf

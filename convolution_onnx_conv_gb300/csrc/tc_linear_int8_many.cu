@@ -44,7 +44,7 @@ struct Int8ManyCfg {
   static_assert(256 * (kRegsEpi + kRegsX + kRegsW) + 128 * kRegsOther <= kThreads * kRegs, "register split");
   static_assert((2 * kStages + 2 * kAUnits + 2 * kBUnits + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
   static_assert(kDCol + 2 * TN <= 512, "TMEM columns");
-  static_assert(2 * kStages % kAUnits == 0, "places of x go with the stages");
+  static_assert(kAUnits % 2 == 0 && kBUnits % 2 == 0, "each unit of a stage has places of its own");
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -194,37 +194,40 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsX));
     const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - 4) >> 2;   // this thread's row; its unit of a stage
-    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * kUnitCols;
+    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t afull0 = map_to_rank(smem_u32(afull), 0);
     const uint8_t* from[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) from[j] = sX + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
-    // (a turn of all stages, so that every address is one of these and a constant)
-    uint32_t phase = 0;
-    for (long long k = 0; k < blocks; k += kStages, phase ^= 1) {
+    int stage = 0, unit = h;
+    uint32_t phase = 0, uphase = 0;
+#pragma unroll 1
+    for (long long k = 0; k < blocks; ++k) {
+      if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      uint4 v[4];
 #pragma unroll
-      for (int s = 0; s < kStages; ++s) {
-        if (k + s >= blocks) break;
-        constexpr int kTurn = kAUnits / 2;   // stages that the places of x last
-        const uint32_t uphase = kTurn == kStages ? phase : s / kTurn & 1;
-        uint64_t* const place = &aempty[2 * (s % kTurn)] + h;
-        if (!mbar_wait(&full[s], phase, abort_flag, p.status)) goto teardown;
-        uint4 v[4];
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kXBytes);
+      const bool room = mbar_test_wait(&aempty[unit], uphase ^ 1);   // (asked before the arithmetic)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      uint32_t f[2][16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + s * Cfg::kXBytes);
-        const bool room = mbar_test_wait(place, uphase ^ 1);   // (asked before the arithmetic)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        uint32_t f[2][16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
-        if (!room && !mbar_wait(place, uphase ^ 1, abort_flag, p.status)) goto teardown;
-        tc_fence_after();
-        tmem_st_32x32b_x16(to0 + 2 * (s % kTurn) * kUnitCols, f[0]);
-        tmem_st_32x32b_x16(to0 + 2 * (s % kTurn) * kUnitCols + 16, f[1]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(smem_u32(&afull[2 * (s % kTurn)] + h), 0));
+      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
+      if (!room && !mbar_wait(&aempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
+      tc_fence_after();
+      tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
+      tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_cta(afull0 + 8 * unit);
+      if ((unit += 2) >= kAUnits) {
+        unit = h;
+        uphase ^= 1;
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
       }
     }
   } else if (warp < 20) {
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     // 16 bytes at a time: thread id's are those of row (id + 128 i) % 96, and j = (id + 128 i) / 96 of a unit's four
     constexpr int kPer = Cfg::kWRows * 4 / 128;
     const int id = threadIdx.x & 127, h = (warp - 12) >> 2;   // its unit of a stage
+    const uint32_t bfull0 = map_to_rank(smem_u32(bfull), 0);
     const uint8_t* from[kPer];
     uint8_t* to[kPer][2];
 #pragma unroll
@@ -241,6 +245,8 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) to[i][e] = sB + row * 128 + (((row & 7) ^ (2 * j + e)) << 4);   // half e of the 16
     }
+    // (a turn of all stages in one piece: addresses are constants then; the other loops are not unrolled, the kernel's
+    // code passes the instruction caches already: 694 -> 667 us for 8192^3)
     uint32_t phase = 0, bphase = 0;
     int place = h;
     for (long long k = 0; k < blocks; k += kStages, phase ^= 1) {
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         }
         fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(smem_u32(&bfull[place]), 0));
+        if (lane == 0) mbar_arrive_remote_cta(bfull0 + 8 * place);
         if ((place += 2) >= kBUnits) {
           place = h;
           bphase ^= 1;

@@ -135,11 +135,11 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   };
   const long long nt = ceil_div(d.N, 128), nt_many = ceil_div(d.N, kManyCols);
   if (int8) {
-    for (int tile = 16; tile <= 64; tile *= 2) {
+    for (int tile = 16; tile <= 64; tile *= 4) {
       for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
         const int units = few_clusters(dev, num_sms, d.dtype, tile, split);
         if (units < 1 || (split > 1 && row_tiles(tile) * nt > units)) continue;   // sharing a tile pays in a single wave
-        offer(kLinearInt8, tile, split, units, nt, tile == 16 ? 300 : tile == 32 ? 400 : 350,
+        offer(kLinearInt8, tile, split, units, nt, tile == 16 ? 300 : 350,
               split == 1 ? 700 : 1000 + 500 * split + 75 * tile);
       }
     }

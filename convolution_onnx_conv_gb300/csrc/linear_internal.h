@@ -124,7 +124,7 @@ enum LinearForm : int { kLinearFew = 0, kLinearMany = 1, kLinearInt8 = 2 };
 struct LinearPlan {
   int form;
   int tile;     // rows of x per tile: kLinearFew 16, 32 or 64; kLinearMany 128, or 256 on CTA pairs;
-                // kLinearInt8 16, 32 or 64, or kInt8PairRows on CTA pairs
+                // kLinearInt8 16 or 64, or kInt8PairRows on CTA pairs
   int split;    // kLinearFew, kLinearInt8: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
   int grid;     // CTAs
 };

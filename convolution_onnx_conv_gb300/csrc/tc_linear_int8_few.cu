@@ -1,12 +1,12 @@
 // Linear layers on int8 operands for few rows per weight matrix: y^T = W x^T with integer sums, on tcgen05 (see
-// linear_int8_dev.cuh).  16, 32 or 64 rows of x are a tile's columns, and the CTAs of a cluster share a tile's
+// linear_int8_dev.cuh).  16 or 64 rows of x are a tile's columns, and the CTAs of a cluster share a tile's
 // reduction where there are fewer tiles than SMs, as in tc_linear_few.cu; their partial sums are integers too.
 //
-//   warp 0      TMA: weight and x tiles of 128 values
-//   warp 1      TMEM, MMA issue
-//   warp 2      the tile schedule
-//   warps 4-..  int8 -> fp16, in groups of four warps that take a unit each in turn
-//   the last    epilogue: 4 warps, or 8 that take half of the columns each
+//   warp 0        TMA: weight and x tiles of 128 values
+//   warp 1        TMEM, MMA issue
+//   warps 2, 3    int8 -> fp16 of x (64 columns: warps 4-7)
+//   8 warps       int8 -> fp16 of the weights: two groups of four warps, each a unit of every stage
+//   the last      epilogue: 4 warps, or 8 that take half of the columns each
 #include "linear_int8_dev.cuh"
 
 namespace convf {
@@ -15,25 +15,26 @@ namespace {
 
 template <int TN>
 struct Int8Cfg {
-  static constexpr int kEpiWarps = TN > 32 ? 8 : 4;
-  static constexpr int kCols = TN > 32 ? TN / 2 : TN;           // columns per epilogue thread
-  // 16 and 32 columns: two CTAs on an SM, so that one's start, exchange and end are behind the other's loads (and a
+  // 16 columns: two CTAs on an SM, so that one's start, exchange and end are behind the other's loads (and a
   // dependent launch's start behind this one's end)
-  static constexpr int kPerSm = TN <= 32 ? 2 : 1;
-  static constexpr int kGroups = kPerSm == 2 ? 2 : 3;           // of four converting warps
-  static constexpr int kThreads = 128 + 128 * kGroups + 32 * kEpiWarps;
+  static constexpr int kPerSm = TN == 16 ? 2 : 1;
+  static constexpr int kXWarps = TN == 16 ? 2 : 4, kXFirst = TN == 16 ? 2 : 4;   // that convert x, and the first of them
+  static constexpr int kWFirst = TN == 16 ? 4 : 8, kEpiFirst = kWFirst + 8;
+  static constexpr int kEpiWarps = TN == 16 ? 4 : 8;
+  static constexpr int kCols = TN == 16 ? TN : TN / 2;          // columns per epilogue thread
+  static constexpr int kThreads = 32 * (kEpiFirst + kEpiWarps);
   static constexpr int kTmemCols = kPerSm == 2 ? 256 : 512;
   static constexpr int kWBytes = 128 * kKBlockBytes, kXBytes = TN * kKBlockBytes;   // of a stage, int8
   static constexpr int kBBytes = TN * 2 * kUnit;                // of a unit of x, fp16
-  static constexpr int kUnits = kPerSm == 2 ? 6 : 8;
-  static constexpr int kDCol = kUnits * kUnitCols;              // the accumulators' first column
+  static constexpr int kBlocks = kPerSm == 2 ? 3 : 5;   // places of converted stages
+  static constexpr int kDCol = 2 * kBlocks * kUnitCols;            // the accumulators' first column
   static constexpr int kRedBytes = TN * 128 * 4;                // partial sums of this CTA's columns, by rank
   static constexpr int kBarBytes = 512;
-  static constexpr int kFixed = 1024 + kUnits * kBBytes + kRedBytes + kScheduleBytes + kBarBytes;
+  static constexpr int kFixed = 1024 + 2 * kBlocks * kBBytes + kRedBytes + kScheduleBytes + kBarBytes;
   static constexpr int kBudget = kPerSm == 2 ? 115712 : 232448;
   static constexpr int kStages = (kBudget - kFixed) / (kWBytes + kXBytes);
   static constexpr int kSmem = kFixed + kStages * (kWBytes + kXBytes);
-  static_assert(kStages >= 3 && (2 * kStages + 2 * kUnits + 6) * 8 + 8 <= kBarBytes && kSmem <= kBudget, "shared memory");
+  static_assert(kStages >= 3 && (2 * kStages + 2 * kBlocks + 6) * 8 + 8 <= kBarBytes && kSmem <= kBudget, "shared memory");
   static_assert(kDCol + 2 * TN <= kTmemCols, "TMEM columns");
 };
 
@@ -42,18 +43,18 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
     linear_int8_few_kernel(const LinearParams p, const int split, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
   using Cfg = Int8Cfg<TN>;
-  constexpr int kStages = Cfg::kStages, kUnits = Cfg::kUnits, kCols = Cfg::kCols;
-  constexpr int kChunkUnits = kInt8Chunk / kUnit;
+  constexpr int kStages = Cfg::kStages, kBlocks = Cfg::kBlocks, kCols = Cfg::kCols;
+  constexpr int kChunkBlocks = kInt8Chunk / kKBlockBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sW = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sX = sW + kStages * Cfg::kWBytes;
   uint8_t* sB = sX + kStages * Cfg::kXBytes;
-  int* red = reinterpret_cast<int*>(sB + kUnits * Cfg::kBBytes);
+  int* red = reinterpret_cast<int*>(sB + 2 * kBlocks * Cfg::kBBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + Cfg::kRedBytes);   // int8 tiles are here
   uint64_t* empty = full + kStages;     // and have been read
-  uint64_t* cfull = empty + kStages;    // a unit is converted
-  uint64_t* cempty = cfull + kUnits;    // and its MMAs have read it
-  uint64_t* tfull = cempty + kUnits;    // an accumulator holds a chunk's sums
+  uint64_t* cfull = empty + kStages;    // a stage is converted: weights in TMEM, x in sB
+  uint64_t* cempty = cfull + kBlocks;   // and its MMAs have read it
+  uint64_t* tfull = cempty + kBlocks;   // an accumulator holds a chunk's sums
   uint64_t* tempty = tfull + 2;         // and has been read
   uint64_t* rfull = tempty + 2;         // every rank's partial sums of this CTA's columns have arrived
   uint64_t* rfree = rfull + 1;          // every rank has read what this CTA sent it
@@ -67,11 +68,11 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 8);   // four warps for each of its two units
+      mbar_init(&empty[s], 8 + Cfg::kXWarps);
     }
-    for (int u = 0; u < kUnits; ++u) {
-      mbar_init(&cfull[u], 4);
-      mbar_init(&cempty[u], 1);
+    for (int b = 0; b < kBlocks; ++b) {
+      mbar_init(&cfull[b], 8 + Cfg::kXWarps);
+      mbar_init(&cempty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -112,135 +113,157 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
   const long long tiles = tile_count(p, prefix);
   const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;
 
-  if (warp < 4) {
-    if (warp == 0) {
-      if (lane == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        for (long long t = t0; t < tiles; t += tstep) {
-          const LinearTile q = tile_at<TN, 128>(p, prefix, t);
-          for (int kb = ka; kb < kb_end; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) goto teardown;
-            mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes);
-            tma_load_3d(sW + stage * Cfg::kWBytes, &tmW, &full[stage], kb * kKBlockBytes, q.n0, q.e);
-            tma_load_2d(sX + stage * Cfg::kXBytes, &tmX, &full[stage], kb * kKBlockBytes, q.row0);
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
-            }
-          }
-        }
-      }
-    } else if (warp == 1) {
-      // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
-      // registers, which is where the MMA takes its descriptors from
-      const bool issue = elect_one();
-      constexpr uint32_t idesc = idesc_f16_f32(128, TN);
-      const uint64_t b0 = sdesc_kmajor_sw128(smem_u32(sB));
-      int unit = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
-      for (long long j = 0; j < mine; ++j) {
-        const int units = 2 * (kb_end - ka);
-        for (int i = 0, in_chunk = 0; i < units; ++i) {
-          const bool first = in_chunk == 0, last = ++in_chunk == kChunkUnits || i == units - 1;
-          // both barriers are asked at once, before either is waited for
-          bool ready = mbar_test_wait(&cfull[unit], phase);
-          if (first) ready = mbar_test_wait(&tempty[buf], bphase ^ 1) & ready;
-          if (!ready) {
-            if (first && !mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) goto teardown;
-            if (!mbar_wait(&cfull[unit], phase, abort_flag, p.status)) goto teardown;
-          }
-          tc_fence_after();
-          const uint32_t a = tmem_base + unit * kUnitCols, d = tmem_base + Cfg::kDCol + buf * TN;
-          const uint64_t b = b0 + unit * (Cfg::kBBytes >> 4);
-          if (issue) {
-#pragma unroll
-            for (int s = 0; s < kUnit / 16; ++s) {   // 16 values: 8 columns of A, 32 bytes of B
-              tc_mma_f16_ts(d, a + 8 * s, b + 2 * s, idesc, !first || s > 0);
-            }
-            tc_commit(&cempty[unit]);
-            if (last) tc_commit(&tfull[buf]);
-          }
-          __syncwarp();
-          if (++unit == kUnits) {
-            unit = 0;
+  const long long blocks = mine * (kb_end - ka);   // stages of this CTA
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (long long t = t0; t < tiles; t += tstep) {
+        const LinearTile q = tile_at<TN, 128>(p, prefix, t);
+        for (int kb = ka; kb < kb_end; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) goto teardown;
+          mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes);
+          tma_load_3d(sW + stage * Cfg::kWBytes, &tmW, &full[stage], kb * kKBlockBytes, q.n0, q.e);
+          tma_load_2d(sX + stage * Cfg::kXBytes, &tmX, &full[stage], kb * kKBlockBytes, q.row0);
+          if (++stage == kStages) {
+            stage = 0;
             phase ^= 1;
-          }
-          if (last) {
-            in_chunk = 0;
-            buf ^= 1;
-            if (buf == 0) bphase ^= 1;
           }
         }
       }
     }
-  } else if (warp < 4 + 4 * Cfg::kGroups) {
-    const int quad = warp & 3, id = threadIdx.x & 127;   // id: this thread's weight row
-    const uint32_t a0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    constexpr int kTasks = TN * 4, kPer = (kTasks + 127) / 128;   // x: 16 bytes a task, a row's four by j
-    // unit u of this CTA's: stage u / 2 % kStages, half u % 2, place u % kUnits
-    const long long units = 2 * mine * (kb_end - ka);
-    const int g = (warp - 4) >> 2;
-    int stage = g / 2 % kStages, place = g % kUnits;
-    uint32_t phase = g / 2 / kStages & 1, pphase = g / kUnits & 1;
-    for (long long u = g; u < units; u += Cfg::kGroups) {
-      const uint32_t half = (static_cast<uint32_t>(u) & 1) << 6;
-      if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-      const uint8_t* w = sW + stage * Cfg::kWBytes + id * kKBlockBytes;
-      const uint8_t* x = sX + stage * Cfg::kXBytes;
-      uint4 wv[4], xv[kPer];
+  } else if (warp == 1) {
+    // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
+    // registers, which is where the MMA takes its descriptors from
+    const bool issue = elect_one();
+    constexpr uint32_t idesc = idesc_f16_f32(128, TN);
+    const uint64_t b0 = sdesc_kmajor_sw128(smem_u32(sB));
+    int block = 0, buf = 0;
+    uint32_t phase = 0, tphase = 0;
+    for (long long j = 0; j < mine; ++j) {
+      for (int kb = ka, in_chunk = 0; kb < kb_end; ++kb) {
+        const bool first = in_chunk == 0, last = ++in_chunk == kChunkBlocks || kb == kb_end - 1;
+        // both barriers are asked at once, before either is waited for
+        bool ready = mbar_test_wait(&cfull[block], phase);
+        if (first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
+        if (!ready) {
+          if (!mbar_wait(&cfull[block], phase, abort_flag, p.status)) goto teardown;
+          if (first && !mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status)) goto teardown;
+        }
+        tc_fence_after();
+        const uint32_t a = tmem_base + 2 * block * kUnitCols, d = tmem_base + Cfg::kDCol + buf * TN;
+        const uint64_t b = b0 + 2 * block * (Cfg::kBBytes >> 4);
+        if (issue) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wv[j] = *reinterpret_cast<const uint4*>(w + ((((id & 7) ^ j) << 4) ^ half));
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int task = id + 128 * i, row = task % TN, j = task / TN;
-        if (kTasks % 128 == 0 || task < kTasks)
-          xv[i] = *reinterpret_cast<const uint4*>(x + row * kKBlockBytes + ((((row & 7) ^ j) << 4) ^ half));
-      }
-      const bool room = mbar_test_wait(&cempty[place], pphase ^ 1);   // (asked before the arithmetic)
-      uint32_t f[16];
-      f16_of_int8_16(wv[0], f);
-      f16_of_int8_16(wv[1], f + 8);
-      if (!room && !mbar_wait(&cempty[place], pphase ^ 1, abort_flag, p.status)) goto teardown;
-      tc_fence_after();
-      tmem_st_32x32b_x16(a0 + place * kUnitCols, f);
-      f16_of_int8_16(wv[2], f);
-      f16_of_int8_16(wv[3], f + 8);
-      tmem_st_32x32b_x16(a0 + place * kUnitCols + 16, f);
-      uint8_t* b = sB + place * Cfg::kBBytes;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int task = id + 128 * i, row = task % TN, j = task / TN;
-        if (kTasks % 128 == 0 || task < kTasks) {
-          uint32_t o[8];
-          f16_of_int8_16(xv[i], o);
-          *reinterpret_cast<uint4*>(b + row * 128 + (((2 * j) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(b + row * 128 + (((2 * j + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int s = 0; s < 2 * kUnit / 16; ++s)   // 16 values: 8 columns of A, 32 bytes of a unit of B
+            tc_mma_f16_ts(d, a + 8 * s, b + (s / 4) * (Cfg::kBBytes >> 4) + 2 * (s % 4), idesc, !first || s > 0);
+          tc_commit(&cempty[block]);
+          if (last) tc_commit(&tfull[buf]);
+        }
+        __syncwarp();
+        if (++block == kBlocks) {
+          block = 0;
+          phase ^= 1;
+        }
+        if (last) {
+          in_chunk = 0;
+          buf ^= 1;
+          if (buf == 0) tphase ^= 1;
         }
       }
+    }
+  } else if (warp >= Cfg::kXFirst && warp < Cfg::kXFirst + Cfg::kXWarps) {
+    // 16 bytes at a time: of a stage's TN rows of 8, thread id takes those of row (id + i kX) % TN, 16-byte place
+    // (id + i kX) / TN
+    constexpr int kX = 32 * Cfg::kXWarps, kPer = TN * 8 / kX, kAtOnce = kPer < 4 ? kPer : 4;
+    const int id = threadIdx.x - 32 * Cfg::kXFirst;
+    int stage = 0, block = 0;
+    uint32_t phase = 0, bphase = 0;
+    bool here = false;
+#pragma unroll 1
+    for (long long k = 0; k < blocks; ++k) {
+      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      bool room = mbar_test_wait(&cempty[block], bphase ^ 1);
+      const uint8_t* x = sX + stage * Cfg::kXBytes;
+      uint8_t* b = sB + 2 * block * Cfg::kBBytes;
+#pragma unroll
+      for (int i0 = 0; i0 < kPer; i0 += kAtOnce) {
+        uint4 v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int task = id + (i0 + i) * kX, row = task % TN, j = task / TN;
+          v[i] = *reinterpret_cast<const uint4*>(x + row * kKBlockBytes + ((j ^ (row & 7)) << 4));
+        }
+        if (!room && !mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
+        room = true;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int task = id + (i0 + i) * kX, row = task % TN, j = task / TN;
+          uint32_t o[8];
+          f16_of_int8_16(v[i], o);
+          uint8_t* to = b + (j >> 2) * Cfg::kBBytes + row * 128;   // unit j / 4, and of its 8 places 2 (j % 4) and the next
+          *reinterpret_cast<uint4*>(to + (((2 * (j & 3)) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to + (((2 * (j & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      here = mbar_test_wait(&full[stage], phase);   // the next stage
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cfull[block]);
+      if (++block == kBlocks) {
+        block = 0;
+        bphase ^= 1;
+      }
+    }
+  } else if (warp >= Cfg::kWFirst && warp < Cfg::kEpiFirst) {
+    const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - Cfg::kWFirst) >> 2;   // this thread's weight row; its unit of a stage
+    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * kUnitCols;
+    const uint8_t* from[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) from[j] = sW + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
+    int stage = 0, block = 0;
+    uint32_t phase = 0, bphase = 0;
+    bool here = false;
+#pragma unroll 1
+    for (long long k = 0; k < blocks; ++k) {
+      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kWBytes);
+      const bool room = mbar_test_wait(&cempty[block], bphase ^ 1);   // (asked before the arithmetic: an answer takes 100 cycles)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      uint32_t f[2][16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
+      if (!room && !mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
+      tc_fence_after();
+      tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols, f[0]);
+      tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols + 16, f[1]);
+      here = mbar_test_wait(&full[stage], phase);   // the next stage
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&cfull[place]);
-        mbar_arrive(&empty[stage]);
-      }
-      place += Cfg::kGroups;
-      if (place >= kUnits) {
-        place -= kUnits;
-        pphase ^= 1;
-      }
-      // the unit kGroups further on
-      stage += (static_cast<int>(u & 1) + Cfg::kGroups) / 2;
-      if (stage >= kStages) {
-        stage -= kStages;
-        phase ^= 1;
+      if (lane == 0) mbar_arrive(&cfull[block]);
+      if (++block == kBlocks) {
+        block = 0;
+        bphase ^= 1;
       }
     }
-  } else {
+  } else if (warp >= Cfg::kEpiFirst) {
     const int quad = warp & 3;
-    const int c0 = (warp - 4 - 4 * Cfg::kGroups) / 4 * kCols;   // this thread's columns
+    const int c0 = (warp - Cfg::kEpiFirst) / 4 * kCols;   // this thread's columns
     const uint32_t from0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::kDCol + c0;
     int buf = 0;
     uint32_t bphase = 0, rphase = 0;
@@ -261,7 +284,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0;
 #pragma unroll 1
-      for (int kb = ka; kb < kb_end; kb += kInt8Chunk / kKBlockBytes) {   // a chunk
+      for (int kb = ka; kb < kb_end; kb += kChunkBlocks) {
         if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
         tc_fence_after();
         int8_add_columns(acc, from0 + buf * TN);
@@ -361,7 +384,6 @@ cudaError_t launch_linear_int8_few(const LinearParams& p, const LinearPlan& plan
                                cudaStream_t stream) {
   switch (plan.tile) {
     case 16: return launch_t<16>(p, plan, tmW, tmX, stream);
-    case 32: return launch_t<32>(p, plan, tmW, tmX, stream);
     case 64: return launch_t<64>(p, plan, tmW, tmX, stream);
   }
   return cudaErrorInvalidValue;
@@ -370,7 +392,6 @@ cudaError_t launch_linear_int8_few(const LinearParams& p, const LinearPlan& plan
 int linear_int8_max_clusters(int tile, int split, int num_sms) {
   switch (tile) {
     case 16: return max_clusters_t<16>(split, num_sms);
-    case 32: return max_clusters_t<32>(split, num_sms);
     case 64: return max_clusters_t<64>(split, num_sms);
   }
   return 0;

@@ -9,8 +9,8 @@
 // and 96 weight rows of it (a single CTA's 128 x 192 tile: 128 and 192), 84 integer instructions at half rate for
 // each of four warps.  What a unit goes through is long (its bytes' arrival, the conversion, the pair's barrier, the
 // MMAs, their end seen in both CTAs), and TMEM holds only four units of x beside two accumulators of 192 columns: so
-// x is converted ahead, in registers, and waits for a place for its stores only; weights, with places for six units
-// in shared memory, have warps of their own.
+// x is converted ahead, in registers, and waits for a place for its stores only, and weights have warps of their own.
+// A unit's weights go to shared memory with as many places, and one barrier each way serves both operands.
 //
 //   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (of a pair: the leader's)
 //   warp 2        the tile schedule
@@ -33,18 +33,18 @@ struct Int8ManyCfg {
   static constexpr int kThreads = 896;
   static constexpr int kXBytes = 128 * kKBlockBytes, kWBytes = kWRows * kKBlockBytes;   // of a stage, int8
   static constexpr int kBBytes = kWRows * 2 * kUnit; // of a unit of weights, fp16
-  static constexpr int kStages = 4, kAUnits = 4, kBUnits = 6;   // places: int8 stages, units of x, units of weights
-  static constexpr int kDCol = kAUnits * kUnitCols;  // the accumulators' first column
+  static constexpr int kStages = 4, kUnits = 4;   // places: int8 stages, units
+  static constexpr int kDCol = kUnits * kUnitCols;  // the accumulators' first column
   // per epilogue warp: two chunks of 32 rows of 64 bytes on their way out, its columns' scales and biases
   static constexpr int kOutBytes = 2 * 2048, kTableBytes = 2 * kCols * 4;
-  static constexpr int kBarBytes = 512;
-  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + kBUnits * kBBytes + 8 * (kOutBytes + kTableBytes) + kBarBytes + kScheduleBytes;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + kUnits * kBBytes + 8 * (kOutBytes + kTableBytes) + kBarBytes + kScheduleBytes;
   // registers: 72 per thread at launch; the epilogue's two warpgroups take what the others give up
   static constexpr int kRegs = 72, kRegsEpi = 128, kRegsX = 56, kRegsW = 48, kRegsOther = 40;
   static_assert(256 * (kRegsEpi + kRegsX + kRegsW) + 128 * kRegsOther <= kThreads * kRegs, "register split");
-  static_assert((2 * kStages + 2 * kAUnits + 2 * kBUnits + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
+  static_assert((2 * kStages + 2 * kUnits + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
   static_assert(kDCol + 2 * TN <= 512, "TMEM columns");
-  static_assert(kAUnits % 2 == 0 && kBUnits % 2 == 0, "each unit of a stage has places of its own");
+  static_assert(kUnits % 2 == 0, "each unit of a stage has places of its own");
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -56,20 +56,18 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     linear_int8_many_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                             const __grid_constant__ CUtensorMap tmY) {
   using Cfg = Int8ManyCfg;
-  constexpr int kStages = Cfg::kStages, kAUnits = Cfg::kAUnits, kBUnits = Cfg::kBUnits, kCols = Cfg::kCols;
+  constexpr int kStages = Cfg::kStages, kUnits = Cfg::kUnits, kCols = Cfg::kCols;
   constexpr int kChunkBlocks = kInt8Chunk / kKBlockBytes;
   extern __shared__ __align__(1024) uint8_t sX[];   // (the swizzle goes by address bits 7 to 9)
   uint8_t* sW = sX + kStages * Cfg::kXBytes;
   uint8_t* sB = sW + kStages * Cfg::kWBytes;
-  uint8_t* sOut = sB + kBUnits * Cfg::kBBytes;
+  uint8_t* sOut = sB + kUnits * Cfg::kBBytes;
   float* sTable = reinterpret_cast<float*>(sOut + 8 * Cfg::kOutBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * (Cfg::kOutBytes + Cfg::kTableBytes));   // int8 tiles are here
   uint64_t* empty = full + kStages;     // and have been read
-  uint64_t* afull = empty + kStages;    // a unit of x is in TMEM, of both CTAs (the leader's)
-  uint64_t* aempty = afull + kAUnits;   // and its MMAs have read it
-  uint64_t* bfull = aempty + kAUnits;   // a unit of weights is converted, of both CTAs (the leader's)
-  uint64_t* bempty = bfull + kBUnits;   // and its MMAs have read it
-  uint64_t* tfull = bempty + kBUnits;  // an accumulator holds a chunk's sums
+  uint64_t* cfull = empty + kStages;    // a unit of x is in TMEM and one of weights in sB, of both CTAs (the leader's)
+  uint64_t* cempty = cfull + kUnits;    // and its MMAs have read them
+  uint64_t* tfull = cempty + kUnits;    // an accumulator holds a chunk's sums
   uint64_t* tempty = tfull + 2;         // and has been read, in both CTAs (the leader's)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -83,13 +81,9 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 16);
     }
-    for (int u = 0; u < kAUnits; ++u) {
-      mbar_init(&afull[u], 8);
-      mbar_init(&aempty[u], 1);
-    }
-    for (int b = 0; b < kBUnits; ++b) {
-      mbar_init(&bfull[b], 8);
-      mbar_init(&bempty[b], 1);
+    for (int u = 0; u < kUnits; ++u) {
+      mbar_init(&cfull[u], 16);
+      mbar_init(&cempty[u], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -145,42 +139,35 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       const bool issue = elect_one();
       constexpr uint32_t idesc = idesc_f16_f32(kInt8PairRows, TN);
       const uint64_t b0 = sdesc_kmajor_sw128(smem_u32(sB));
-      int unit = 0, bunit = 0, buf = 0;
-      uint32_t aphase = 0, bphase = 0, tphase = 0;
+      int unit = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
       for (long long j = 0; j < mine; ++j) {
         for (int kb = 0, in_chunk = 0; kb < p.num_kb; ++kb) {
           const bool first = in_chunk == 0, last = ++in_chunk == kChunkBlocks || kb == p.num_kb - 1;
           const uint32_t d = tmem_base + Cfg::kDCol + buf * TN;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            // the barriers are asked at once, before any is waited for
-            bool ready = mbar_test_wait_cluster(&afull[unit], aphase);
-            ready = mbar_test_wait_cluster(&bfull[bunit], bphase) & ready;
+            // both barriers are asked at once, before either is waited for
+            bool ready = mbar_test_wait_cluster(&cfull[unit], phase);
             if (h == 0 && first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
             if (!ready) {
-              if (!mbar_wait_cluster(&afull[unit], aphase, abort_flag, p.status)) goto teardown;
-              if (!mbar_wait_cluster(&bfull[bunit], bphase, abort_flag, p.status)) goto teardown;
+              if (!mbar_wait_cluster(&cfull[unit], phase, abort_flag, p.status)) goto teardown;
               if (h == 0 && first && !mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status)) goto teardown;
             }
             tc_fence_after();
             const uint32_t a = tmem_base + unit * kUnitCols;
-            const uint64_t b = b0 + bunit * (Cfg::kBBytes >> 4);
+            const uint64_t b = b0 + unit * (Cfg::kBBytes >> 4);
             if (issue) {
 #pragma unroll
               for (int s = 0; s < kUnit / 16; ++s)   // 16 values: 8 columns of A, 32 bytes of B
                 tc_mma_f16_ts_pair(d, a + 8 * s, b + 2 * s, idesc, !first || h > 0 || s > 0);
-              tc_commit_pair(&aempty[unit], 3);
-              tc_commit_pair(&bempty[bunit], 3);
+              tc_commit_pair(&cempty[unit], 3);
               if (h == 1 && last) tc_commit_pair(&tfull[buf], 3);
             }
             __syncwarp();
-            if (++unit == kAUnits) {
+            if (++unit == kUnits) {
               unit = 0;
-              aphase ^= 1;
-            }
-            if (++bunit == kBUnits) {
-              bunit = 0;
-              bphase ^= 1;
+              phase ^= 1;
             }
           }
           if (last) {
@@ -195,39 +182,41 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsX));
     const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - 4) >> 2;   // this thread's row; its unit of a stage
     const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t afull0 = map_to_rank(smem_u32(afull), 0);
+    const uint32_t cfull0 = map_to_rank(smem_u32(cfull), 0);
     const uint8_t* from[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) from[j] = sX + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
     int stage = 0, unit = h;
     uint32_t phase = 0, uphase = 0;
+    bool here = false;
 #pragma unroll 1
     for (long long k = 0; k < blocks; ++k) {
-      if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       uint4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kXBytes);
-      const bool room = mbar_test_wait(&aempty[unit], uphase ^ 1);   // (asked before the arithmetic)
+      const bool room = mbar_test_wait(&cempty[unit], uphase ^ 1);   // (asked before the arithmetic: an answer takes 100 cycles)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
-      uint32_t f[2][16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
-      if (!room && !mbar_wait(&aempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
-      tc_fence_after();
-      tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
-      tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(afull0 + 8 * unit);
-      if ((unit += 2) >= kAUnits) {
-        unit = h;
-        uphase ^= 1;
-      }
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
+      }
+      uint32_t f[2][16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
+      if (!room && !mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
+      tc_fence_after();
+      tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
+      tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
+      here = mbar_test_wait(&full[stage], phase);   // of the next stage
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_cta(cfull0 + 8 * unit);
+      if ((unit += 2) >= kUnits) {
+        unit = h;
+        uphase ^= 1;
       }
     }
   } else if (warp < 20) {
@@ -235,47 +224,48 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     // 16 bytes at a time: thread id's are those of row (id + 128 i) % 96, and j = (id + 128 i) / 96 of a unit's four
     constexpr int kPer = Cfg::kWRows * 4 / 128;
     const int id = threadIdx.x & 127, h = (warp - 12) >> 2;   // its unit of a stage
-    const uint32_t bfull0 = map_to_rank(smem_u32(bfull), 0);
+    const uint32_t cfull0 = map_to_rank(smem_u32(cfull), 0);
     const uint8_t* from[kPer];
-    uint8_t* to[kPer][2];
+    uint8_t* to[kPer];   // the first half of the 16; the other is at 16 bytes before or behind it
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int row = (id + 128 * i) % Cfg::kWRows, j = (id + 128 * i) / Cfg::kWRows;
       from[i] = sW + row * kKBlockBytes + (((row & 7) ^ j ^ (4 * h)) << 4);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) to[i][e] = sB + row * 128 + (((row & 7) ^ (2 * j + e)) << 4);   // half e of the 16
+      to[i] = sB + row * 128 + (((row & 7) ^ (2 * j)) << 4);
     }
-    // (a turn of all stages in one piece: addresses are constants then; the other loops are not unrolled, the kernel's
-    // code passes the instruction caches already: 694 -> 667 us for 8192^3)
-    uint32_t phase = 0, bphase = 0;
-    int place = h;
-    for (long long k = 0; k < blocks; k += kStages, phase ^= 1) {
+    const int other = (id & 1) ? -16 : 16;   // (rows of a thread are all odd or all even)
+    int stage = 0, unit = h;
+    uint32_t phase = 0, uphase = 0;
+    bool here = false;
+#pragma unroll 1
+    for (long long k = 0; k < blocks; ++k) {
+      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      uint4 v[kPer];
 #pragma unroll
-      for (int s = 0; s < kStages; ++s) {
-        if (k + s >= blocks) break;
-        if (!mbar_wait(&full[s], phase, abort_flag, p.status)) goto teardown;
-        uint4 v[kPer];
+      for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + stage * Cfg::kWBytes);
+      const bool room = mbar_test_wait(&cempty[unit], uphase ^ 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (!room && !mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
+      const int at = unit * Cfg::kBBytes;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + s * Cfg::kWBytes);
-        const bool room = mbar_test_wait(&bempty[place], bphase ^ 1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        if (!room && !mbar_wait(&bempty[place], bphase ^ 1, abort_flag, p.status)) goto teardown;
-        const int at = place * Cfg::kBBytes;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          uint32_t o[8];
-          f16_of_int8_16(v[i], o);
-          *reinterpret_cast<uint4*>(to[i][0] + at) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(to[i][1] + at) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote_cta(bfull0 + 8 * place);
-        if ((place += 2) >= kBUnits) {
-          place = h;
-          bphase ^= 1;
-        }
+      for (int i = 0; i < kPer; ++i) {
+        uint32_t o[8];
+        f16_of_int8_16(v[i], o);
+        *reinterpret_cast<uint4*>(to[i] + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(to[i] + at + other) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      here = mbar_test_wait(&full[stage], phase);   // of the next stage
+      fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_cta(cfull0 + 8 * unit);
+      if ((unit += 2) >= kUnits) {
+        unit = h;
+        uphase ^= 1;
       }
     }
   } else {

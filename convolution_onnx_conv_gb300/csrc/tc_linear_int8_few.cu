@@ -4,7 +4,7 @@
 //
 //   warp 0        TMA: weight and x tiles of 128 values
 //   warp 1        TMEM, MMA issue
-//   warps 2, 3    int8 -> fp16 of x (64 columns: warps 4-7)
+//   warps 2, 3    int8 -> fp16 of x (64 columns: warps 4-11)
 //   8 warps       int8 -> fp16 of the weights: two groups of four warps, each a unit of every stage
 //   the last      epilogue: 4 warps, or 8 that take half of the columns each
 #include "linear_int8_dev.cuh"
@@ -18,8 +18,8 @@ struct Int8Cfg {
   // 16 columns: two CTAs on an SM, so that one's start, exchange and end are behind the other's loads (and a
   // dependent launch's start behind this one's end)
   static constexpr int kPerSm = TN == 16 ? 2 : 1;
-  static constexpr int kXWarps = TN == 16 ? 2 : 4, kXFirst = TN == 16 ? 2 : 4;   // that convert x, and the first of them
-  static constexpr int kWFirst = TN == 16 ? 4 : 8, kEpiFirst = kWFirst + 8;
+  static constexpr int kXWarps = TN == 16 ? 2 : 8, kXFirst = TN == 16 ? 2 : 4;   // that convert x, and the first of them
+  static constexpr int kWFirst = TN == 16 ? 4 : 12, kEpiFirst = kWFirst + 8;
   static constexpr int kEpiWarps = TN == 16 ? 4 : 8;
   static constexpr int kCols = TN == 16 ? TN : TN / 2;          // columns per epilogue thread
   static constexpr int kThreads = 32 * (kEpiFirst + kEpiWarps);

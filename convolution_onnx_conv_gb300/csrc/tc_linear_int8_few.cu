@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
   const long long tiles = tile_count(p, prefix);
   const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;
 
-  const long long blocks = mine * (kb_end - ka);   // stages of this CTA
+  const int blocks = static_cast<int>(mine * (kb_end - ka));   // stages of this CTA (see tc_linear_int8_many.cu)
 
   if (warp == 0) {
     if (lane == 0) {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
     uint32_t phase = 0, bphase = 0;
     bool here = false;
 #pragma unroll 1
-    for (long long k = 0; k < blocks; ++k) {
+    for (int k = 0; k < blocks; ++k) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       bool room = mbar_test_wait(&cempty[block], bphase ^ 1);
       const uint8_t* x = sX + stage * Cfg::kXBytes;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
     uint32_t phase = 0, bphase = 0;
     bool here = false;
 #pragma unroll 1
-    for (long long k = 0; k < blocks; ++k) {
+    for (int k = 0; k < blocks; ++k) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       uint4 v[4];
 #pragma unroll

@@ -13,7 +13,7 @@
 // A unit's weights go to shared memory with as many places, and one barrier each way serves both operands.
 //
 //   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (of a pair: the leader's)
-//   warp 2        the tile schedule
+//   warp 2        works out the CTA's next tiles
 //   warps 4-11    int8 -> fp16 of x: two groups of four warps, each a unit of every stage
 //   warps 12-19   int8 -> fp16 of the weights, in two groups as well
 //   warps 20-27   epilogue: warp w the rows 32 (w % 4) .. and half of the columns
@@ -26,6 +26,7 @@ namespace convf {
 namespace {
 
 constexpr int TN = kInt8PairCols;   // an MMA's columns: weight rows
+constexpr int kTileBatch = 16;      // tiles that the scheduler works out at a time
 
 struct Int8ManyCfg {
   static constexpr int kWRows = TN / 2;              // weight rows that a CTA loads and converts
@@ -35,14 +36,14 @@ struct Int8ManyCfg {
   static constexpr int kBBytes = kWRows * 2 * kUnit; // of a unit of weights, fp16
   static constexpr int kStages = 4, kUnits = 4;   // places: int8 stages, units
   static constexpr int kDCol = kUnits * kUnitCols;  // the accumulators' first column
-  // per epilogue warp: two chunks of 32 rows of 64 bytes on their way out, its columns' scales and biases
-  static constexpr int kOutBytes = 2 * 2048, kTableBytes = 2 * kCols * 4;
+  // per epilogue warp: three chunks of 32 rows of 64 bytes on their way out, its columns' scales and biases
+  static constexpr int kOutBytes = 3 * 2048, kTableBytes = 2 * kCols * 4;
   static constexpr int kBarBytes = 256;
-  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + kUnits * kBBytes + 8 * (kOutBytes + kTableBytes) + kBarBytes + kScheduleBytes;
+  static constexpr int kSmem = kStages * (kXBytes + kWBytes) + kUnits * kBBytes + 8 * (kOutBytes + kTableBytes) + kBarBytes + 2 * kTileBatch * 16 + kScheduleBytes;
   // registers: 72 per thread at launch; the epilogue's two warpgroups take what the others give up
   static constexpr int kRegs = 72, kRegsEpi = 128, kRegsX = 56, kRegsW = 48, kRegsOther = 40;
   static_assert(256 * (kRegsEpi + kRegsX + kRegsW) + 128 * kRegsOther <= kThreads * kRegs, "register split");
-  static_assert((2 * kStages + 2 * kUnits + 4) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
+  static_assert((2 * kStages + 2 * kUnits + 8) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
   static_assert(kDCol + 2 * TN <= 512, "TMEM columns");
   static_assert(kUnits % 2 == 0, "each unit of a stage has places of its own");
 };
@@ -69,9 +70,12 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   uint64_t* cempty = cfull + kUnits;    // and its MMAs have read them
   uint64_t* tfull = cempty + kUnits;    // an accumulator holds a chunk's sums
   uint64_t* tempty = tfull + 2;         // and has been read, in both CTAs (the leader's)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* tqfull = tempty + 2;        // a batch of tiles is worked out
+  uint64_t* tqempty = tqfull + 2;       // and read by the loads' warp and the epilogue's
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tqempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
+  LinearTile* tileq = reinterpret_cast<LinearTile*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
+  int* prefix = reinterpret_cast<int*>(tileq + 2 * kTileBatch);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -88,6 +92,8 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 16);
+      mbar_init(&tqfull[b], 1);
+      mbar_init(&tqempty[b], 9);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -111,7 +117,20 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   const long long tiles = tile_count(p, prefix);
   const long long t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
   const long long mine = tiles > t0 ? (tiles - t0 - 1) / tstep + 1 : 0;   // tiles of this pair
-  const long long blocks = mine * p.num_kb;                               // and their stages
+  // and their stages (operands that fit the device's memory give less than 2^26; 64 bits cost the converting loops
+  // registers that they have not: 88.6 instead of 84.6 us for 4096^3)
+  const int blocks = static_cast<int>(mine * p.num_kb);
+  // this CTA's j-th tile, read by one thread (the loads') or a warp in the order of j; false: give up
+  auto next_tile = [&](long long j, LinearTile& q, bool whole_warp) {
+    const int slot = static_cast<int>(j / kTileBatch) & 1, at = static_cast<int>(j % kTileBatch);
+    if (at == 0 && !mbar_wait(&tqfull[slot], static_cast<uint32_t>(j / (2 * kTileBatch)) & 1, abort_flag, p.status)) return false;
+    q = tileq[slot * kTileBatch + at];
+    if (at == kTileBatch - 1) {
+      if (whole_warp) __syncwarp();
+      if (!whole_warp || lane == 0) mbar_arrive(&tqempty[slot]);
+    }
+    return true;
+  };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
@@ -119,8 +138,9 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       if (lane == 0) {
         int stage = 0;
         uint32_t phase = 0;
-        for (long long t = t0; t < tiles; t += tstep) {
-          const LinearTile q = tile_at<kInt8PairRows, TN>(p, prefix, t);
+        for (long long j = 0; j < mine; ++j) {
+          LinearTile q;
+          if (!next_tile(j, q, false)) goto teardown;
           for (int kb = 0; kb < p.num_kb; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) goto teardown;
             mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes);
@@ -132,6 +152,15 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
             }
           }
         }
+      }
+    } else if (warp == 2) {
+      for (long long j = 0; j < mine; j += kTileBatch) {
+        const int slot = static_cast<int>(j / kTileBatch) & 1;
+        if (!mbar_wait(&tqempty[slot], (static_cast<uint32_t>(j / (2 * kTileBatch)) & 1) ^ 1, abort_flag, p.status)) goto teardown;
+        if (lane < kTileBatch && j + lane < mine)
+          tileq[slot * kTileBatch + lane] = tile_at<kInt8PairRows, TN>(p, prefix, t0 + (j + lane) * tstep);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tqfull[slot]);
       }
     } else if (warp == 1 && rank == 0) {
       // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
@@ -190,7 +219,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     uint32_t phase = 0, uphase = 0;
     bool here = false;
 #pragma unroll 1
-    for (long long k = 0; k < blocks; ++k) {
+    for (int k = 0; k < blocks; ++k) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       uint4 v[4];
 #pragma unroll
@@ -237,8 +266,8 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     int stage = 0, unit = h;
     uint32_t phase = 0, uphase = 0;
     bool here = false;
-#pragma unroll 1
-    for (long long k = 0; k < blocks; ++k) {
+#pragma unroll 2   // (593 -> 580 us for 8192^3; x's loop too, or either more often: slower, by the instruction caches)
+    for (int k = 0; k < blocks; ++k) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       uint4 v[kPer];
 #pragma unroll
@@ -276,9 +305,10 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     uint8_t* out = sOut + (warp - 20) * Cfg::kOutBytes;
     float* table = sTable + (warp - 20) * (Cfg::kTableBytes / 4);   // scales, then biases
     int buf = 0;
-    uint32_t tphase = 0, turn = 0;
-    for (long long t = t0; t < tiles; t += tstep) {
-      const LinearTile q = tile_at<kInt8PairRows, TN>(p, prefix, t);
+    uint32_t tphase = 0;
+    for (long long j = 0; j < mine; ++j) {
+      LinearTile q;
+      if (!next_tile(j, q, true)) goto teardown;
       const int n0 = q.n0 + half * kCols;   // this warp's first column
       const long long row0 = q.row0 + mrow;
       const float xs = p.x_scale[(q.row0 + min(mrow + lane, q.rows - 1)) * p.xs_row];
@@ -305,63 +335,84 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         if (buf == 0) tphase ^= 1;
       }
       if (mrow < q.rows && n0 < p.N) {
-        // 64 bytes of each row at a time through shared memory (16-byte units swizzled by row): whole warps' rows leave
-        // by TMA, others by the elements, lanes side by side.  (A TMA store clips the columns past N by units of 16
-        // bytes and would write over what follows rows that end inside one.)
+        // Three chunks of 64 bytes of each row at a time (all bf16 columns, half of the fp32 ones) through shared memory,
+        // 16-byte units swizzled by row: whole warps' rows leave by TMA, a group's last rows by such units, unaligned or
+        // ragged ones by the elements, lanes side by side.  (A TMA store clips the columns past N by units of 16 bytes
+        // and would write over what follows rows that end inside one.)
         auto send = [&](auto bf16) {
           constexpr bool BF16 = decltype(bf16)::value;
-          constexpr int kEach = BF16 ? 32 : 16;   // columns
+          constexpr int kEach = BF16 ? 32 : 16;   // columns of a chunk
+          const bool whole = p.vec_y && mrow + 32 <= q.rows;
 #pragma unroll
-          for (int c = 0; c < kCols; c += kEach) {
-            uint8_t* chunk = out + (turn & 1) * 2048;
-            ++turn;
-            const int n = n0 + c;
-            if (lane == 0) bulk_wait_read<1>();   // the store from this place
+          for (int c0 = 0; c0 < kCols; c0 += 3 * kEach) {
+            if (lane < 3) bulk_wait_read<0>();   // the stores from these places
             __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              constexpr int kOf = BF16 ? 8 : 4;
+            for (int i = 0; i < 12; ++i) {   // unit i % 4 of chunk i / 4
+              constexpr int kOf = kEach / 4;
               float v[kOf];
 #pragma unroll
-              for (int i = 0; i < kOf; i += 4) {
-                const int at = c + u * kOf + i;
-                const float4 s = *reinterpret_cast<const float4*>(table + at), b = *reinterpret_cast<const float4*>(table + kCols + at);
-                v[i] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at]), __fmul_rn(xs, s.x)), b.x);
-                v[i + 1] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 1]), __fmul_rn(xs, s.y)), b.y);
-                v[i + 2] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 2]), __fmul_rn(xs, s.z)), b.z);
-                v[i + 3] = __fadd_rn(__fmul_rn(__int2float_rn(acc[at + 3]), __fmul_rn(xs, s.w)), b.w);
+              for (int k = 0; k < kOf; k += 4) {
+                const int at = c0 + i * kOf + k;
+                const float4 s = *reinterpret_cast<const float4*>(table + at);
+                v[k] = __fmul_rn(__int2float_rn(acc[at]), __fmul_rn(xs, s.x));
+                v[k + 1] = __fmul_rn(__int2float_rn(acc[at + 1]), __fmul_rn(xs, s.y));
+                v[k + 2] = __fmul_rn(__int2float_rn(acc[at + 2]), __fmul_rn(xs, s.z));
+                v[k + 3] = __fmul_rn(__int2float_rn(acc[at + 3]), __fmul_rn(xs, s.w));
+                if (p.bias) {
+                  const float4 b = *reinterpret_cast<const float4*>(table + kCols + at);
+                  v[k] = __fadd_rn(v[k], b.x);
+                  v[k + 1] = __fadd_rn(v[k + 1], b.y);
+                  v[k + 2] = __fadd_rn(v[k + 2], b.z);
+                  v[k + 3] = __fadd_rn(v[k + 3], b.w);
+                }
               }
               if (p.clamp) {
 #pragma unroll
-                for (int i = 0; i < kOf; ++i) v[i] = act_clamp(v[i], p.lo, p.hi);
+                for (int k = 0; k < kOf; ++k) v[k] = act_clamp(v[k], p.lo, p.hi);
               }
               uint4 w;
               if constexpr (BF16)
                 w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
               else
                 w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-              *reinterpret_cast<uint4*>(chunk + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = w;
+              *reinterpret_cast<uint4*>(out + (i >> 2) * 2048 + lane * 64 + (((i & 3) ^ ((lane >> 1) & 3)) << 4)) = w;
             }
-            if (p.vec_y && mrow + 32 <= q.rows && (p.whole_units || n + kEach <= p.N)) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && n < p.N) tma_store_2d(&tmY, chunk, n, static_cast<int>(row0));
-            } else {
-              __syncwarp();
-              constexpr int kRows = 32 / kEach;   // rows at a time
-              const int col = lane % kEach, rows = min(32, q.rows - mrow);
-              for (int r = lane / kEach; r < rows; r += kRows) {
-                if (n + col < p.N && CONVF_IN_BOUNDS(row0 + r < p.rows, p.status)) {
-                  const long long at = (row0 + r) * p.ldy + n + col;
-                  const uint8_t* from = chunk + r * 64 + (((col * 64 / kEach >> 4) ^ ((r >> 1) & 3)) << 4) + col * (64 / kEach) % 16;
-                  if constexpr (BF16)
-                    static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(from);
-                  else
-                    static_cast<uint32_t*>(p.y)[at] = *reinterpret_cast<const uint32_t*>(from);
+            if (whole) fence_proxy_async_smem();
+            __syncwarp();
+            if (whole && lane < 3) {   // a chunk each
+              const int n = n0 + c0 + lane * kEach;
+              if (n < p.N && (p.whole_units || n + kEach <= p.N)) tma_store_2d(&tmY, out + lane * 2048, n, static_cast<int>(row0));
+              bulk_commit();
+            }
+#pragma unroll 1
+            for (int i = 0; i < 3; ++i) {
+              const int n = n0 + c0 + i * kEach;
+              const bool units = p.vec_y && (p.whole_units || n + kEach <= p.N);   // the rows' 16-byte units are whole
+              if ((whole && units) || n >= p.N) continue;
+              const uint8_t* chunk = out + i * 2048;
+              const int rows = min(32, q.rows - mrow);
+              if (units) {
+                const int u = lane & 3;
+                for (int r = lane >> 2; r < rows; r += 8)
+                  if (n + u * (kEach / 4) < p.N && CONVF_IN_BOUNDS(row0 + r < p.rows, p.status))
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + ((row0 + r) * p.ldy + n) * (64 / kEach) + u * 16) =
+                        *reinterpret_cast<const uint4*>(chunk + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+              } else {
+                constexpr int kRows = 32 / kEach;   // rows at a time
+                const int col = lane % kEach;
+                for (int r = lane / kEach; r < rows; r += kRows) {
+                  if (n + col < p.N && CONVF_IN_BOUNDS(row0 + r < p.rows, p.status)) {
+                    const long long at = (row0 + r) * p.ldy + n + col;
+                    const uint8_t* from = chunk + r * 64 + (((col * 64 / kEach >> 4) ^ ((r >> 1) & 3)) << 4) + col * (64 / kEach) % 16;
+                    if constexpr (BF16)
+                      static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(from);
+                    else
+                      static_cast<uint32_t*>(p.y)[at] = *reinterpret_cast<const uint32_t*>(from);
+                  }
                 }
               }
             }
-            if (lane == 0) bulk_commit();   // (a group each, stored by TMA or not: places are taken in turn)
           }
         };
         if (p.out_bf16)
@@ -371,7 +422,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       }
       __syncwarp();   // the table has been read
     }
-    if (lane == 0) bulk_wait_all();   // the stores have been written before the CTA ends
+    if (lane < 3) bulk_wait_all();   // the stores have been written before the CTA ends
   }
 
 teardown:

@@ -85,12 +85,15 @@ struct RowsParams {
   long long ldh;
   const void* weight;        // [cols] or null
   int weight_bf16;
-  float eps;
+  float eps, inv_cols;       // inv_cols: 1 / cols
   uint8_t* q;
   long long ldq;
   float* scale;              // [rows]; e4m3: [rows][lds]
   long long lds;
   int x_align, r_align, w_align, q_align;   // as QuantParams' (r_align: the residual's and h's, 32 without them)
+  const uint8_t *x_end, *r_end;             // behind the last bytes of x and the residual
+  const uint8_t *x_spare, *r_spare;         // 80 bytes of each from a multiple of 32 on; small: one of them has no such
+  int small;
 };
 template <int KIND>
 cudaError_t launch_rows(const RowsParams& p, bool bf16, int num_sms, cudaStream_t stream);

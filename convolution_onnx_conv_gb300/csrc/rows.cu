@@ -36,6 +36,16 @@ convf_status launch(const RowsParams& p, int x_dtype, void* stream) {
   return record_ok();
 }
 
+// behind the last of `rows` rows of `row` bytes, `stride` bytes apart
+const uint8_t* end_of(const void* p, long long rows, long long row, long long stride) {
+  return p && rows > 0 ? static_cast<const uint8_t*>(p) + (rows - 1) * stride + row : static_cast<const uint8_t*>(p);
+}
+// 80 bytes that a thread without columns may read, or null
+const uint8_t* spare_of(const void* p, const uint8_t* end) {
+  const uint8_t* from = reinterpret_cast<const uint8_t*>((reinterpret_cast<uintptr_t>(p) + 31) & ~static_cast<uintptr_t>(31));
+  return end - static_cast<const uint8_t*>(p) >= 31 + 80 ? from : nullptr;
+}
+
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 }  // namespace
@@ -75,6 +85,9 @@ convf_status conv_fused_quantize_rows(const convf_quant_rows_args* a, void* stre
   p.x_align = common_alignment(bits(a->x) | a->ldx * esz | (a->gated ? static_cast<long long>(a->cols) * esz : 0));
   p.q_align = common_alignment(bits(a->q) | a->ldq);
   p.r_align = p.w_align = 32;
+  p.x_end = end_of(a->x, a->x_rows, wide * esz, a->ldx * esz);
+  p.x_spare = spare_of(a->x, p.x_end);
+  p.small = !p.x_spare;
   return a->gated ? launch<kRowsGated>(p, a->x_dtype, stream) : launch<kRowsPlain>(p, a->x_dtype, stream);
 }
 
@@ -130,10 +143,16 @@ convf_status conv_fused_rms_norm_quantize(const convf_norm_args* a, void* stream
   p.residual = a->residual; p.ldr = a->ldr; p.residual_bf16 = a->residual_dtype == CONVF_OUT_BF16;
   p.h = a->h; p.ldh = a->ldh;
   p.weight = a->weight; p.weight_bf16 = a->weight && a->weight_dtype == CONVF_OUT_BF16; p.eps = a->eps;
+  p.inv_cols = 1.f / static_cast<float>(a->cols);
   p.q = static_cast<uint8_t*>(a->q); p.ldq = a->ldq; p.scale = a->scale; p.lds = a->lds;
   p.x_align = common_alignment(bits(a->x) | a->ldx * xsz);
   p.r_align = common_alignment((a->residual ? bits(a->residual) | a->ldr * rsz : 0) | (a->h ? bits(a->h) | a->ldh * rsz : 0));
   p.w_align = common_alignment(bits(a->weight));
+  p.x_end = end_of(a->x, a->rows, cols * xsz, a->ldx * xsz);
+  p.r_end = end_of(a->residual, a->rows, cols * rsz, a->ldr * rsz);
+  p.x_spare = spare_of(a->x, p.x_end);
+  p.r_spare = spare_of(a->residual, p.r_end);
+  p.small = !p.x_spare || (a->residual && !p.r_spare);
   p.q_align = common_alignment(bits(a->q) | a->ldq);
   return int8 ? launch<kRowsNormInt8>(p, a->x_dtype, stream) : launch<kRowsNormE4m3>(p, a->x_dtype, stream);
 }

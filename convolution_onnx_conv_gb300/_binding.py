@@ -904,8 +904,11 @@ def rms_norm_quantize(x, weight=None, eps=1e-6, residual=None, int8=False, q=Non
     on = x.get_device()
     if on != T.current_device():
         raise ValueError(f"x is on device {on}, the current device is {T.current_device()}")
-    T.refuse_apart(on, weight=weight, residual=residual, q=q, scale=scale, h=h)
-    device = x.device
+    if (weight is not None and weight.get_device() != on) or (residual is not None and residual.get_device() != on) \
+            or (q is not None and q.get_device() != on) or (scale is not None and scale.get_device() != on) \
+            or (h is not None and h.get_device() != on):
+        T.refuse_apart(on, weight=weight, residual=residual, q=q, scale=scale, h=h)
+    device, kind = x.device, _kind(x, "x")
     wp = wk = rp = rk = hp = ldr = ldh = 0
     if weight is not None:
         if not weight.is_cuda or weight.shape != (cols,) or not weight.is_contiguous():
@@ -918,6 +921,8 @@ def rms_norm_quantize(x, weight=None, eps=1e-6, residual=None, int8=False, q=Non
         rp, rk = residual.data_ptr(), _kind(residual, "residual")
         if h is None:
             h, ldh = T.empty((rows, cols), dtype=residual.dtype, device=device), cols
+        elif h is residual:
+            ldh = ldr
         else:
             hr, hc, ldh = _rows_2d(h, "h")
             if h.dtype is not residual.dtype or hr != rows or hc != cols:
@@ -925,10 +930,11 @@ def rms_norm_quantize(x, weight=None, eps=1e-6, residual=None, int8=False, q=Non
         hp = h.data_ptr()
     elif h is not None:
         raise ValueError("h goes with a residual (without one it is x)")
-    q, ldq = _bytes_like(q, rows, cols, T.i8 if int8 else T.e4m3, device)
     if int8:
+        q, ldq = _bytes_like(q, rows, cols, T.i8, device)
         scale, lds = _row_scales(scale, rows, device), 1
     else:
+        q, ldq = _bytes_like(q, rows, cols, T.e4m3, device)
         lds = nblk = (cols + 127) // 128
         if scale is None:
             scale = T.empty((rows, nblk), dtype=T.f32, device=device)
@@ -940,7 +946,7 @@ def rms_norm_quantize(x, weight=None, eps=1e-6, residual=None, int8=False, q=Non
         stream = T.stream(on)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    st = T.norm(ctypes.byref(NormArgs(rows, cols, x.data_ptr(), _kind(x, "x"), ldx, rp, rk, ldr, hp, ldh, wp, wk, eps,
+    st = T.norm(ctypes.byref(NormArgs(rows, cols, x.data_ptr(), kind, ldx, rp, rk, ldr, hp, ldh, wp, wk, eps,
                                       CONVF_LINEAR_INT8 if int8 else CONVF_LINEAR_E4M3, q.data_ptr(), ldq,
                                       scale.data_ptr(), lds)), stream)
     if st != CONVF_OK:

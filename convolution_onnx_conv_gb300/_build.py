@@ -29,7 +29,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxe
 
 UNITS = [("api.cu", []), ("k_depthwise.cu", []), ("k_int8.cu", []), ("k_watchdog.cu", []), ("k_pad.cu", []),
          ("tc_window.cu", []), ("tc_halo.cu", []), ("k_mbblock.cu", []), ("chain.cu", []),
-         ("tc_chain.cu", []), ("linear.cu", []), ("k_quant.cu", []), ("tc_linear_few.cu", []), ("tc_linear_many.cu", []), ("rows.cu", []), ("tc_linear_int8_few.cu", []), ("tc_linear_int8_many.cu", [])] + [
+         ("tc_chain.cu", []), ("linear.cu", []), ("k_quant.cu", []), ("tc_linear_few.cu", []), ("tc_linear_many.cu", []), ("rows.cu", []), ("tc_linear_int8_few.cu", []), ("linear_int8_direct.cu", []), ("tc_linear_int8_many.cu", [])] + [
     ("k_rows.cu", [f"-DCONVF_ROWS_KIND={k}"]) for k in range(4)] + [
     ("tc_conv_inst.cu", [f"-DCONVF_BN={bn}"]) for bn in (32, 64, 128, 256)]
 

@@ -294,18 +294,20 @@ __device__ __forceinline__ void put_16(R* at, int n, const float (&f)[16]) {
     for (int k = 0; k < kWords / 4; ++k) unit(k);
     return;
   }
+  if constexpr (ALIGN != 32) {
 #pragma unroll
-  for (int k = 0; k < kWords / 4; ++k) {
-    const int e0 = kEach * k - before;   // the unit's first element, counted from this lane's first
-    if ((e0 >= 0 || lane > 0) && e0 + kEach <= n) {
-      unit(k);
-    } else {
+    for (int k = 0; k < kWords / 4; ++k) {
+      const int e0 = kEach * k - before;   // the unit's first element, counted from this lane's first
+      if ((e0 >= 0 || lane > 0) && e0 + kEach <= n) {
+        unit(k);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if ((e0 + i >= 0 || lane > 0) && e0 + i < n) {
-          const uint32_t word = w[4 * k + i * static_cast<int>(sizeof(R)) / 4];
-          reinterpret_cast<Bits*>(at)[e0 + i] = static_cast<Bits>(sizeof(R) == 2 && (i & 1) ? word >> 16 : word);
-        }
+        for (int i = 0; i < kEach; ++i)
+          if ((e0 + i >= 0 || lane > 0) && e0 + i < n) {
+            const uint32_t word = w[4 * k + i * static_cast<int>(sizeof(R)) / 4];
+            reinterpret_cast<Bits*>(at)[e0 + i] = static_cast<Bits>(sizeof(R) == 2 && (i & 1) ? word >> 16 : word);
+          }
+      }
     }
   }
 }
@@ -388,6 +390,7 @@ __global__ void __launch_bounds__(SHARE == kWarpRow ? 128 : SHARE == kWideRow ? 
     v.row = there ? src : 0;
     v.n = WHOLE ? 16 : there ? p.cols - c : 0;
     if (!WHOLE && p.small) {
+      v.x.first = v.second.first = 0;
       v.whole = v.n <= 0;
       return;
     }

@@ -98,8 +98,21 @@ int few_clusters(int dev, int num_sms, int dtype, int tile, int split) {
   return n;
 }
 
+// CTAs of a direct int8 kernel that run at once (as few_clusters)
+int direct_ctas(int dev, int num_sms, int tile) {
+  static int known[kMaxDevices][2];
+  int* at = dev >= 0 && dev < kMaxDevices ? &known[dev][tile == kInt8MmaRows] : nullptr;
+  if (at && *at) return *at;
+  const int n = linear_int8_direct_ctas(tile, num_sms);
+  if (at) *at = n;
+  return n;
+}
+
 // weight rows of a plan's tile
-int tile_columns(const LinearPlan& plan) { return plan.tile < 128 ? 128 : plan.form == kLinearInt8 ? kInt8PairCols : kManyCols; }
+int tile_columns(const LinearPlan& plan, int K) {
+  if (plan.form == kLinearInt8Direct) return plan.tile == kInt8DotRows ? int8_dot_cols(K) : kInt8MmaCols;
+  return plan.tile < 128 ? 128 : plan.form == kLinearInt8 ? kInt8PairCols : kManyCols;
+}
 
 // What a run of `rows` rows launches: the form with the least estimated time.  How the rows fall on
 // the experts is known on the device only, so the estimate goes by their mean, with half a tile per
@@ -123,9 +136,7 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   LinearPlan plan{};
   long long best = -1;
   const long long bytes = taken * d.N * d.K * esz + static_cast<long long>(rows) * (d.K * esz + d.N * 2LL);
-  auto offer = [&](int form, int tile, int split, long long units, long long n_tiles, long long per_kb, long long ends) {
-    const long long waves = ceil_div(row_tiles(tile) * n_tiles, units);
-    const long long model = 3500 + waves * (ceil_div(num_kb, split) * per_kb + ends), memory = 3500 + bytes / 6300;
+  auto take = [&](int form, int tile, int split, long long units, long long n_tiles, long long model, long long memory) {
     const long long ns = (model > memory ? model : memory) + model / 8;
     if (best >= 0 && ns >= best) return;
     best = ns;
@@ -133,12 +144,35 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
     const int ctas = (form == kLinearMany && tile == 256) || (form == kLinearInt8 && tile == kInt8PairRows) ? 2 : split;
     plan = LinearPlan{form, tile, split, ctas * static_cast<int>(most < units ? most : units)};
   };
+  auto offer = [&](int form, int tile, int split, long long units, long long n_tiles, long long per_kb, long long ends) {
+    const long long waves = ceil_div(row_tiles(tile) * n_tiles, units);
+    take(form, tile, split, units, n_tiles, 3500 + waves * (ceil_div(num_kb, split) * per_kb + ends), 3500 + bytes / 6300);
+  };
   const long long nt = ceil_div(d.N, 128), nt_many = ceil_div(d.N, kManyCols);
   if (int8) {
-    // fitted to runs of every form at 1 to 8192 rows, 1 to 64 experts and N, K from 512 to 8192; over those 150 sizes
-    // the choice takes 0.4% more than the best form on the average and 9% at most (64 rows of 4096 x 4096: 64 columns,
-    // split 4 15.6 us, unsplit 18.8, 16 columns 23.1, pairs 21.3; 1024 rows over 8 experts of 2048 x 2048: pairs 24.3,
-    // 64 columns 27.6, 16 columns 48.0; over 32 experts 58.4, 38.7 and 54.5)
+    // Fitted to runs of every form at 1 to 8192 rows, 1 to 64 experts and N, K from 300 to 16384.  The tensor cores'
+    // forms, over 150 sizes: 0.4% more than the best of them on the average and 9% at most (64 rows of 4096 x 4096: 64
+    // columns, split 4 15.6 us, unsplit 18.8, 16 columns 23.1, pairs 21.3; 1024 rows over 8 experts of 2048 x 2048: pairs
+    // 24.3, 64 columns 27.6, 16 columns 48.0; over 32 experts 58.4, 38.7 and 54.5).  With the direct forms, over 230 sizes
+    // of few rows, 1.3% and 32% (a row count says nothing of how it falls on the experts): 4096 x 4096, 1 row: by dot
+    // products 2.8 us, direct MMAs 5.2, 16 columns 10.3; 4 rows 3.8, 5.2, 11.6; 8 rows 7, 5.3, 11.7; 32 rows 19, 14.4,
+    // 18.6, 64 columns 14.9; 64 rows 35, 22.5, 22.3, 15.7; 64 rows over 64 experts of 2048 x 2048 26.1, 33.3, 28.5.
+    const long long dot_cols = int8_dot_cols(d.K), dot = direct_ctas(dev, num_sms, kInt8DotRows), mma = direct_ctas(dev, num_sms, kInt8MmaRows);
+    const long long mean = ceil_div(rows, taken);   // rows of an expert
+    const long long kilos = d.N * static_cast<long long>(d.K) / 1000;
+    if (dot > 0 && mean <= 64) {
+      const long long tiles = row_tiles(kInt8DotRows) * ceil_div(d.N, dot_cols), warps = dot * kInt8DotWarps;
+      const long long loads = ceil_div(tiles, warps) * (ceil_div(d.K * dot_cols, 4096) * 800 + 800);
+      const long long products = row_tiles(kInt8DotRows) * kilos * (mean > 2 ? 4 : mean) * 15 / 1000;
+      take(kLinearInt8Direct, kInt8DotRows, 1, warps, ceil_div(d.N, dot_cols), 1300 + (loads > products ? loads : products), 1300 + bytes / 6800);
+      plan.grid = static_cast<int>(ceil_div(plan.grid, kInt8DotWarps));
+    }
+    if (mma > 0 && mean <= 64) {
+      const long long tiles = row_tiles(kInt8MmaRows) * ceil_div(d.N, kInt8MmaCols), groups = mean > 8 ? 2 : 1;
+      const long long loads = ceil_div(tiles, mma) * (ceil_div(d.K, 2048) * 1030 * groups + 600);
+      const long long products = row_tiles(kInt8MmaRows) * kilos * groups * 150 / 1000;
+      take(kLinearInt8Direct, kInt8MmaRows, 1, mma, ceil_div(d.N, kInt8MmaCols), 2500 + (loads > products ? loads : products), 2500 + bytes / 6300);
+    }
     for (int tile = 16; tile <= (rows > 16 ? 64 : 16); tile *= 4) {
       for (int split = 1; split <= 8 && split <= num_kb; split *= 2) {
         const int units = few_clusters(dev, num_sms, d.dtype, tile, split);
@@ -357,17 +391,18 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
   if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
     return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
   const LinearPlan plan = make_plan(d, l->device, l->num_sms, a->rows);
-  CUtensorMap tmX;
+  CUtensorMap tmX{};
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.K), static_cast<cuuint64_t>(a->rows)};
   const cuuint64_t stride = a->ldx * esz;
   const int x_box = plan.tile < 128 ? plan.tile : 128;
-  st = encode_map(&tmX, scaled ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
-                  a->x, size, &stride, x_box, "x");
+  if (plan.form != kLinearInt8Direct)   // (which reads its operands as they are)
+    st = encode_map(&tmX, scaled ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<int>(esz), 2,
+                    a->x, size, &stride, x_box, "x");
   if (st != CONVF_OK) return st;
   LinearParams p{};
   p.rows = a->rows; p.N = d.N; p.experts = d.experts;
   p.num_kb = static_cast<int>(ceil_div(d.K * esz, kKBlockBytes));
-  p.n_tiles = static_cast<int>(ceil_div(d.N, tile_columns(plan)));
+  p.n_tiles = static_cast<int>(ceil_div(d.N, tile_columns(plan, d.K)));
   // bf16 operands: the MMA's own accumulator truncates, so its sums go to registers every 256 values where
   // the result is fp32 (1.2e-6 of the result at K = 1000 without it, 3e-7 with it), and every 4096 values
   // where it is bf16: terms of one sign then lose 1e-5 of their sum at most, whatever K is (without it 8e-4
@@ -388,7 +423,9 @@ convf_status conv_fused_linear_run(convf_linear* l, const convf_linear_args* a, 
     if (st != CONVF_OK) return st;
   }
   const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = plan.form == kLinearInt8 ? (plan.tile == kInt8PairRows ? launch_linear_int8_many(p, plan, l->tmW64, tmX, tmY, strm)
+  const Int8Operands int8_operands{static_cast<const int8_t*>(l->w), static_cast<const int8_t*>(a->x), d.ldw, d.expert_stride, a->ldx, d.K};
+  const cudaError_t e = plan.form == kLinearInt8Direct ? launch_linear_int8_direct(p, plan, int8_operands, strm)
+                        : plan.form == kLinearInt8 ? (plan.tile == kInt8PairRows ? launch_linear_int8_many(p, plan, l->tmW64, tmX, tmY, strm)
                                                                                : launch_linear_int8_few(p, plan, l->tmW128, tmX, strm))
                         : plan.form == kLinearFew
                             ? launch_linear_few(p, plan, e4m3, l->tmW128, tmX, strm)
@@ -434,8 +471,8 @@ convf_status conv_fused_linear_describe(const convf_linear* l, int rows, char* b
     if (cudaGetDevice(&dev) != cudaSuccess || dev != l->device)
       return record_error(CONVF_ERR_INVALID_ARG, "the current device (%d) is not the layer's device (%d)", dev, l->device);
     const LinearPlan plan = make_plan(l->d, l->device, l->num_sms, rows);
-    snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.tile < 128 ? "few_rows" : "many_rows",
-             plan.tile, tile_columns(plan), plan.split, plan.grid);
+    snprintf(buf + n, len - n, " form=%s tile=%dx%d split=%d grid=%d", plan.form == kLinearInt8Direct ? "direct" : plan.tile < 128 ? "few_rows" : "many_rows",
+             plan.tile, tile_columns(plan, l->d.K), plan.split, plan.grid);
   }
   return record_ok();
 }

@@ -58,6 +58,11 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t p
       : "memory");
   return ok != 0;
 }
+// Arrive on the pair's leader's mbarrier: this CTA's operands of an MMA are in place.  What it tells of is read by the
+// tensor cores and TMA's side only, not by the other CTA's threads, and each writer has made its writes visible to
+// those before: shared memory by fence.proxy.async, TMEM by tcgen05.wait::st and the fence before.  So the release orders
+// those within the CTA and no more.  (At cluster scope it also waits for every store in flight to be seen by the other
+// CTA: 1380 cycles, of about 400 that a unit has.)
 __device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

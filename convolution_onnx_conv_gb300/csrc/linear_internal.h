@@ -123,11 +123,11 @@ struct LinearParams {
 };
 
 // What a run launches (linear_plan): the form, its row tile, and how many CTAs share a tile's k.
-enum LinearForm : int { kLinearFew = 0, kLinearMany = 1, kLinearInt8 = 2 };
+enum LinearForm : int { kLinearFew = 0, kLinearMany = 1, kLinearInt8 = 2, kLinearInt8Direct = 3 };
 struct LinearPlan {
   int form;
   int tile;     // rows of x per tile: kLinearFew 16, 32 or 64; kLinearMany 128, or 256 on CTA pairs;
-                // kLinearInt8 16 or 64, or kInt8PairRows on CTA pairs
+                // kLinearInt8 16 or 64, or kInt8PairRows on CTA pairs; kLinearInt8Direct kInt8DotRows or kInt8MmaRows
   int split;    // kLinearFew, kLinearInt8: CTAs of a cluster that share a tile's reduction (1, 2, 4 or 8)
   int grid;     // CTAs
 };
@@ -154,6 +154,18 @@ cudaError_t launch_linear_int8_few(const LinearParams& p, const LinearPlan& plan
 cudaError_t launch_linear_int8_many(const LinearParams& p, const LinearPlan& plan, const CUtensorMap& tmW, const CUtensorMap& tmX,
                                     const CUtensorMap& tmY, cudaStream_t stream);
 int linear_int8_max_clusters(int tile, int split, int num_sms);
+// A handful of rows, from the operands as they are: no tensor maps.
+constexpr int kInt8DotRows = 4, kInt8DotWarps = 4;   // of x, of a warp's tile; warps of a CTA
+// weight rows of a warp's tile: as many as fill a lane's loads
+constexpr int int8_dot_cols(int K) { return K <= 512 ? 8 : K <= 1024 ? 4 : 2; }
+constexpr int kInt8MmaRows = 16, kInt8MmaCols = 16;   // of a CTA's tile
+struct Int8Operands {
+  const int8_t *w, *x;
+  long long ldw, w_stride, ldx;   // w_stride: between experts
+  int K;
+};
+cudaError_t launch_linear_int8_direct(const LinearParams& p, const LinearPlan& plan, const Int8Operands& o, cudaStream_t stream);
+int linear_int8_direct_ctas(int tile, int num_sms);   // that run at once on the current device (0 on an error)
 
 constexpr int kManyCols = 256;   // weight rows of a kLinearMany tile
 

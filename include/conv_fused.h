@@ -519,7 +519,7 @@ typedef struct {
 } convf_quant_rows_args;
 
 /* Quantises on `stream` (asynchronous, no allocation, one launch).  Any alignment and any row stride of
- * at least a row is served; rows that begin on 8 bytes are read and written as vectors.  q and scale
+ * at least a row is served (rows of q that begin on 16 bytes are written fastest).  q and scale
  * must not overlap x, index or each other (rows at the same distance may lie between each other's). */
 convf_status conv_fused_quantize_rows(const convf_quant_rows_args* a, void* stream);
 

@@ -71,14 +71,15 @@ def test_every_form():
         for n, k in ((64, 16384), (128, 4000), (640, 3000), (1024, 2049), (4096, 512), (8192, 130), (20000, 128)):
             x, w, xs, ws = operands(rows + n, rows, 1, n, k)
             lin = cf.Int8Linear(rows16(w)[0], ws[0])
-            form = re.search(r"tile=(\d+)x\d+ split=(\d+)", lin.describe(rows)).groups()
+            form = re.search(r"form=(\w+) tile=(\d+)x\d+ split=(\d+)", lin.describe(rows)).groups()
             if seen.get(form, 0) < 3:
                 seen[form] = seen.get(form, 0) + 1
                 y = lin(rows16(x), xs)
                 done(lin)
                 assert torch.equal(y, expected(x, w[0], xs, ws[0])), lin.describe(rows)
             lin.close()
-    assert {t for t, _ in seen} == {"16", "64", "256"} and {s for _, s in seen} == {"1", "2", "4", "8"}, sorted(seen)
+    assert {(f, t) for f, t, _ in seen} == {("direct", "4"), ("direct", "16"), ("few_rows", "16"), ("few_rows", "64"), ("many_rows", "256")}, sorted(seen)
+    assert {s for _, _, s in seen} >= {"1", "2", "4"}, sorted(seen)
 
 
 @pytest.mark.parametrize("rows", [1, 40, 260])
@@ -208,6 +209,46 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(y, want[r]) for y, r in zip(outs, want))
     done(lin)
+
+
+def test_every_form_at_once():
+    """Layers of every form on streams of their own, side by side, many times: none takes what another waits for."""
+    cases = []
+    for seed, (rows, n, k) in enumerate([(1, 2048, 2048), (12, 1040, 4096), (60, 4096, 300), (128, 2048, 2048), (900, 1000, 1100)]):
+        x, w, xs, ws = operands(20 + seed, rows, 1, n, k)
+        lin = cf.Int8Linear(rows16(w)[0], ws[0], out_bf16=True)
+        cases.append((lin, rows16(x), xs, expected(x, w[0], xs, ws[0], out=BF16), torch.cuda.Stream()))
+    counts = [0, 1, 7, 2, 30, 3, 1, 0]
+    x, w, xs, ws = operands(30, sum(counts), len(counts), 520, 1500)
+    off = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    experts = cf.ExpertLinear(rows16(w), ws, out_bf16=True)
+    want = torch.cat([expected(x[a:b], w[e], xs[a:b], ws[e], out=BF16) for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))])
+    x16, side = rows16(x), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [[lin(a, s, stream=st) for _ in range(4)] for lin, a, s, _, st in cases]
+        ragged = [experts(x16, off, xs, stream=side) for _ in range(4)]
+        torch.cuda.synchronize()
+        for (lin, _, _, y, _), got in zip(cases, outs):
+            assert all(torch.equal(g, y) for g in got) and lin.status() == cf.CONVF_OK
+        assert all(torch.equal(g, want) for g in ragged) and experts.status() == cf.CONVF_OK
+
+
+@pytest.mark.parametrize("k", [500, 1000, 2048, 2055])
+def test_groups_of_a_few_rows(k):
+    """Groups of no rows to nine, some of them one behind another empty, of a warp's tiles over the groups' borders."""
+    counts = [0, 0, 1, 2, 0, 3, 4, 5, 0, 0, 0, 6, 8, 9, 1, 0, 1, 0, 0]
+    n = 37
+    x, w, xs, ws = operands(k, sum(counts) + 3, len(counts), n, k)
+    off = torch.tensor([1] + counts, device="cuda").cumsum(0).to(torch.int32)
+    lin = cf.ExpertLinear(rows16(w), ws)
+    y = torch.full((x.shape[0], n), -7.0, device="cuda")
+    lin(rows16(x), off, xs, y=y)
+    done(lin)
+    want = torch.full_like(y, -7.0)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        want[a:b] = expected(x[a:b], w[e], xs[a:b], ws[e])
+    assert torch.equal(y, want), lin.describe(x.shape[0])
 
 
 def test_offsets_past_32_bits():

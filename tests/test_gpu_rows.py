@@ -200,6 +200,29 @@ def test_norm_in_place(cols, res, int8):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("cols", [512, 4096])
+def test_norm_in_place_in_whole_rows(cols, res, int8):
+    """As above, in rows that a kernel without checks takes, each CTA with several of them and the last asked for twice."""
+    for rows in (1, 2900):
+        x, r = randn(23, rows, cols, dtype=res), randn(24, rows, cols, dtype=res)
+        w = randn(25, cols)
+        a = r.clone()
+        check_norm(x, w, 1e-6, r, int8, cf.rms_norm_quantize(x, w, residual=a, int8=int8, h=a))
+        b = x.clone()
+        check_norm(x, w, 1e-6, r, int8, cf.rms_norm_quantize(b, w, residual=r, int8=int8, h=b))
+
+
+def test_one_row_gathered_many_times():
+    x = randn(26, 9, 1000, dtype=BF16)
+    index = torch.randint(0, 9, (700,), generator=gen(27), device="cuda", dtype=torch.int32)
+    index[100:400] = 5
+    q, s = cf.quantize_rows(x, index=index)
+    rq, rs = cf.quantize_rows(x)
+    assert torch.equal(q, rq[index.long()]) and torch.equal(s, rs[index.long()])
+
+
+@pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("offset,ld", [(0, 300), (1, 300), (8, 304), (3, 301), (4, 320)])
 @pytest.mark.parametrize("dtype,res", [(BF16, BF16), (BF16, F32), (F32, BF16)])
 def test_norm_any_alignment_and_stride(offset, ld, dtype, res, int8):

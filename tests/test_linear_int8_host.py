@@ -52,7 +52,7 @@ def test_create_refuses_operands(w, ws, bias, needle):
     assert e.value.status == BAD and needle in str(e.value)
 
 
-@pytest.mark.parametrize("name", ["linear_int8_dev.cuh", "tc_linear_int8_few.cu", "tc_linear_int8_many.cu"])
+@pytest.mark.parametrize("name", ["linear_int8_dev.cuh", "linear_int8_direct.cu", "tc_linear_int8_few.cu", "tc_linear_int8_many.cu"])
 def test_no_read_only_loads_of_what_the_kernel_before_may_write(name):
     text = source(name)
     assert not re.search(r"__ldg\b|\.nc\b|__ldcg|__ldca", text)

@@ -1,4 +1,4 @@
-// Host side of the block-scaled operators (conv_fused_quantize_blocks, conv_fused_linear_*):
+// Host side of conv_fused_quantize_blocks and the linear layers (conv_fused_linear_*: block-scaled, bf16, int8):
 // validates every argument (refuse, never guess) and launches on the caller's stream.  Weights
 // and scales are read where they are; nothing of a run is kept for the next.
 #include <cuda.h>

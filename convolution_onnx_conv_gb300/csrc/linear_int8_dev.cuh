@@ -1,7 +1,8 @@
 // Device-side parts shared by the int8 linear kernels: fp16 MMAs whose first operand is in TMEM, int8 -> fp16, and
 // the last step of an output element.
 //
-// sm_103a's tcgen05.mma has no integer kind, and its warp-level int8 MMA reaches a twelfth of the fp16 rate.  An
+// sm_103a's tcgen05.mma has no integer kind, and its warp-level int8 MMA (25 cycles of an SM for 16 x 8 x 32) reaches a
+// twenty-fifth of the fp16 rate: enough for a handful of rows only (linear_int8_direct.cu).  For more: an
 // int8 value is an fp16 number, the product of two is at most 2^14 and fp32 holds every integer up to 2^24: fp16
 // MMAs add kInt8Chunk products exactly, and the chunks' sums are added as int32 in registers.  So every sum is the
 // integer, whatever the order, and all forms give the same bits.

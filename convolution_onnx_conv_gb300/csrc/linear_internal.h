@@ -1,4 +1,4 @@
-// Interface between the host side of the block-scaled operators (linear.cu) and their kernels.
+// Interface between the host side of the linear layers and the 8-bit rows (linear.cu, rows.cu) and their kernels.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -2,6 +2,11 @@
 // linear_int8_dev.cuh).  16 or 64 rows of x are a tile's columns, and the CTAs of a cluster share a tile's
 // reduction where there are fewer tiles than SMs, as in tc_linear_few.cu; their partial sums are integers too.
 //
+// For tens of rows, and for experts with a few each (fewer: linear_int8_direct.cu).  Bound by what a k-block goes through
+// (its bytes' arrival, the conversion of 128 weight rows, the MMAs: 350 to 590 ns, of which the bytes take 100) and, where
+// the reduction is shared, by 3 to 7 us of start, exchange and end.  64 x 4096 x 4096: 15.3 us (tensor pipe 12%, logic pipe
+// 33%); 96 x 8192 x 2048 12.6; 1001 x 1000 x 2048 12.3; 128 rows over 24 experts of 2048 x 2048 24.1 (floor 14.9).
+//
 //   warp 0        TMA: weight and x tiles of 128 values
 //   warp 1        TMEM, MMA issue
 //   warps 2, 3    int8 -> fp16 of x (64 columns: warps 4-11)

@@ -152,8 +152,8 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
   if (int8) {
     // Fitted to runs of every form at 1 to 8192 rows, 1 to 64 experts and N, K from 300 to 16384.  The tensor cores'
     // forms, over 150 sizes: 0.4% more than the best of them on the average and 9% at most (64 rows of 4096 x 4096: 64
-    // columns, split 4 15.6 us, unsplit 18.8, 16 columns 23.1, pairs 21.3; 1024 rows over 8 experts of 2048 x 2048: pairs
-    // 24.3, 64 columns 27.6, 16 columns 48.0; over 32 experts 58.4, 38.7 and 54.5).  With the direct forms, over 230 sizes
+    // columns, split 4 15.0 us, unsplit 16.4, 16 columns 19.4, pairs 21.3; 1024 rows over 8 experts of 2048 x 2048: pairs
+    // 24.3, 64 columns 27.6, 16 columns 48.0; over 32 experts 58.4, 38.7 and 54.5; the k-blocks' times are from later runs).  With the direct forms, over 230 sizes
     // of few rows, 1.3% and 32% (a row count says nothing of how it falls on the experts): 4096 x 4096, 1 row: by dot
     // products 2.8 us, direct MMAs 5.2, 16 columns 10.3; 4 rows 3.8, 5.2, 11.6; 8 rows 7, 5.3, 11.7; 32 rows 19, 14.4,
     // 18.6, 64 columns 14.9; 64 rows 35, 22.5, 22.3, 15.7; 64 rows over 64 experts of 2048 x 2048 26.1, 33.3, 28.5.
@@ -165,7 +165,7 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
       const long long loads = ceil_div(tiles, warps) * (ceil_div(d.K * dot_cols, 4096) * 800 + 800);
       const long long products = row_tiles(kInt8DotRows) * kilos * (mean > 2 ? 4 : mean) * 15 / 1000;
       take(kLinearInt8Direct, kInt8DotRows, 1, warps, ceil_div(d.N, dot_cols), 1300 + (loads > products ? loads : products), 1300 + bytes / 6800);
-      plan.grid = static_cast<int>(ceil_div(plan.grid, kInt8DotWarps));
+      plan.grid = static_cast<int>(ceil_div(plan.grid, kInt8DotWarps));   // (the first to offer: it has been taken)
     }
     if (mma > 0 && mean <= 64) {
       const long long tiles = row_tiles(kInt8MmaRows) * ceil_div(d.N, kInt8MmaCols), groups = mean > 8 ? 2 : 1;
@@ -178,7 +178,7 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
         const int units = few_clusters(dev, num_sms, d.dtype, tile, split);
         const long long tiles = row_tiles(tile) * nt;
         if (units < 1 || (split > 1 && tiles > units)) continue;   // sharing a tile pays in a single wave
-        const long long per_kb = tile == 64 ? 350 : tiles * split <= num_sms ? 450 : 590;
+        const long long per_kb = tile == 64 ? 285 : tiles * split <= num_sms ? 380 : 500;
         const long long ends = split == 1 ? (tile == 64 ? 1340 : 230) : (tile == 64 ? 6800 : 3210) + 70 * split;
         offer(kLinearInt8, tile, split, units, nt, per_kb, ends);
       }

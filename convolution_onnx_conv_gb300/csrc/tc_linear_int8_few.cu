@@ -3,14 +3,16 @@
 // reduction where there are fewer tiles than SMs, as in tc_linear_few.cu; their partial sums are integers too.
 //
 // For tens of rows, and for experts with a few each (fewer: linear_int8_direct.cu).  Bound by what a k-block goes through
-// (its bytes' arrival, the conversion of 128 weight rows, the MMAs: 350 to 590 ns, of which the bytes take 100) and, where
-// the reduction is shared, by 3 to 7 us of start, exchange and end.  64 x 4096 x 4096: 15.3 us (tensor pipe 12%, logic pipe
-// 33%); 96 x 8192 x 2048 12.6; 1001 x 1000 x 2048 12.3; 128 rows over 24 experts of 2048 x 2048 24.1 (floor 14.9).
+// (its bytes' arrival, the conversion of 128 weight rows, the MMAs: 290 to 500 ns, of which the bytes take 100) and, where
+// the reduction is shared, by 3 to 7 us of start, exchange and end.  64 x 4096 x 4096: 15.0 us; 64 x 8192 x 8192 25.8 (tensor
+// pipe 12%, logic pipe 33%); 96 x 8192 x 2048 11.8; 1001 x 1000 x 2048 11.4; 128 rows over 24 experts of 2048 x 2048 26.5
+// (floor 14.9).  A group of converting warps takes every other stage whole: its barriers' answers and its stores' ways then
+// come once for two units (a unit of every stage each: 27.8, 12.6 and 12.3 us).
 //
 //   warp 0        TMA: weight and x tiles of 128 values
 //   warp 1        TMEM, MMA issue
 //   warps 2, 3    int8 -> fp16 of x (64 columns: warps 4-11)
-//   8 warps       int8 -> fp16 of the weights: two groups of four warps, each a unit of every stage
+//   8 warps       int8 -> fp16 of the weights: two groups of four warps, each every other stage
 //   the last      epilogue: 4 warps, or 8 that take half of the columns each
 #include "linear_int8_dev.cuh"
 
@@ -40,6 +42,10 @@ struct Int8Cfg {
   static constexpr int kStages = (kBudget - kFixed) / (kWBytes + kXBytes);
   static constexpr int kSmem = kFixed + kStages * (kWBytes + kXBytes);
   static_assert(kStages >= 3 && (2 * kStages + 2 * kBlocks + 6) * 8 + 8 <= kBarBytes && kSmem <= kBudget, "shared memory");
+  // A group of converting warps sees every phase of its places' barriers, one after another: loads may land out of order,
+  // and a wait by parity that skipped a phase would take the one before it for its own.  (Places of converted stages may
+  // change between the groups: MMAs end in order.)
+  static_assert(kStages % 2 == 0, "a place for int8 tiles belongs to one group");
   static_assert(kDCol + 2 * TN <= kTmemCols, "TMEM columns");
 };
 
@@ -73,10 +79,10 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 8 + Cfg::kXWarps);
+      mbar_init(&empty[s], 4 + Cfg::kXWarps / 2);
     }
     for (int b = 0; b < kBlocks; ++b) {
-      mbar_init(&cfull[b], 8 + Cfg::kXWarps);
+      mbar_init(&cfull[b], 4 + Cfg::kXWarps / 2);
       mbar_init(&cempty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -181,13 +187,13 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
   } else if (warp >= Cfg::kXFirst && warp < Cfg::kXFirst + Cfg::kXWarps) {
     // 16 bytes at a time: of a stage's TN rows of 8, thread id takes those of row (id + i kX) % TN, 16-byte place
     // (id + i kX) / TN
-    constexpr int kX = 32 * Cfg::kXWarps, kPer = TN * 8 / kX, kAtOnce = kPer < 4 ? kPer : 4;
-    const int id = threadIdx.x - 32 * Cfg::kXFirst;
-    int stage = 0, block = 0;
+    constexpr int kX = 16 * Cfg::kXWarps, kPer = TN * 8 / kX, kAtOnce = kPer < 4 ? kPer : 4;
+    const int id = (threadIdx.x - 32 * Cfg::kXFirst) % kX, g = (threadIdx.x - 32 * Cfg::kXFirst) / kX;   // group: its stages are g, g + 2, ..
+    int stage = g, block = g;
     uint32_t phase = 0, bphase = 0;
     bool here = false;
 #pragma unroll 1
-    for (int k = 0; k < blocks; ++k) {
+    for (int k = g; k < blocks; k += 2) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
       bool room = mbar_test_wait(&cempty[block], bphase ^ 1);
       const uint8_t* x = sX + stage * Cfg::kXBytes;
@@ -214,55 +220,58 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == kStages) {
-        stage = 0;
+      if ((stage += 2) >= kStages) {
+        stage -= kStages;
         phase ^= 1;
       }
       here = mbar_test_wait(&full[stage], phase);   // the next stage
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
       __syncwarp();
       if (lane == 0) mbar_arrive(&cfull[block]);
-      if (++block == kBlocks) {
-        block = 0;
+      if ((block += 2) >= kBlocks) {
+        block -= kBlocks;
         bphase ^= 1;
       }
     }
   } else if (warp >= Cfg::kWFirst && warp < Cfg::kEpiFirst) {
-    const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - Cfg::kWFirst) >> 2;   // this thread's weight row; its unit of a stage
-    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * kUnitCols;
+    const int quad = warp & 3, id = threadIdx.x & 127, g = (warp - Cfg::kWFirst) >> 2;   // this thread's weight row; its group's stages: g, g + 2, ..
+    const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const uint8_t* from[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) from[j] = sW + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
-    int stage = 0, block = 0;
+    for (int j = 0; j < 4; ++j) from[j] = sW + id * kKBlockBytes + (((id & 7) ^ j) << 4);
+    int stage = g, block = g;
     uint32_t phase = 0, bphase = 0;
     bool here = false;
 #pragma unroll 1
-    for (int k = 0; k < blocks; ++k) {
+    for (int k = g; k < blocks; k += 2) {
       if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-      uint4 v[4];
+      uint4 v[8];   // (a row's second unit: its places with bit 6 the other way)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kWBytes);
+      for (int j = 0; j < 8; ++j)
+        v[j] = *reinterpret_cast<const uint4*>(sW + ((static_cast<uint32_t>(from[j & 3] - sW) + stage * Cfg::kWBytes) ^ (j & 4 ? 64u : 0u)));
       const bool room = mbar_test_wait(&cempty[block], bphase ^ 1);   // (asked before the arithmetic: an answer takes 100 cycles)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == kStages) {
-        stage = 0;
+      if ((stage += 2) >= kStages) {
+        stage -= kStages;
         phase ^= 1;
       }
-      uint32_t f[2][16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
       if (!room && !mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
       tc_fence_after();
-      tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols, f[0]);
-      tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols + 16, f[1]);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t f[16];
+        f16_of_int8_16(v[j], f);
+        f16_of_int8_16(v[j + 1], f + 8);
+        tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols + 8 * j, f);
+      }
       here = mbar_test_wait(&full[stage], phase);   // the next stage
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&cfull[block]);
-      if (++block == kBlocks) {
-        block = 0;
+      if ((block += 2) >= kBlocks) {
+        block -= kBlocks;
         bphase ^= 1;
       }
     }

@@ -59,14 +59,6 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t p
       : "memory");
   return ok != 0;
 }
-// Arrive on the pair's leader's mbarrier: this CTA's operands of an MMA are in place.  What it tells of is read by the
-// tensor cores and TMA's side only, not by the other CTA's threads, and each writer has made its writes visible to
-// those before: shared memory by fence.proxy.async, TMEM by tcgen05.wait::st and the fence before.  So the release orders
-// those within the CTA and no more.  (At cluster scope it also waits for every store in flight to be seen by the other
-// CTA: 1380 cycles, of about 400 that a unit has.)
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 // Four int8 values as fp16: {0, 2} and {1, 3}.  0x6400 | (b ^ 0x80) is 1024 + 128 + b.  (Each mask and bias in one
 // three-input operation: from C++ the compiler made two of them, 200 instead of 140 cycles for 64 values a thread.)
 __device__ __forceinline__ uint32_t int8_magic(uint32_t w) {

@@ -15,8 +15,14 @@
 // Bound by the MMAs: 8192 x 8192 x 8192 580 us, 1.90 PFLOP/s, 98% of the library's measured bf16 burst (fp16 operands of as
 // many values, ready, would take 570); 4096 x 4096 x 4096 83 us (tensor pipe 78% of the cycles, logic pipe 54%).
 //
-//   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (of a pair: the leader's)
+// A pair's MMAs are issued by one of its CTAs, the leader, and read what both have converted.  The other CTA's converting
+// warps hand over within their own CTA, and a thread that has nothing else in flight passes it on to the leader at
+// cluster scope, where it is ordered for a thread of another CTA (the converting warps' own release at that scope waits for
+// their stores to be seen by the leader's CTA: 1380 cycles, of about 400 that a unit has).
+//
+//   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (the leader's)
 //   warp 2        works out the CTA's next tiles
+//   warps 1, 3    of the other CTA: each passes on one unit of every stage
 //   warps 4-11    int8 -> fp16 of x: two groups of four warps, each a unit of every stage
 //   warps 12-19   int8 -> fp16 of the weights, in two groups as well
 //   warps 20-27   epilogue: warp w the rows 32 (w % 4) .. and half of the columns
@@ -46,7 +52,7 @@ struct Int8ManyCfg {
   // registers: 72 per thread at launch; the epilogue's two warpgroups take what the others give up
   static constexpr int kRegs = 72, kRegsEpi = 128, kRegsX = 56, kRegsW = 48, kRegsOther = 40;
   static_assert(256 * (kRegsEpi + kRegsX + kRegsW) + 128 * kRegsOther <= kThreads * kRegs, "register split");
-  static_assert((2 * kStages + 2 * kUnits + 8) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
+  static_assert((2 * kStages + 3 * kUnits + 8) * 8 + 8 <= kBarBytes && kSmem <= 232448, "shared memory");
   static_assert(kDCol + 2 * TN <= 512, "TMEM columns");
   static_assert(kUnits % 2 == 0, "each unit of a stage has places of its own");
 };
@@ -70,7 +76,8 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * (Cfg::kOutBytes + Cfg::kTableBytes));   // int8 tiles are here
   uint64_t* empty = full + kStages;     // and have been read
   uint64_t* cfull = empty + kStages;    // a unit of x is in TMEM and one of weights in sB, of both CTAs (the leader's)
-  uint64_t* cempty = cfull + kUnits;    // and its MMAs have read them
+  uint64_t* cpeer = cfull + kUnits;     // of the other CTA (its own)
+  uint64_t* cempty = cpeer + kUnits;    // and its MMAs have read them
   uint64_t* tfull = cempty + kUnits;    // an accumulator holds a chunk's sums
   uint64_t* tempty = tfull + 2;         // and has been read, in both CTAs (the leader's)
   uint64_t* tqfull = tempty + 2;        // a batch of tiles is worked out
@@ -89,7 +96,8 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       mbar_init(&empty[s], 16);
     }
     for (int u = 0; u < kUnits; ++u) {
-      mbar_init(&cfull[u], 16);
+      mbar_init(&cfull[u], 9);   // the leader's converting warps, and the other CTA's
+      mbar_init(&cpeer[u], 8);
       mbar_init(&cempty[u], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -123,6 +131,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   // and their stages (operands that fit the device's memory give less than 2^26; 64 bits cost the converting loops
   // registers that they have not: 88.6 instead of 84.6 us for 4096^3)
   const int blocks = static_cast<int>(mine * p.num_kb);
+  uint64_t* const converted = rank == 0 ? cfull : cpeer;   // where this CTA's converting warps arrive
   // this CTA's j-th tile, read by one thread (the loads') or a warp in the order of j; false: give up
   auto next_tile = [&](long long j, LinearTile& q, bool whole_warp) {
     const int slot = static_cast<int>(j / kTileBatch) & 1, at = static_cast<int>(j % kTileBatch);
@@ -165,7 +174,24 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&tqfull[slot]);
       }
-    } else if (warp == 1 && rank == 0) {
+    } else if (rank != 0) {
+      if (lane == 0) {
+        const uint32_t cfull0 = map_to_rank(smem_u32(cfull), 0);
+        const int h = warp >> 1;   // its unit of a stage
+        int unit = h;
+        uint32_t phase = 0;
+        for (int k = 0; k < blocks; ++k) {
+          if (!mbar_wait(&cpeer[unit], phase, abort_flag, p.status)) goto teardown;
+          tc_fence_after();   // (what was stored to TMEM is ordered by this thread's barriers too)
+          tc_fence_before();
+          mbar_arrive_remote(cfull0 + 8 * unit);
+          if ((unit += 2) >= kUnits) {
+            unit = h;
+            phase ^= 1;
+          }
+        }
+      }
+    } else if (warp == 1) {
       // the whole warp walks the loop and one lane issues: the loop's state then stays in uniform
       // registers, which is where the MMA takes its descriptors from
       const bool issue = elect_one();
@@ -214,7 +240,6 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsX));
     const int quad = warp & 3, id = threadIdx.x & 127, h = (warp - 4) >> 2;   // this thread's row; its unit of a stage
     const uint32_t to0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t cfull0 = map_to_rank(smem_u32(cfull), 0);
     const uint8_t* from[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) from[j] = sX + id * kKBlockBytes + (((id & 7) ^ j ^ (4 * h)) << 4);
@@ -245,7 +270,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(cfull0 + 8 * unit);
+      if (lane == 0) mbar_arrive(&converted[unit]);
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;
@@ -256,7 +281,6 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     // 16 bytes at a time: thread id's are those of row (id + 128 i) % 96, and j = (id + 128 i) / 96 of a unit's four
     constexpr int kPer = Cfg::kWRows * 4 / 128;
     const int id = threadIdx.x & 127, h = (warp - 12) >> 2;   // its unit of a stage
-    const uint32_t cfull0 = map_to_rank(smem_u32(cfull), 0);
     const uint8_t* from[kPer];
     uint8_t* to[kPer];   // the first half of the 16; the other is at 16 bytes before or behind it
 #pragma unroll
@@ -294,7 +318,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       here = mbar_test_wait(&full[stage], phase);   // of the next stage
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(cfull0 + 8 * unit);
+      if (lane == 0) mbar_arrive(&converted[unit]);
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;

@@ -1,0 +1,25 @@
+"""What orders the hand-offs of the tensor-core kernels, as their sources have it (no GPU)."""
+import os
+import re
+
+import pytest
+
+from test_block_scaled_host import CSRC, source
+
+SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_another_ctas_barrier_is_told_at_cluster_scope(name):
+    """A release at CTA scope (the default too) orders nothing for a thread of another CTA.  Relaxed arrivals hand back
+    what has been read, and hand over no data."""
+    for arrive in re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster", source(name)):
+        assert re.match(r"mbarrier\.arrive\.(release|relaxed)\.cluster\.shared::cluster", arrive), arrive
+
+
+def test_converting_warps_arrive_within_their_cta():
+    """The pair's converting warps and the leader's MMAs: a thread between them passes on what the other CTA has
+    converted."""
+    text = source("tc_linear_int8_many.cu")
+    assert len(re.findall(r"mbar_arrive\(&converted\[unit\]\)", text)) == 2
+    assert len(re.findall(r"mbar_arrive_remote\(", text)) == 1 and "mbar_wait(&cpeer[unit], phase" in text

@@ -158,10 +158,9 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
         // both barriers are asked at once, before either is waited for
         bool ready = mbar_test_wait(&cfull[block], phase);
         if (first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
-        if (!ready) {
-          if (!mbar_wait(&cfull[block], phase, abort_flag, p.status)) goto teardown;
-          if (first && !mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status)) goto teardown;
-        }
+        if (!ready) ready = mbar_wait(&cfull[block], phase, abort_flag, p.status) &&
+                            (!first || mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status));
+        if (!whole_warp(ready)) goto teardown;
         tc_fence_after();
         const uint32_t a = tmem_base + 2 * block * kUnitCols, d = tmem_base + Cfg::kDCol + buf * TN;
         const uint64_t b = b0 + 2 * block * (Cfg::kBBytes >> 4);
@@ -194,8 +193,8 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
     bool here = false;
 #pragma unroll 1
     for (int k = g; k < blocks; k += 2) {
-      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
-      bool room = mbar_test_wait(&cempty[block], bphase ^ 1);
+      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
+      const bool room = mbar_test_wait(&cempty[block], bphase ^ 1);
       const uint8_t* x = sX + stage * Cfg::kXBytes;
       uint8_t* b = sB + 2 * block * Cfg::kBBytes;
 #pragma unroll
@@ -206,8 +205,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
           const int task = id + (i0 + i) * kX, row = task % TN, j = task / TN;
           v[i] = *reinterpret_cast<const uint4*>(x + row * kKBlockBytes + ((j ^ (row & 7)) << 4));
         }
-        if (!room && !mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
-        room = true;
+        if (i0 == 0 && !whole_warp(room || mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status))) goto teardown;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           const int task = id + (i0 + i) * kX, row = task % TN, j = task / TN;
@@ -244,7 +242,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
     bool here = false;
 #pragma unroll 1
     for (int k = g; k < blocks; k += 2) {
-      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
       uint4 v[8];   // (a row's second unit: its places with bit 6 the other way)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -256,7 +254,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
         stage -= kStages;
         phase ^= 1;
       }
-      if (!room && !mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(room || mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status))) goto teardown;
       tc_fence_after();
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
       for (int c = 0; c < kCols; ++c) acc[c] = 0;
 #pragma unroll 1
       for (int kb = ka; kb < kb_end; kb += kChunkBlocks) {
-        if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait(&tfull[buf], bphase, abort_flag, p.status))) goto teardown;
         tc_fence_after();
         int8_add_columns(acc, from0 + buf * TN);
         tc_fence_before();
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
       } else {
         // column c is finished by rank c / per: send it there, then finish this rank's own
         const int per = TN / split;
-        if (!mbar_wait_cluster(rfree, rphase ^ 1, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait_cluster(rfree, rphase ^ 1, abort_flag, p.status))) goto teardown;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const int col = c0 + c, to = col / per;
@@ -326,7 +324,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
         asm volatile("fence.acq_rel.cluster;" ::: "memory");
         __syncwarp();
         if (lane < split) mbar_arrive_remote(map_to_rank(smem_u32(rfull), lane));
-        if (!mbar_wait_cluster(rfull, rphase, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait_cluster(rfull, rphase, abort_flag, p.status))) goto teardown;
         const int own = min(per, q.rows - rank * per);
         for (int j = c0 / kCols; j < own; j += Cfg::kEpiWarps / 4) {
           int sum = 0;

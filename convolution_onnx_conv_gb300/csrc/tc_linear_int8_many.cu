@@ -133,13 +133,16 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
   const int blocks = static_cast<int>(mine * p.num_kb);
   uint64_t* const converted = rank == 0 ? cfull : cpeer;   // where this CTA's converting warps arrive
   // this CTA's j-th tile, read by one thread (the loads') or a warp in the order of j; false: give up
-  auto next_tile = [&](long long j, LinearTile& q, bool whole_warp) {
+  auto next_tile = [&](long long j, LinearTile& q, bool whole) {
     const int slot = static_cast<int>(j / kTileBatch) & 1, at = static_cast<int>(j % kTileBatch);
-    if (at == 0 && !mbar_wait(&tqfull[slot], static_cast<uint32_t>(j / (2 * kTileBatch)) & 1, abort_flag, p.status)) return false;
+    if (at == 0) {
+      const bool there = mbar_wait(&tqfull[slot], static_cast<uint32_t>(j / (2 * kTileBatch)) & 1, abort_flag, p.status);
+      if (whole ? !whole_warp(there) : !there) return false;
+    }
     q = tileq[slot * kTileBatch + at];
     if (at == kTileBatch - 1) {
-      if (whole_warp) __syncwarp();
-      if (!whole_warp || lane == 0) mbar_arrive(&tqempty[slot]);
+      if (whole) __syncwarp();
+      if (!whole || lane == 0) mbar_arrive(&tqempty[slot]);
     }
     return true;
   };
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     } else if (warp == 2) {
       for (long long j = 0; j < mine; j += kTileBatch) {
         const int slot = static_cast<int>(j / kTileBatch) & 1;
-        if (!mbar_wait(&tqempty[slot], (static_cast<uint32_t>(j / (2 * kTileBatch)) & 1) ^ 1, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait(&tqempty[slot], (static_cast<uint32_t>(j / (2 * kTileBatch)) & 1) ^ 1, abort_flag, p.status))) goto teardown;
         if (lane < kTileBatch && j + lane < mine)
           tileq[slot * kTileBatch + lane] = tile_at<kInt8PairRows, TN>(p, prefix, t0 + (j + lane) * tstep);
         __syncwarp();
@@ -208,10 +211,9 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
             // both barriers are asked at once, before either is waited for
             bool ready = mbar_test_wait_cluster(&cfull[unit], phase);
             if (h == 0 && first) ready = mbar_test_wait(&tempty[buf], tphase ^ 1) & ready;
-            if (!ready) {
-              if (!mbar_wait_cluster(&cfull[unit], phase, abort_flag, p.status)) goto teardown;
-              if (h == 0 && first && !mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status)) goto teardown;
-            }
+            if (!ready) ready = mbar_wait_cluster(&cfull[unit], phase, abort_flag, p.status) &&
+                                (h > 0 || !first || mbar_wait(&tempty[buf], tphase ^ 1, abort_flag, p.status));
+            if (!whole_warp(ready)) goto teardown;
             tc_fence_after();
             const uint32_t a = tmem_base + unit * kUnitCols;
             const uint64_t b = b0 + unit * (Cfg::kBBytes >> 4);
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     bool here = false;
 #pragma unroll 1
     for (int k = 0; k < blocks; ++k) {
-      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
       uint4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kXBytes);
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       uint32_t f[2][16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
-      if (!room && !mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status))) goto teardown;
       tc_fence_after();
       tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
       tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     bool here = false;
 #pragma unroll 2   // (593 -> 580 us for 8192^3; x's loop too, or either more often: slower, by the instruction caches)
     for (int k = 0; k < blocks; ++k) {
-      if (!here && !mbar_wait(&full[stage], phase, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
       uint4 v[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + stage * Cfg::kWBytes);
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         stage = 0;
         phase ^= 1;
       }
-      if (!room && !mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status)) goto teardown;
+      if (!whole_warp(room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status))) goto teardown;
       const int at = unit * Cfg::kBBytes;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       for (int c = 0; c < kCols; ++c) acc[c] = 0;
 #pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += kChunkBlocks) {
-        if (!mbar_wait(&tfull[buf], tphase, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait(&tfull[buf], tphase, abort_flag, p.status))) goto teardown;
         tc_fence_after();
         int8_add_columns(acc, from0 + buf * TN);
         tc_fence_before();

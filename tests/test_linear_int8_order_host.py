@@ -23,3 +23,12 @@ def test_converting_warps_arrive_within_their_cta():
     text = source("tc_linear_int8_many.cu")
     assert len(re.findall(r"mbar_arrive\(&converted\[unit\]\)", text)) == 2
     assert len(re.findall(r"mbar_arrive_remote\(", text)) == 1 and "mbar_wait(&cpeer[unit], phase" in text
+
+
+@pytest.mark.parametrize("name,single", [("tc_linear_int8_few.cu", 1), ("tc_linear_int8_many.cu", 2)])
+def test_warps_leave_their_waits_together(name, single):
+    """Lanes that a wait lets go one by one are no warp for the TMEM accesses behind it.  `single`: the roles of one thread."""
+    waits = [line for line in source(name).split("\n") if "goto teardown" in line]
+    assert sum("whole_warp(" not in w and "next_tile(" not in w for w in waits) == single, waits
+    for line in source(name).split("\n"):
+        assert not re.search(r"\bif \(!\w+ && !mbar_wait", line), line

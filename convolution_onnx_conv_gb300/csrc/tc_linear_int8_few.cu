@@ -216,16 +216,16 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
           *reinterpret_cast<uint4*>(to + (((2 * (j & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if ((stage += 2) >= kStages) {
-        stage -= kStages;
-        phase ^= 1;
-      }
-      here = mbar_test_wait(&full[stage], phase);   // the next stage
+      const int next = stage + 2 >= kStages ? stage + 2 - kStages : stage + 2;
+      phase ^= next < stage;
+      here = mbar_test_wait(&full[next], phase);
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
       __syncwarp();
-      if (lane == 0) mbar_arrive(&cfull[block]);
+      if (lane == 0) {
+        mbar_arrive(&cfull[block]);
+        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
+      }
+      stage = next;
       if ((block += 2) >= kBlocks) {
         block -= kBlocks;
         bphase ^= 1;
@@ -248,12 +248,6 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
       for (int j = 0; j < 8; ++j)
         v[j] = *reinterpret_cast<const uint4*>(sW + ((static_cast<uint32_t>(from[j & 3] - sW) + stage * Cfg::kWBytes) ^ (j & 4 ? 64u : 0u)));
       const bool room = mbar_test_wait(&cempty[block], bphase ^ 1);   // (asked before the arithmetic: an answer takes 100 cycles)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if ((stage += 2) >= kStages) {
-        stage -= kStages;
-        phase ^= 1;
-      }
       if (!whole_warp(room || mbar_wait(&cempty[block], bphase ^ 1, abort_flag, p.status))) goto teardown;
       tc_fence_after();
 #pragma unroll
@@ -263,11 +257,17 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
         f16_of_int8_16(v[j + 1], f + 8);
         tmem_st_32x32b_x16(to0 + 2 * block * kUnitCols + 8 * j, f);
       }
-      here = mbar_test_wait(&full[stage], phase);   // the next stage
+      const int next = stage + 2 >= kStages ? stage + 2 - kStages : stage + 2;
+      phase ^= next < stage;
+      here = mbar_test_wait(&full[next], phase);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&cfull[block]);
+      if (lane == 0) {
+        mbar_arrive(&cfull[block]);
+        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
+      }
+      stage = next;
       if ((block += 2) >= kBlocks) {
         block -= kBlocks;
         bphase ^= 1;

@@ -255,12 +255,6 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kXBytes);
       const bool room = mbar_test_wait(&cempty[unit], uphase ^ 1);   // (asked before the arithmetic: an answer takes 100 cycles)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
       uint32_t f[2][16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
@@ -268,11 +262,17 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       tc_fence_after();
       tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
       tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
-      here = mbar_test_wait(&full[stage], phase);   // of the next stage
+      const int next = stage + 1 == kStages ? 0 : stage + 1;
+      phase ^= next == 0;
+      here = mbar_test_wait(&full[next], phase);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&converted[unit]);
+      if (lane == 0) {
+        mbar_arrive(&converted[unit]);
+        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
+      }
+      stage = next;
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;
@@ -302,12 +302,6 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + stage * Cfg::kWBytes);
       const bool room = mbar_test_wait(&cempty[unit], uphase ^ 1);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
       if (!whole_warp(room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status))) goto teardown;
       const int at = unit * Cfg::kBBytes;
 #pragma unroll
@@ -317,10 +311,16 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         *reinterpret_cast<uint4*>(to[i] + at) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(to[i] + at + other) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      here = mbar_test_wait(&full[stage], phase);   // of the next stage
+      const int next = stage + 1 == kStages ? 0 : stage + 1;
+      phase ^= next == 0;
+      here = mbar_test_wait(&full[next], phase);
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
       __syncwarp();
-      if (lane == 0) mbar_arrive(&converted[unit]);
+      if (lane == 0) {
+        mbar_arrive(&converted[unit]);
+        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
+      }
+      stage = next;
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;

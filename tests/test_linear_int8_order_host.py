@@ -32,3 +32,11 @@ def test_warps_leave_their_waits_together(name, single):
     assert sum("whole_warp(" not in w and "next_tile(" not in w for w in waits) == single, waits
     for line in source(name).split("\n"):
         assert not re.search(r"\bif \(!\w+ && !mbar_wait", line), line
+
+
+@pytest.mark.parametrize("name,arrive", [("tc_linear_int8_few.cu", "cfull[block]"), ("tc_linear_int8_many.cu", "converted[unit]")])
+def test_a_stage_is_given_back_with_what_it_became(name, arrive):
+    """Not when its bytes have been asked for: the copy that overwrites them starts at that arrival."""
+    text = source(name)
+    given = len(re.findall(r"mbar_arrive\(&empty\[stage\]\)", text))
+    assert given == len(re.findall(re.escape(f"mbar_arrive(&{arrive});") + r"\s*mbar_arrive\(&empty\[stage\]\);", text)) == 2

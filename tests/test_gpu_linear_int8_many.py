@@ -23,6 +23,7 @@ class Noise:
         self.on, self.stream = on, torch.cuda.Stream()
         self.a = torch.zeros((1 << 28,), dtype=torch.uint8, device="cuda")
         self.b = torch.zeros_like(self.a)
+        self.stream.wait_stream(torch.cuda.current_stream())   # (their memory was other work's of that stream)
 
     def some(self):
         if self.on:

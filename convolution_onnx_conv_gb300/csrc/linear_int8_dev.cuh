@@ -59,6 +59,14 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t p
       : "memory");
   return ok != 0;
 }
+// Arrive on another CTA's mbarrier and publish, in the cluster, what this thread has written to its CTA's shared memory or
+// has seen written there (behind a wait for those who wrote it).  The fence is for shared memory alone.
+__device__ __forceinline__ void mbar_arrive_remote_shared(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
+}
 // Whether all lanes of a warp say so.  Lanes leave a wait, or find that there is no need for one, each by itself; the TMEM
 // accesses behind it are one operation of all 32 (tcgen05.ld and .st are .sync.aligned, undefined in a warp that has come
 // apart), and a lane that gave up would be waited for.  So the lanes go on together or not at all.

@@ -16,9 +16,10 @@
 // many values, ready, would take 570); 4096 x 4096 x 4096 83 us (tensor pipe 78% of the cycles, logic pipe 54%).
 //
 // A pair's MMAs are issued by one of its CTAs, the leader, and read what both have converted.  The other CTA's converting
-// warps hand over within their own CTA, and a thread that has nothing else in flight passes it on to the leader at
-// cluster scope, where it is ordered for a thread of another CTA (the converting warps' own release at that scope waits for
-// their stores to be seen by the leader's CTA: 1380 cycles, of about 400 that a unit has).
+// warps hand over within their own CTA, and a thread of it passes that on to the leader at cluster scope, where it is
+// ordered for a thread of another CTA, by a fence for what is in shared memory (8192 x 8192 x 8192 622 us; by an arrival that
+// releases all memory, which also waits for the results on their way out, 905; by such fences of the converting warps
+// themselves 634).
 //
 //   warps 0, 1    TMA: weight and x tiles of 128 values; TMEM and MMA issue (the leader's)
 //   warp 2        works out the CTA's next tiles
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
           if (!mbar_wait(&cpeer[unit], phase, abort_flag, p.status)) goto teardown;
           tc_fence_after();   // (what was stored to TMEM is ordered by this thread's barriers too)
           tc_fence_before();
-          mbar_arrive_remote(cfull0 + 8 * unit);
+          mbar_arrive_remote_shared(cfull0 + 8 * unit);
           if ((unit += 2) >= kUnits) {
             unit = h;
             phase ^= 1;

@@ -22,7 +22,9 @@ def test_converting_warps_arrive_within_their_cta():
     converted."""
     text = source("tc_linear_int8_many.cu")
     assert len(re.findall(r"mbar_arrive\(&converted\[unit\]\)", text)) == 2
-    assert len(re.findall(r"mbar_arrive_remote\(", text)) == 1 and "mbar_wait(&cpeer[unit], phase" in text
+    assert len(re.findall(r"mbar_arrive_remote_shared\(", text)) == 1 and "mbar_wait(&cpeer[unit], phase" in text
+    assert re.search(r"void mbar_arrive_remote_shared.*?fence\.release\.sync_restrict::shared::cta\.cluster;.*?mbarrier\.arrive\.relaxed",
+                     source("linear_int8_dev.cuh"), re.S)
 
 
 @pytest.mark.parametrize("name,single", [("tc_linear_int8_few.cu", 1), ("tc_linear_int8_many.cu", 2)])

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     bool here = false;
 #pragma unroll 1
     for (int k = 0; k < blocks; ++k) {
-      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
+      const bool there = here || mbar_wait(&full[stage], phase, abort_flag, p.status);   // (one vote on both waits, below)
       uint4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(from[j] + stage * Cfg::kXBytes);
@@ -259,21 +259,22 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
       uint32_t f[2][16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) f16_of_int8_16(v[j], &f[j >> 1][8 * (j & 1)]);
-      if (!whole_warp(room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status))) goto teardown;
+      if (!whole_warp(there && (room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status)))) goto teardown;
       tc_fence_after();
       tmem_st_32x32b_x16(to0 + unit * kUnitCols, f[0]);
       tmem_st_32x32b_x16(to0 + unit * kUnitCols + 16, f[1]);
-      const int next = stage + 1 == kStages ? 0 : stage + 1;
-      phase ^= next == 0;
-      here = mbar_test_wait(&full[next], phase);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
+      __syncwarp();
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      here = mbar_test_wait(&full[stage], phase);   // of the next stage
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&converted[unit]);
-        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
-      }
-      stage = next;
+      if (lane == 0) mbar_arrive(&converted[unit]);
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;
@@ -298,12 +299,14 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
     bool here = false;
 #pragma unroll 2   // (593 -> 580 us for 8192^3; x's loop too, or either more often: slower, by the instruction caches)
     for (int k = 0; k < blocks; ++k) {
-      if (!whole_warp(here || mbar_wait(&full[stage], phase, abort_flag, p.status))) goto teardown;
+      const bool there = here || mbar_wait(&full[stage], phase, abort_flag, p.status);
       uint4 v[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const uint4*>(from[i] + stage * Cfg::kWBytes);
       const bool room = mbar_test_wait(&cempty[unit], uphase ^ 1);
-      if (!whole_warp(room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status))) goto teardown;
+      // (no access of the whole warp follows: the vote is taken once the unit has been handed over; both waits' votes in
+      // front of them 8 us more)
+      const bool go = there && (room || mbar_wait(&cempty[unit], uphase ^ 1, abort_flag, p.status));
       const int at = unit * Cfg::kBBytes;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -312,16 +315,17 @@ __global__ void __launch_bounds__(Int8ManyCfg::kThreads, 1)
         *reinterpret_cast<uint4*>(to[i] + at) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(to[i] + at + other) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      const int next = stage + 1 == kStages ? 0 : stage + 1;
-      phase ^= next == 0;
-      here = mbar_test_wait(&full[next], phase);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      here = mbar_test_wait(&full[stage], phase);   // of the next stage
       fence_proxy_async_smem();   // what was stored to shared memory is the MMA's to read
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&converted[unit]);
-        mbar_arrive(&empty[stage]);   // (its bytes have been used by now, not only asked for)
-      }
-      stage = next;
+      if (lane == 0 && go) mbar_arrive(&converted[unit]);
+      if (!whole_warp(go)) goto teardown;
       if ((unit += 2) >= kUnits) {
         unit = h;
         uphase ^= 1;

@@ -94,7 +94,9 @@ __device__ __forceinline__ void f16_of_int8_16(const uint4& v, uint32_t* f) {
   f16_of_int8(v.w, f[6], f[7]);
 }
 
-// What is behind a sum: its weight row's scale and bias, the clamp.
+// What is behind a sum: its weight row's scale and bias, the clamp.  Without a bias nothing is added, and -0 is what leaves
+// every product as it is: adding 0 would turn a product of -0 (a negative sum times a scale that underflows) into 0.
+constexpr float kNoBias = -0.f;
 struct Int8Finish {
   float ws, bias, lo, hi;
   __device__ __forceinline__ float operator()(int sum, float xs) const {

@@ -62,7 +62,7 @@ __device__ __forceinline__ void dot_tile(const LinearParams& p, const Int8Operan
   if (mine) {
     const long long en = static_cast<long long>(q.e) * p.N + n;
     ws = p.w_scale[en];
-    bias = p.bias ? p.bias[en] : 0.f;
+    bias = p.bias ? p.bias[en] : kNoBias;
     xs = p.x_scale[(q.row0 + mr) * p.xs_row];
   }
   int acc[R][COLS];
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_int8_mma_kernel(const Line
     if (mine) {
       const long long en = static_cast<long long>(q.e) * p.N + n;
       ws = p.w_scale[en];
-      bias = p.bias ? p.bias[en] : 0.f;
+      bias = p.bias ? p.bias[en] : kNoBias;
       xs = p.x_scale[(q.row0 + mr) * p.xs_row];
     }
     if (q.rows <= 8)

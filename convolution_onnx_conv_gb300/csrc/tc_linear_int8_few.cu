@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Int8Cfg<TN>::kThreads, Int8Cfg<TN>::kPerSm)
       const int nrow = quad * 32 + lane;   // this thread's weight row of the CTA's tile
       const int n = q.n0 + nrow;
       const long long en = static_cast<long long>(q.e) * p.N + n;
-      const float ws = n < p.N ? p.w_scale[en] : 0.f, bias = p.bias && n < p.N ? p.bias[en] : 0.f;
+      const float ws = n < p.N ? p.w_scale[en] : 0.f, bias = p.bias && n < p.N ? p.bias[en] : kNoBias;
       float held[kHeld];
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {

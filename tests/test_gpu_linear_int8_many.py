@@ -77,3 +77,28 @@ def test_calls_of_experts_repeat(busy):
         want = torch.cat([expected(x[a:b], w[e], xs[a:b], ws[e], out=BF16) for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))])
         calls.append((lin, lambda y, lin=lin, x=rows16(x), xs=xs, off=off: lin(x, off, xs, y=y), want))
     repeat(calls, 100, Noise(busy))
+
+
+FORMS = [(17, 1024, 1000, "direct tile=4x", 1), (48, 1500, 1500, "direct tile=16x", 1), (64, 2048, 520, "few_rows tile=16x", 1),
+         (40, 2048, 3000, "few_rows tile=16x", 2), (128, 136, 8192, "few_rows tile=16x", 4), (80, 264, 3000, "few_rows tile=16x", 8),
+         (64, 6000, 1000, "few_rows tile=64x", 1), (17, 6000, 8192, "few_rows tile=64x", 2), (400, 520, 6000, "few_rows tile=64x", 4),
+         (200, 136, 16384, "few_rows tile=64x", 8), (1000, 3000, 1000, "many_rows tile=256x", 1)]
+
+
+def of_form(layer, rows, form, split):
+    text = layer.describe(rows)
+    assert f"form={form}" in text and f"split={split} " in text, text
+
+
+@pytest.mark.parametrize("rows,n,k,form,split", FORMS)
+def test_zeros_keep_their_sign(rows, n, k, form, split):
+    """Scales whose product underflows leave a zero of the sum's sign, in every form; with a bias of 0 added it is 0."""
+    x, w, xs, ws = operands(rows + n, rows, 1, n, k)
+    xs, ws = xs * 0 + 1e-30, ws * 0 + 1e-30
+    s = x.double() @ w[0].double().T
+    for bias in (None, torch.zeros(n, device="cuda")):
+        lin = cf.Int8Linear(rows16(w)[0], ws[0], bias=bias)
+        of_form(lin, rows, form, split)
+        y = lin(rows16(x), xs)
+        done(lin)
+        assert not y.any() and torch.equal(torch.signbit(y), (s < 0) if bias is None else torch.zeros_like(y, dtype=torch.bool))

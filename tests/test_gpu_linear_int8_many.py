@@ -102,3 +102,90 @@ def test_zeros_keep_their_sign(rows, n, k, form, split):
         y = lin(rows16(x), xs)
         done(lin)
         assert not y.any() and torch.equal(torch.signbit(y), (s < 0) if bias is None else torch.zeros_like(y, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("n", [4099, 4100])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_every_way_out(n, out):
+    """Results by whole tiles, by 16-byte units and by the elements: rows of y that begin and end on 16 bytes or do not, and
+    what lies beside them; with a bias and a clamp, and without."""
+    rows, k = 1500, 2100
+    x, w, xs, ws = operands(n, rows, 1, n, k)
+    bias = torch.randn((n,), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    for b, act, lo, hi in ((None, cf.CONVF_ACT_NONE, -float("inf"), float("inf")), (bias, cf.CONVF_ACT_NONE, -float("inf"), float("inf")),
+                           (bias, cf.CONVF_ACT_RELU, 0.0, float("inf")), (None, cf.CONVF_ACT_CLIP, -2.5, 3.0)):
+        lin = cf.Int8Linear(rows16(w)[0], ws[0], bias=b, act=act, clip=(-2.5, 3.0), out_bf16=out == BF16)
+        many(lin, rows)
+        want = expected(x, w[0], xs, ws[0], b, lo, hi, out)
+        for offset, ld in ((0, n), (0, 4128), (1, n + 5), (3, 4128)):
+            buf = torch.full((rows * ld + 8,), -7.0, dtype=out, device="cuda")
+            y = torch.as_strided(buf, (rows, n), (ld, 1), offset)
+            lin(rows16(x, pad=1), xs, y=y)
+            done(lin)
+            assert torch.equal(y, want), (offset, ld)
+            y.fill_(-7)
+            assert bool((buf == -7).all()), (offset, ld)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("k", [1030, 4096])
+def test_experts(k, out):
+    """Groups of a part of a tile, of several, of none; rows that no expert takes; a bias for each and a clamp."""
+    counts = [700, 0, 1500, 513, 1, 900, 1280, 260]
+    n, before, after = 2000, 3, 5
+    rows = sum(counts) + before + after
+    x, w, xs, ws = operands(k, rows, len(counts), n, k)
+    bias = torch.randn(ws.shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    off = torch.tensor([0] + counts).cumsum(0) + before
+    lin = cf.ExpertLinear(rows16(w), ws, bias=bias, act=cf.CONVF_ACT_RELU, out_bf16=out == BF16)
+    many(lin, rows)
+    y = torch.full((rows, n + 8), -7.0, dtype=out, device="cuda")
+    lin(rows16(x), off.to(torch.int32).cuda(), xs, y=y[:, :n])
+    done(lin)
+    want = torch.full_like(y, -7.0)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        want[a:b, :n] = expected(x[a:b], w[e], xs[a:b], ws[e], bias[e], lo=0.0, out=out)
+    assert torch.equal(y, want)
+
+
+def test_many_tiles_of_a_short_reduction():
+    """More tiles for a pair than the scheduler has places for, an accumulator of less than one stage."""
+    rows, n = 40000, 4096
+    for k in (100, 300):
+        x, w, xs, ws = operands(k, rows, 1, n, k)
+        lin = cf.Int8Linear(rows16(w)[0], ws[0], out_bf16=True)
+        many(lin, rows)
+        y = lin(rows16(x), xs)
+        done(lin)
+        assert torch.equal(y, expected(x, w[0], xs, ws[0], out=BF16))
+
+
+@pytest.mark.parametrize("rows,n,k,form,split", FORMS + [(16, 8192, 32768, "few_rows tile=16x", 2), (512, 4096, 131071, "many_rows tile=256x", 1)])
+def test_the_largest_sums_in_every_form(rows, n, k, form, split):
+    """Terms of one sign and the largest size, which fill an accumulator's 24 bits and, at the largest K, all of int32."""
+    x = torch.full((rows, k), -128, dtype=I8, device="cuda")
+    w = torch.full((n, k), -128, dtype=I8, device="cuda")
+    w[::3] = 127
+    x[0, -1] = 1
+    xs, ws = torch.ones(rows, device="cuda"), torch.ones(n, device="cuda")
+    lin = cf.Int8Linear(rows16(w), ws)
+    of_form(lin, rows, form, split)
+    y = lin(rows16(x), xs)
+    done(lin)
+    assert torch.equal(y, expected(x, w, xs, ws))
+
+
+def test_every_form_at_once_with_many_rows():
+    """Layers of every form, two of them for many rows, on streams of their own, side by side, many times."""
+    cases = []
+    for seed, (rows, n, k, form, split) in enumerate(FORMS + [(1100, 4000, 1100, "many_rows tile=256x", 1)]):
+        x, w, xs, ws = operands(50 + seed, rows, 1, n, k)
+        lin = cf.Int8Linear(rows16(w)[0], ws[0], out_bf16=True)
+        of_form(lin, rows, form, split)
+        cases.append((lin, rows16(x), xs, expected(x, w[0], xs, ws[0], out=BF16), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [[lin(a, s, stream=st) for _ in range(4)] for lin, a, s, _, st in cases]
+        torch.cuda.synchronize()
+        for (lin, _, _, y, _), got in zip(cases, outs):
+            assert all(torch.equal(g, y) for g in got) and lin.status() == cf.CONVF_OK

@@ -259,12 +259,12 @@ __global__ void __launch_bounds__(kMbThreads, 1)
         const int g = gc + j;
         const int b = g & 1;
         if (p.expand) {
-          if (!mbar_wait(&bexp[b], (g >> 1) & 1, abort_flag, p.status)) { okk = false; break; }
+          if (!whole_warp(mbar_wait(&bexp[b], (g >> 1) & 1, abort_flag, p.status))) { okk = false; break; }
           tc_fence_after();
         } else if (j == 0) {
-          if (!mbar_wait(&bx[ti % p.nxb], (ti / p.nxb) & 1, abort_flag, p.status)) { okk = false; break; }
+          if (!whole_warp(mbar_wait(&bx[ti % p.nxb], (ti / p.nxb) & 1, abort_flag, p.status))) { okk = false; break; }
         }
-        if (!mbar_wait(&bvec[b], (g >> 1) & 1, abort_flag, p.status)) { okk = false; break; }
+        if (!whole_warp(mbar_wait(&bvec[b], (g >> 1) & 1, abort_flag, p.status))) { okk = false; break; }
         const float* vec = sVec + b * kVecRows * 64;
         named_barrier(1, kMbWorkers);         // the previous chunk's depthwise is done with sH1
         // ---- hidden epilogue: pixel rows of the halo -> fp32 rows of sH1
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
         if (p.expand) tc_fence_before();
         named_barrier(1, kMbWorkers);         // sH1 complete
         // the previous chunk's project MMAs are done reading the A operands
-        if (g > 0 && !mbar_wait(bprj, (g - 1) & 1, abort_flag, p.status)) { okk = false; break; }
+        if (g > 0 && !whole_warp(mbar_wait(bprj, (g - 1) & 1, abort_flag, p.status))) { okk = false; break; }
         // ---- depthwise 3x3 (stride ST, pad 1) + BN + ReLU6 -> bf16 hi/lo A operands
         if (dox < p.TW) {
           f32x2 tp[9][2];
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
       if (!okk) break;
       gc += p.nch;
       // ---- project epilogue: TMEM rows = output pixels -> BN (+ skip) -> fp32 NHWC
-      if (!mbar_wait(bprj, (gc - 1) & 1, abort_flag, p.status)) break;
+      if (!whole_warp(mbar_wait(bprj, (gc - 1) & 1, abort_flag, p.status))) break;
       tc_fence_after();
       {
         const int m = q * 32 + lane;

@@ -67,10 +67,6 @@ __device__ __forceinline__ void mbar_arrive_remote_shared(uint32_t cluster_addr)
       "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
       : "memory");
 }
-// Whether all lanes of a warp say so.  Lanes leave a wait, or find that there is no need for one, each by itself; the TMEM
-// accesses behind it are one operation of all 32 (tcgen05.ld and .st are .sync.aligned, undefined in a warp that has come
-// apart), and a lane that gave up would be waited for.  So the lanes go on together or not at all.
-__device__ __forceinline__ bool whole_warp(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 // Four int8 values as fp16: {0, 2} and {1, 3}.  0x6400 | (b ^ 0x80) is 1024 + 128 + b.  (Each mask and bias in one
 // three-input operation: from C++ the compiler made two of them, 200 instead of 140 cycles for 64 values a thread.)
 __device__ __forceinline__ uint32_t int8_magic(uint32_t w) {

@@ -75,6 +75,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Whether all lanes of a warp say so.  Lanes leave a wait, or find that there is no need for one, each by itself; the TMEM
+// accesses behind it are one operation of all 32 (tcgen05.ld and .st are .sync.aligned, undefined in a warp that has come
+// apart), and a lane that gave up would be waited for.  So the lanes go on together or not at all.
+__device__ __forceinline__ bool whole_warp(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
+
 // gpu-scope acquire load / release store of a flag word
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
   int v;

@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(TcCfg<BN, GATHER, PAIR>::kThreads, 1)
         const bool has_cols = c0 < p.Kout;
         for (int c = 0; c < nch; ++c, ++chunk) {
           const int acc = chunk & 1;
-          if (!mbar_wait(&tfull[acc], (chunk >> 1) & 1, abort_flag, p.status)) goto teardown;
+          if (!whole_warp(mbar_wait(&tfull[acc], (chunk >> 1) & 1, abort_flag, p.status))) goto teardown;
           tc_fence_after();
           if (has_cols) {
             const uint32_t buf = lane_base + static_cast<uint32_t>(acc * BN + eg * HC);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(TcCfg<BN, GATHER, PAIR>::kThreads, 1)
       if (SK && seg % G != eg) continue;
       const int acc = seg & 1;                         // accumulator buffer of segment seg
       const uint32_t acc_phase = (seg >> 1) & 1;
-      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status)) break;
+      if (!whole_warp(mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status))) break;
       tc_fence_after();
       // 0 whole tile, 1 owner, 2 contributor (always 0 without stream-K)
       const int mode = !SK ? 0 : (ka > 0 ? 2 : (kend < p.num_kb ? 1 : 0));
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(TcCfg<BN, GATHER, PAIR>::kThreads, 1)
           mbar_arrive(&tempty[acc]);
       }
       // RSM: this tile's residual (buffer acc) in shared memory
-      if (RSM && !mbar_wait(&rfull[acc], acc_phase, abort_flag, p.status)) break;
+      if (RSM && !whole_warp(mbar_wait(&rfull[acc], acc_phase, abort_flag, p.status))) break;
       const uint8_t* sResT = sRes + acc * Cfg::kResTileBytes;
       for (int ch = cbeg; ch < cend; ch += kRead) {
         const bool two = kRead == 2 && ch + 1 < cend;

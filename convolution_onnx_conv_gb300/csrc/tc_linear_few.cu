@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(FewCfg<F8, TN>::kThreads, FewCfg<F8, TN>::kPer
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
       for (int kb = ka; kb < kb_end; kb += F8 ? 1 : p.chunk_kb) {
-        if (!mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
-        if (F8 && !mbar_wait(&sfull[buf], bphase, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(mbar_wait(&tfull[buf], bphase, abort_flag, p.status) &&
+                        (!F8 || mbar_wait(&sfull[buf], bphase, abort_flag, p.status)))) goto teardown;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(ManyCfg<PAIR>::kThreads, 1)
       }
 #pragma unroll 1
       for (int kb = 0; kb < p.num_kb; kb += F8 ? 1 : p.chunk_kb) {
-        if (!ready && !mbar_wait(&tfull[buf], bphase, abort_flag, p.status)) goto teardown;
+        if (!whole_warp(ready || mbar_wait(&tfull[buf], bphase, abort_flag, p.status))) goto teardown;
         tc_fence_after();
         const uint32_t from = from0 + (buf & 2) * 128;
         f32x2 r[32];

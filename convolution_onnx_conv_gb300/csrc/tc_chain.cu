@@ -490,7 +490,8 @@ __device__ void chain_epilogue(const ChainParams& p, uint8_t* sEpi, uint64_t* tf
     const int half = g.bn >> 1;   // this group's columns: 32, 64 or 128
     const int nch = half >> 5;
     const int col0 = n0 + eg * half;
-    if (!whole_warp(mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status))) return;
+    if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status)) return;
+    __syncwarp();   // together, as tcgen05.ld asks for (by whole_warp() the kernel spills: 0.442 ms for ResNet-50's layers, not 0.425)
     tc_fence_after();
     if (rows && g.res != nullptr && g.rsrc >= 0) {
       // the residual rows of this tile are the producing step's row block rb (same shape)

@@ -130,14 +130,25 @@ __device__ __forceinline__ void int8_put_columns(const LinearParams& p, const In
     }
   }
 }
+// 16 columns of the accumulator, and the wait for them in the same statement: in a statement of its own it would keep the
+// compiler from moving memory accesses above it, but not a use of the registers.
+__device__ __forceinline__ void tmem_ld_16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 // acc += the accumulator's columns from `from`
 template <int kCols>
 __device__ __forceinline__ void int8_add_columns(int (&acc)[kCols], uint32_t from) {
 #pragma unroll
   for (int c = 0; c < kCols; c += 16) {
     uint32_t r[16];
-    tmem_ld_32x32b_x16(from + c, r);
-    tmem_ld_wait();
+    tmem_ld_16_wait(from + c, r);
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
   }

@@ -50,3 +50,9 @@ def test_warps_that_read_accumulators_leave_their_wait_together(name):
     """Every kernel's epilogue: tcgen05.ld follows."""
     for wait in re.findall(r"[^\n]*mbar_wait\(&tfull[^\n]*\n[^\n]*", source(name)):
         assert "whole_warp(" in wait or wait.split("\n")[1].strip() == "__syncwarp();", wait
+
+
+@pytest.mark.parametrize("name", ["linear_int8_dev.cuh", "tc_linear_int8_few.cu", "tc_linear_int8_many.cu"])
+def test_accumulators_are_loaded_and_waited_for_in_one_statement(name):
+    """In two, nothing keeps the compiler from using the registers between them."""
+    assert not re.search(r"tmem_ld_32x32b_x\d+\(|tmem_ld_wait\(", source(name))

@@ -13,8 +13,11 @@
 // columns for; rows wider than a CTA are read twice, the second time from L2.
 //
 // 8192 x 4096 bf16 with a bf16 residual, e4m3: 41.3 us, 5.7 TB/s (84% of a copy's rate); int8 39.5; without a residual
-// 8192 x 4096 to int8 18.5 us, 5.5 TB/s.  Gated 8192 x 2 * 2048 20.4 us (floor 12.4), by its instructions.  Below 4096
-// columns, and above 8192, by the latency of a row's reduction: 4095 x 2000 with an fp32 residual 21.2 us, 4.3 TB/s.
+// 8192 x 4096 to int8 17.3 to 18.5 us, 5.5 to 5.8 TB/s.  Gated 8192 x 2 * 2048 bf16 19.6 us (floor 12.4; issue slots 53%, ALU
+// 40%), fp32 24.2 for 2 * 2048 of 8192 rows (22.3).  Below 4096 columns, above 8192 and for gated bf16 rows what bounds it
+// is waiting: a CTA has a row in flight and one asked for, and a row ends at a barrier.  4095 x 2000 with an fp32 residual
+// 19.8 to 21.2 us, 4.3 TB/s.  Rows gathered by an index take the form with bounds tests: a permutation of 8192 x 4096 bf16 20.8 us
+// (17.3 in order), 16380 rows of 4095 x 2000 20.1 (floor 7.3, each row four times).
 //
 // Rows that do not begin on 16 bytes (any odd number of bf16 columns) are read and written by 16 bytes all the
 // same: aligned units that hold a thread's columns, shifted into place in registers by what is the same for the
@@ -354,7 +357,11 @@ template <typename T, typename R, int ALIGN>
 constexpr int kBytesPerColumn = sizeof(T) * (kGated ? 2 : 1) + (kHasResidual<R> ? sizeof(typename std::conditional<kHasResidual<R>, R, T>::type) : 0) + (ALIGN ? 0 : 2);
 template <typename T, typename R, int ALIGN>
 constexpr int kThreadsPerSm = kBytesPerColumn<T, R, ALIGN> <= 4 ? 1024 : kBytesPerColumn<T, R, ALIGN> <= 8 ? 768 : 512;
-constexpr int kWideThreads = 512;   // two such CTAs on an SM
+// Two CTAs of the two-pass form on an SM: 64 registers a thread, too few for a row's bytes and a second operand's (a
+// residual's, a gate's other half), with which it spills 16 to 1116 bytes.  3000 x 9001 fp32 with an fp32 residual 427 us
+// (floor 52), 3000 x 20000 508 (115), bf16 with bf16 182 (62); gated fp32 4096 x 2 * 12001 386 (65).  Without a second
+// operand it spills up to 164 bytes: 4096 x 20000 bf16 74 us (36), fp32 90 (61).
+constexpr int kWideThreads = 512;
 
 // How a row is shared out: to a warp (up to 512 columns), to a CTA of as many warps as 512 columns each take, or to a
 // CTA that passes over it twice.
@@ -514,6 +521,7 @@ __global__ void __launch_bounds__(SHARE == kWarpRow ? 128 : SHARE == kWideRow ? 
       }
     }
   };
+  // (rsqrtf is within 2 units in the last place; only scales have it in them)
   auto factor = [&](float sum) { return kNorm ? rsqrtf(fmaf(sum, p.inv_cols, p.eps)) : 1.f; };
   // columns from c of row `row`: int8 by the row's scale, e4m3 by each block's (8 lanes)
   auto put = [&](long long row, const float (&t)[16], int c, BlockScale bs, float f) {

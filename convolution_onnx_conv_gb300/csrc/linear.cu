@@ -156,7 +156,10 @@ LinearPlan make_plan(const convf_linear_desc& d, int dev, int num_sms, int rows)
     // 24.3, 64 columns 27.6, 16 columns 48.0; over 32 experts 58.4, 38.7 and 54.5; the k-blocks' times are from later runs).  With the direct forms, over 230 sizes
     // of few rows, 1.3% and 32% (a row count says nothing of how it falls on the experts): 4096 x 4096, 1 row: by dot
     // products 2.8 us, direct MMAs 5.2, 16 columns 10.3; 4 rows 3.8, 5.2, 11.6; 8 rows 7, 5.3, 11.7; 32 rows 19, 14.4,
-    // 18.6, 64 columns 14.9; 64 rows 35, 22.5, 22.3, 15.7; 64 rows over 64 experts of 2048 x 2048 26.1, 33.3, 28.5.
+    // 18.6, 64 columns 14.9; 64 rows 35, 22.5, 22.3, 15.7; 64 rows over 64 experts of 2048 x 2048 26.1, 33.3, 28.5.  Those
+    // 32% are the worst of the groups that were run, not of all: where one expert takes every row, the choice by the mean loses
+    // more.  64 rows of one of 64 experts of 4096 x 4096 40.0 us (dot products; one layer of 64 rows 15.0), 256 rows 38.8
+    // (17.4), 1024 rows 56.7 (38.4); of 2048 x 2048 13.1 (8.0), 13.4 (10.9), 19.2 (16.2).
     const long long dot_cols = int8_dot_cols(d.K), dot = direct_ctas(dev, num_sms, kInt8DotRows), mma = direct_ctas(dev, num_sms, kInt8MmaRows);
     const long long mean = ceil_div(rows, taken);   // rows of an expert
     const long long kilos = d.N * static_cast<long long>(d.K) / 1000;

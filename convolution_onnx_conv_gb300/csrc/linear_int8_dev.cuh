@@ -8,7 +8,8 @@
 // integer, whatever the order, and all forms give the same bits.
 //
 // The bytes stay int8 up to shared memory (TMA); converting warps make fp16 of them there: a byte in the low bits
-// of an fp16 number 1024 + .. and a subtraction, 3 integer instructions (half rate: what bounds the conversion) and
+// of an fp16 number 1024 + .. and a subtraction (Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run: Bringing
+// Large Scale MoE Models into Cloud Scale Production", 2022), 3 integer instructions (half rate: what bounds the conversion) and
 // 2 packed additions for 4 values.  Converted weights, the MMA's 128 rows, go to TMEM, from where the MMA can read
 // its first operand, and not back to shared memory (reading 1 byte, writing 2 and the MMA reading those would be 5
 // bytes of its bandwidth a value); rows of x are the MMA's columns and go back to shared memory.  Values keep no

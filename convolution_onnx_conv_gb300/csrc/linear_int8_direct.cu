@@ -12,7 +12,9 @@
 // way.  Warps share nothing but the schedule, wait for nothing but loads, and have tiles one behind another: one search
 // of the schedule, and the next tile's rows are known and come to L2 meanwhile.  Bound by memory: 16384 x 16384, 1 row
 // 40.3 us (6.7 TB/s, 98% of a copy's rate), 24 experts of 2048 x 2048, a row each, 14.2 (through the tensor cores 24.1);
-// 4096 x 4096, 1 row 2.8 us, 4 rows 3.8.  (The same with 5 CTAs of 102 registers on an SM, not 4 of 128: 3.0 and 4.7.)
+// 4096 x 4096, 1 row 2.8 us, 4 rows 3.8.  (The same with 5 CTAs of 102 registers on an SM, not 4 of 128: 3.0 and 4.7.)  With 4
+// and 8 weight rows a warp a tile of 4 rows spills (84 and 248 bytes): 20000 x 1024, 1 row 4.5 us, 4 rows 6.2; 20000 x 512
+// 3.9 and 4.9.
 //
 // Up to 16 rows: mma.sync m16n8k32, 25 cycles of an SM for 512 bytes of weights and 8 rows (20 bytes per cycle, which is
 // what bounds it; with both operands as fp16 the MMAs take 16 cycles, but the conversion 12 more).  A CTA takes 16 weight

@@ -2,10 +2,11 @@
 // linear_int8_dev.cuh).  16 or 64 rows of x are a tile's columns, and the CTAs of a cluster share a tile's
 // reduction where there are fewer tiles than SMs, as in tc_linear_few.cu; their partial sums are integers too.
 //
-// For tens of rows, and for experts with a few each (fewer: linear_int8_direct.cu).  Bound by what a k-block goes through
-// (its bytes' arrival, the conversion of 128 weight rows, the MMAs: 290 to 500 ns, of which the bytes take 100) and, where
-// the reduction is shared, by 3 to 7 us of start, exchange and end.  64 x 4096 x 4096: 15.0 us; 64 x 8192 x 8192 25.8 (tensor
-// pipe 12%, logic pipe 33%); 96 x 8192 x 2048 11.8; 1001 x 1000 x 2048 11.4; 128 rows over 24 experts of 2048 x 2048 26.5
+// For tens of rows, and for experts with a few each (fewer: linear_int8_direct.cu).  A launch takes 3.5 us, a k-block 285 to
+// 500 ns (its bytes' arrival, the conversion of 128 weight rows, the MMAs; of these the bytes take 100), a tile's start and
+// end 0.2 to 1.3 us and, where the reduction is shared, with the exchange 3 to 7: these are what bounds small layers, not
+// the k-blocks (64 x 4096 x 4096, shared by 4, has 8 of them a CTA, 2.3 us of 15.2).  64 x 8192 x 8192 26.4 us (tensor
+// pipe 12%, logic pipe 33%); 96 x 8192 x 2048 12.0; 1001 x 1000 x 2048 11.7; 128 rows over 24 experts of 2048 x 2048 25
 // (floor 14.9).  A group of converting warps takes every other stage whole: its barriers' answers and its stores' ways then
 // come once for two units (a unit of every stage each: 27.8, 12.6 and 12.3 us).
 //

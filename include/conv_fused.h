@@ -453,7 +453,11 @@ void conv_fused_chain_destroy(convf_chain* c);
  * read in place (no prepack), and the row count is an argument of the run. */
 
 /* Operand type of a linear layer. */
-typedef enum { CONVF_LINEAR_BF16 = 0, CONVF_LINEAR_E4M3 = 1, CONVF_LINEAR_INT8 = 3 /* 2 is no type */ } convf_linear_dtype;
+typedef enum {
+  CONVF_LINEAR_BF16 = 0,
+  CONVF_LINEAR_E4M3 = 1,
+  CONVF_LINEAR_INT8 = 3    /* 2 was refused while there were two types, and stays refused */
+} convf_linear_dtype;
 
 /* What conv_fused_quantize_blocks reads and writes.  With v the values to quantise, [rows][cols]
  * in float32:
@@ -498,7 +502,8 @@ convf_status conv_fused_quantize_blocks(const convf_quant_args* a, void* stream)
 
 /* What conv_fused_quantize_rows reads and writes.  With v the values to quantise, [rows][cols] in
  * float32: x, rows of x by an index, or gated rows, as convf_quant_args has them (gated values here
- * with every operation rounded to nearest: g / (1 + exp(-g)) * u);
+ * g / (1 + exp(-g)) * u with the sum, the quotient and the product each rounded to nearest and exp within two
+ * units in the last place);
  *   scale[r] = max |v[r]| / 127                        (float32, round to nearest)
  *   q[r][c] = rint(v[r][c] / scale[r])                 (float32 quotient, then nearest, ties to even)
  * and q = 0 where the scale is 0 (a row of zeros, or of values so small that it underflows).  q is in
@@ -526,7 +531,8 @@ convf_status conv_fused_quantize_rows(const convf_quant_rows_args* a, void* stre
 /* What conv_fused_rms_norm_quantize reads and writes, in float32:
  *   h[r][c] = x[r][c] + residual[r][c]                 (x without a residual)
  *   t[r][c] = h[r][c] * weight[c]                      (h without a weight)
- *   f[r]    = 1 / sqrt(mean over c of h[r][c]^2 + eps)
+ *   f[r]    = 1 / sqrt(mean over c of h[r][c]^2 + eps)  (the reciprocal root within two units in the last
+ *             place; the order of the sum, and so its last bits, goes by the row's width, type and alignment)
  * and q, scale stand for t * f: CONVF_LINEAR_INT8 quantises rows t as conv_fused_quantize_rows does,
  * CONVF_LINEAR_E4M3 blocks of 128 columns of t as conv_fused_quantize_blocks does (block_rows = 1),
  * and each scale is multiplied by f[r], once.  (f is positive: the 8-bit values of t and of t * f are the
@@ -563,7 +569,8 @@ convf_status conv_fused_rms_norm_quantize(const convf_norm_args* a, void* stream
  * digits), is added to a float32 sum over the blocks.  bf16: the tensor core sums 256 products (float32
  * results) or 4096 (bf16 results), truncating where it adds, and those sums are added in float32 to
  * nearest.  int8: the sum is the exact integer; y = act(float(sum) * (x_scale * w_scale) + bias), in float32,
- * each operation rounded to nearest.  y is rounded once. */
+ * each operation rounded to nearest (without a bias nothing is added: a product of -0 stays one).  y is rounded
+ * once. */
 typedef struct {
   int N, K;                /* W[e]: [N][K]; int8: K at most 131071 (sums stay within 32 bits)  */
   int experts;             /* >= 1, at most 1024                                               */

@@ -82,3 +82,15 @@ def test_norm_in_place(cols, res, int8):
         check_norm(x, w, 1e-6, r, int8, cf.rms_norm_quantize(x, w, residual=a, int8=int8, h=a))
         b = torch.as_strided(x.as_strided((rows * ld,), (1,)).clone(), (rows, cols), (ld, 1))
         check_norm(x, w, 1e-6, r, int8, cf.rms_norm_quantize(b, w, residual=r, int8=int8, h=b))
+
+
+def test_gates_next_to_zero():
+    """Gates whose remainders are subnormal: where 1 + exp(-g) is 2 in float32 the gate is g / 2 rounded to nearest, down
+    to the smallest numbers.  One column a row, so that the scale is the value over 127."""
+    e = torch.randint(-149, -25, (20000,), generator=gen(30), device="cuda")
+    g = torch.ldexp(1 + torch.rand((20000,), generator=gen(31), device="cuda", dtype=torch.float64), e).float()
+    g = g * torch.where(torch.rand((20000,), generator=gen(32), device="cuda") < 0.5, -1.0, 1.0)
+    x = torch.stack([g, torch.ones_like(g)], 1)
+    _, s = cf.quantize_rows(x, gated=True)
+    v = (g.double() / 2).float().double().abs()
+    assert torch.equal(s.double(), (v / 127).float().double())

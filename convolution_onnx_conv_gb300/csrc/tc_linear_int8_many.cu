@@ -12,9 +12,9 @@
 // x is converted ahead, in registers, and waits for a place for its stores only, and weights have warps of their own.
 // A unit's weights go to shared memory with as many places, and one barrier each way serves both operands.
 //
-// Bound by the MMAs: 8192 x 8192 x 8192 606 us, 1.81 PFLOP/s, 94% of the library's measured bf16 burst (fp16 operands of as
-// many values, ready, would take 570; small values, which take less power, 584 us); 4096 x 4096 x 4096 86 us (tensor pipe
-// 78% of the cycles and logic pipe 54%, before the units' hand-over between the CTAs was ordered: 83 us).
+// Bound by the MMAs: 8192 x 8192 x 8192 606 to 613 us, 1.81 PFLOP/s, 94% of the library's measured bf16 burst (fp16 operands of
+// as many values, ready, would take 570; small values, which take less power, 584 us); 4096 x 4096 x 4096 86 us (tensor pipe
+// 74% of the cycles, ALU pipe 53%).
 //
 // A pair's MMAs are issued by one of its CTAs, the leader, and read what both have converted.  The other CTA's converting
 // warps hand over within their own CTA, and a thread of it passes that on to the leader at cluster scope, where it is

@@ -44,9 +44,11 @@ struct Int8Cfg {
   static constexpr int kSmem = kFixed + kStages * (kWBytes + kXBytes);
   static_assert(kStages >= 3 && (2 * kStages + 2 * kBlocks + 6) * 8 + 8 <= kBarBytes && kSmem <= kBudget, "shared memory");
   // A group of converting warps sees every phase of its places' barriers, one after another: loads may land out of order,
-  // and a wait by parity that skipped a phase would take the one before it for its own.  (Places of converted stages may
-  // change between the groups: MMAs end in order.)
+  // and a wait by parity that skipped a phase would take the one before it for its own.  Places of converted stages may
+  // change between the groups, since MMAs end in order: a group at stage k has seen the end of stage k - 2 - kBlocks (its last
+  // one's place), and so of k - 2 kBlocks, the phase that its wait for the end of k - kBlocks could be taken in by.
   static_assert(kStages % 2 == 0, "a place for int8 tiles belongs to one group");
+  static_assert(kBlocks >= 2, "the phase before the one waited for has ended");
   static_assert(kDCol + 2 * TN <= kTmemCols, "TMEM columns");
 };
 
